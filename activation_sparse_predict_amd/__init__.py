@@ -10,6 +10,10 @@ Entry points (same names and meaning as the C functions):
   predict(layer, x, idx, count, scores=None, mask=None, ws=None)
   sparse_ffn(layer, x, idx, count, y, mask=None, ws=None)
   ffn_stack(layers, x, out, counts=None, trace=None, ws=None, nz_counts=None)
+  Cache(k_pool, v_pool, meta, slots, max_pages) with .extend, .append, .fork, .release, .compact
+  attn_prompt(q, k, v, out, cu)
+  attn_decode(cache, layer, q, out, prefix=None, seqs=None)
+  Q4Matrix(nibbles, scales, bias, batch) and matvec(mat, x, y)
 """
 from __future__ import annotations
 
@@ -21,7 +25,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpi.so")
 
 PI_OK, PI_EINVAL, PI_EUNSUPPORTED, PI_EWORKSPACE, PI_EHIP = 0, 1, 2, 3, 4
-PI_F32, PI_F16, PI_Q4_0 = 0, 1, 2
+PI_F32, PI_F16, PI_Q4_0, PI_BF16 = 0, 1, 2, 3
 PI_RELU, PI_REGLU, PI_RELU2 = 0, 1, 2
 
 _DTYPE = {"f32": PI_F32, "f16": PI_F16, "q4_0": PI_Q4_0}
@@ -51,6 +55,21 @@ class PiTrace(ctypes.Structure):
     _fields_ = [("x_in", ctypes.c_void_p), ("scores", ctypes.c_void_p), ("mask", ctypes.c_void_p),
                 ("idx", ctypes.c_void_p), ("count", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("events", ctypes.POINTER(ctypes.c_void_p)), ("n_events", ctypes.c_int32)]
+
+
+class PiHeads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class PiCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("meta", ctypes.c_void_p),
+                ("layers", ctypes.c_int32), ("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("slots", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+# bits of a cache's error word
+PI_CACHE_ESLOT, PI_CACHE_EPAGE, PI_CACHE_EFULL, PI_CACHE_ELENGTH = 1, 2, 4, 8
 
 
 # kernels of one layer, in the order the trace events bracket them
@@ -86,6 +105,22 @@ def lib():
         L.pi_ffn_stack_static.argtypes = [P, I32, P, I32, P, P, P, P, P]
         L.pi_ffn_stack_static.restype = ctypes.c_int
         L.pi_last_hip_error.restype = ctypes.c_char_p
+        F, I64 = ctypes.c_float, ctypes.c_int64
+        for name, res, args in (
+                ("pi_cache_meta_words", SZ, [I32, I32, I32]),
+                ("pi_cache_workspace_bytes", SZ, [P]),
+                ("pi_cache_extend", ctypes.c_int, [P, P, P, I32, P]),
+                ("pi_cache_append", ctypes.c_int, [P, I32, P, P, I32, P, P, I32, P]),
+                ("pi_cache_fork", ctypes.c_int, [P, P, P, I32, P, SZ, P]),
+                ("pi_cache_release", ctypes.c_int, [P, P, I32, P]),
+                ("pi_cache_compact", ctypes.c_int, [P, P, P, SZ, P]),
+                ("pi_attn_prompt", ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, I32, P, I32, F, P]),
+                ("pi_attn_workspace_bytes", SZ, [P, I32, I32]),
+                ("pi_attn_decode", ctypes.c_int, [P, I32, P, P, I32, I32, P, P, F, P, SZ, P]),
+                ("pi_matvec_workspace_bytes", SZ, [I32, I32, I32]),
+                ("pi_matvec", ctypes.c_int, [P, I32, I32, P, P, I32, I64, P, I32, I64, I32, P, SZ, P])):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = res, args
         got = int(L.pi_abi_version())
         if got != ABI_VERSION:
             raise RuntimeError(f"{LIB_PATH} has ABI version {got}, this binding expects {ABI_VERSION} "
@@ -274,6 +309,203 @@ def ffn_stack_static(layers, x, out, counts=None, trace=None, batch: int = 1, st
     _check(st, "pi_ffn_stack_static")
 
 
+# ------------------------------------------ the attention half of a decoder layer
+def _dtype_of(t) -> int:
+    """pi_dtype of a float tensor (other types: PI_EINVAL)."""
+    import torch
+    kind = {torch.float32: PI_F32, torch.float16: PI_F16, torch.bfloat16: PI_BF16}.get(t.dtype)
+    if kind is None:
+        raise PiError(PI_EINVAL, f"tensor of {t.dtype}")
+    return kind
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise PiError(PI_EINVAL, what)
+
+
+def _ints(t, n: Optional[int], what: str) -> Optional[int]:
+    """Address of a contiguous int32 tensor of n elements (any number where n is None), or None for None."""
+    import torch
+    if t is None:
+        return None
+    _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and (n is None or t.numel() == n), what)
+    return t.data_ptr()
+
+
+def _heads(t, what: str) -> PiHeads:
+    """A [tokens][heads][dim] tensor with strides; the last dimension contiguous."""
+    _need(t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] == 1), what)
+    # the stride of a dimension of one element says nothing
+    token = t.stride(0) if t.shape[0] > 1 else 0
+    head = t.stride(1) if t.shape[1] > 1 else 0
+    return PiHeads(t.data_ptr() or None, token, head)
+
+
+class Cache:
+    """A paged key/value cache (pi_cache in include/pi.h) over tensors of the caller's.
+
+    k_pool, v_pool: [layers][pages][kv_heads][page][dim], float16 or bfloat16.  meta: the page
+    tables, one int32 tensor; .table, .lens, .ref, .free and .words are views of its parts.
+    Workspaces are allocated on first use and kept, so a call that is captured into a graph
+    has to have run once before with the same sizes; calls on one cache belong on one stream."""
+
+    def __init__(self, k_pool, v_pool, meta, slots: int, max_pages: int):
+        import torch
+        _need(k_pool.dim() == 5 and k_pool.shape == v_pool.shape and k_pool.dtype == v_pool.dtype
+              and k_pool.is_contiguous() and v_pool.is_contiguous(), "Cache: pools")
+        layers, pages, kv_heads, page, dim = k_pool.shape
+        self.k_pool, self.v_pool, self.meta = k_pool, v_pool, meta
+        self.layers, self.pages, self.kv_heads, self.page, self.dim = layers, pages, kv_heads, page, dim
+        self.slots, self.max_pages = int(slots), int(max_pages)
+        words = self.meta_words(slots, max_pages, pages)
+        _need(words > 0 and meta.dtype == torch.int32 and meta.dim() == 1 and meta.is_contiguous()
+              and meta.numel() == words, "Cache: meta")
+        self.struct = PiCache(_p(k_pool), _p(v_pool), _p(meta), layers, pages, kv_heads, page, dim,
+                              _dtype_of(k_pool), self.slots, self.max_pages)
+        self._ref = ctypes.byref(self.struct)
+        a = self.slots * self.max_pages
+        b = a + self.slots
+        self.table, self.lens = meta[:a].view(self.slots, self.max_pages), meta[a:b]
+        self.ref, self.free = meta[b:b + pages], meta[b + pages:b + 2 * pages]
+        self.words = meta[b + 2 * pages:]
+        n = int(lib().pi_cache_workspace_bytes(self._ref))
+        if n == 0:                                   # say which rule it is
+            _check(lib().pi_cache_release(self._ref, None, 1, None), "Cache")
+        self.ws = torch.empty(n, dtype=torch.uint8, device=k_pool.device)
+        self._attn_ws = {}
+
+    @staticmethod
+    def meta_words(slots: int, max_pages: int, pages: int) -> int:
+        return int(lib().pi_cache_meta_words(slots, max_pages, pages))
+
+    @classmethod
+    def create(cls, layers: int, pages: int, kv_heads: int, page: int, dim: int, slots: int, max_pages: int,
+               dtype=None, device="cuda") -> "Cache":
+        """An empty cache in tensors of its own (float16 unless dtype says otherwise)."""
+        import torch
+        shape = (layers, pages, kv_heads, page, dim)
+        k = torch.zeros(shape, dtype=dtype or torch.float16, device=device)
+        meta = torch.zeros(cls.meta_words(slots, max_pages, pages), dtype=torch.int32, device=device)
+        cache = cls(k, torch.zeros_like(k), meta, slots, max_pages)
+        cache.free.copy_(torch.arange(pages - 1, -1, -1, dtype=torch.int32))
+        cache.words[0] = pages
+        return cache
+
+    def extend(self, seqs, counts, stream=None):
+        """Room for counts[i] more tokens in slot seqs[i]."""
+        n = seqs.numel()
+        _check(lib().pi_cache_extend(self._ref, _ints(seqs, n, "extend: seqs"), _ints(counts, n, "extend: counts"), n,
+                                     _stream(stream)), "pi_cache_extend")
+
+    def append(self, layer: int, k, v, cu, seqs, stream=None):
+        """Rows cu[i] .. cu[i + 1] - 1 of k and v [tokens][kv_heads][dim] become the last tokens of slot seqs[i]."""
+        want = (self.kv_heads, self.dim)
+        _need(k.shape == v.shape and tuple(k.shape[1:]) == want and k.dtype == v.dtype == self.k_pool.dtype,
+              "append: k, v")
+        n = seqs.numel()
+        kh, vh = _heads(k, "append: k"), _heads(v, "append: v")
+        _check(lib().pi_cache_append(self._ref, layer, ctypes.byref(kh), ctypes.byref(vh), k.shape[0],
+                                     _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
+                                     _stream(stream)), "pi_cache_append")
+
+    def fork(self, parents, children, stream=None):
+        """The empty slot children[i] becomes a copy of slot parents[i]."""
+        n = parents.numel()
+        _check(lib().pi_cache_fork(self._ref, _ints(parents, n, "fork: parents"), _ints(children, n, "fork: children"),
+                                   n, _p(self.ws), self.ws.numel(), _stream(stream)), "pi_cache_fork")
+
+    def release(self, seqs, stream=None):
+        """The listed slots become empty."""
+        n = seqs.numel()
+        _check(lib().pi_cache_release(self._ref, _ints(seqs, n, "release: seqs"), n, _stream(stream)),
+               "pi_cache_release")
+
+    def compact(self, moved=None, stream=None):
+        """The pages in use move to the front of the pool; moved [pages]: the new place of each."""
+        _check(lib().pi_cache_compact(self._ref, _ints(moved, self.pages, "compact: moved"), _p(self.ws),
+                                      self.ws.numel(), _stream(stream)), "pi_cache_compact")
+
+    def errors(self) -> int:
+        """The error word (waits for the device)."""
+        return int(self.words[1])
+
+    def attn_workspace(self, batch: int, heads: int):
+        import torch
+        if (batch, heads) not in self._attn_ws:
+            n = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
+            _need(n > 0, "attn_decode: batch, heads")
+            self._attn_ws[batch, heads] = torch.empty(n, dtype=torch.uint8, device=self.k_pool.device)
+        return self._attn_ws[batch, heads]
+
+
+def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
+    """Causal attention over packed sequences, rows cu[i] .. cu[i + 1] - 1 each.
+
+    q, out: [tokens][heads][dim]; k, v: [tokens][kv_heads][dim]; scale 0: 1 / sqrt(dim)."""
+    _need(q.shape == out.shape and k.shape == v.shape and q.dim() == k.dim() == 3 and q.shape[0] == k.shape[0]
+          and q.shape[2] == k.shape[2] and q.dtype == k.dtype == v.dtype == out.dtype, "attn_prompt: q, k, v, out")
+    h = [_heads(t, "attn_prompt: strides") for t in (q, k, v, out)]
+    _check(lib().pi_attn_prompt(*(ctypes.byref(x) for x in h), q.shape[0], q.shape[1], k.shape[1], q.shape[2],
+                                _dtype_of(q), _ints(cu, None, "attn_prompt: cu"), cu.numel() - 1, scale,
+                                _stream(stream)), "pi_attn_prompt")
+
+
+def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale: float = 0.0, ws=None, stream=None):
+    """Attention of one query row [heads][dim] per batch row over what its slot holds in a layer.
+
+    seqs: the slots (None: row b is slot b).  prefix: an int32 tensor of one element, how many
+    leading pages the slots that are not empty have in common.  ws: as Cache.attn_workspace."""
+    _need(q.shape == out.shape and q.dim() == 3 and q.shape[2] == cache.dim
+          and q.dtype == out.dtype == cache.k_pool.dtype, "attn_decode: q, out")
+    batch, heads = q.shape[:2]
+    ws = cache.attn_workspace(batch, heads) if ws is None else ws
+    hq, ho = _heads(q, "attn_decode: q"), _heads(out, "attn_decode: out")
+    _check(lib().pi_attn_decode(cache._ref, layer, ctypes.byref(hq), ctypes.byref(ho), batch, heads,
+                                _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,
+                                _p(ws), ws.numel(), _stream(stream)), "pi_attn_decode")
+
+
+class Q4Matrix:
+    """A Q4_0 matrix [rows][cols] with the workspace of its products of up to `batch` rows.
+
+    nibbles: uint8 [rows][cols / 2]; scales: float16 (or its bits) [rows][cols / 32]; bias: float32
+    [rows] or None.  Products with one matrix belong on one stream."""
+
+    def __init__(self, nibbles, scales, bias=None, batch: int = 1):
+        import torch
+        _need(nibbles.dtype == torch.uint8 and nibbles.dim() == 2 and nibbles.is_contiguous(), "Q4Matrix: nibbles")
+        self.rows, self.cols, self.batch = nibbles.shape[0], 2 * nibbles.shape[1], int(batch)
+        _need(scales.dtype in (torch.float16, torch.int16) and scales.is_contiguous()
+              and tuple(scales.shape) == (self.rows, self.cols // 32), "Q4Matrix: scales")
+        _need(bias is None or (bias.dtype == torch.float32 and bias.is_contiguous()
+                               and tuple(bias.shape) == (self.rows,)), "Q4Matrix: bias")
+        self.nibbles, self.scales, self.bias = nibbles, scales, bias
+        self.struct = PiMat(_p(nibbles), _p(scales))
+        n = int(lib().pi_matvec_workspace_bytes(self.rows, self.cols, self.batch))
+        _need(n > 0, "Q4Matrix: rows, cols, batch")
+        self.ws = torch.empty(n, dtype=torch.uint8, device=nibbles.device)
+
+    @classmethod
+    def upload(cls, mat, bias=None, batch: int = 1, device="cuda") -> "Q4Matrix":
+        """Copy a host Q4_0 matrix (.nibbles, .scales as NumPy arrays) to the GPU."""
+        import numpy as np
+        import torch
+        nib = torch.from_numpy(np.ascontiguousarray(mat.nibbles)).to(device)
+        sc = torch.from_numpy(np.ascontiguousarray(mat.scales).view(np.int16)).to(device)
+        return cls(nib, sc, None if bias is None else torch.from_numpy(np.ascontiguousarray(bias)).to(device), batch)
+
+
+def matvec(mat: Q4Matrix, x, y, stream=None):
+    """y[b] = W x[b] + bias; x [batch][cols], y [batch][rows], float32, float16 or bfloat16 each."""
+    _need(x.dim() == y.dim() == 2 and x.shape[0] == y.shape[0] <= mat.batch and x.shape[1] == mat.cols
+          and y.shape[1] == mat.rows and x.stride(1) == 1 and (y.stride(1) == 1 or mat.rows == 1), "matvec: x, y")
+    batch = x.shape[0]
+    ldx, ldy = (x.stride(0), y.stride(0)) if batch > 1 else (mat.cols, mat.rows)
+    _check(lib().pi_matvec(ctypes.byref(mat.struct), mat.rows, mat.cols, _p(mat.bias), _p(x), _dtype_of(x), ldx, _p(y),
+                           _dtype_of(y), ldy, batch, _p(mat.ws), mat.ws.numel(), _stream(stream)), "pi_matvec")
+
+
 # ------------------------------------------------------- HIP runtime plumbing
 _hip = None
 
@@ -377,4 +609,6 @@ class HipGraph:
 
 
 EXPORTED = ("pi_workspace_bytes", "pi_predict", "pi_sparse_ffn", "pi_ffn_stack", "pi_ffn_stack_static",
-            "pi_status_str", "pi_abi_version", "pi_last_hip_error")
+            "pi_cache_meta_words", "pi_cache_workspace_bytes", "pi_cache_extend", "pi_cache_append", "pi_cache_fork",
+            "pi_cache_release", "pi_cache_compact", "pi_attn_prompt", "pi_attn_workspace_bytes", "pi_attn_decode",
+            "pi_matvec_workspace_bytes", "pi_matvec", "pi_status_str", "pi_abi_version", "pi_last_hip_error")

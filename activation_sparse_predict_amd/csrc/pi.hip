@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "pi_batch.hpp"
+#include "pi_host.hpp"
 #include "pi_kernels.hpp"
 
 namespace {
@@ -654,6 +655,8 @@ pi_status launch_status() {
 }
 
 }  // namespace
+
+pi_status pih::launched() { return launch_status(); }
 
 namespace {
 

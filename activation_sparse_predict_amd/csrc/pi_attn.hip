@@ -1,0 +1,150 @@
+// Host side of the attention operators (pi.h): checks, workspace, launches.
+#include "pi_attn.hpp"
+
+#include <algorithm>
+#include <cmath>
+
+#include "pi_host.hpp"
+
+using namespace pih;
+
+namespace {
+
+pi_status check_shape(int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype) {
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || dim < 8 || dim % 8 != 0) return PI_EINVAL;
+  if (dtype != PI_F16 && dtype != PI_BF16) return dtype == PI_F32 ? PI_EUNSUPPORTED : PI_EINVAL;
+  if (dim > 256 || heads > 4096) return PI_EUNSUPPORTED;
+  return PI_OK;
+}
+
+// 2^x instead of e^x: c = scale log2(e); false if the scale is not finite and positive
+bool scale_of(float scale, int dim, float* c) {
+  const double s = scale == 0.f ? 1.0 / std::sqrt((double)dim) : (double)scale;
+  *c = (float)(s * 1.4426950408889634);
+  return std::isfinite(*c) && *c > 0.f;
+}
+
+pia::Rows rows_of(const pi_heads* h) {
+  return pia::Rows{static_cast<const uint16_t*>(h->p), h->token_stride, h->head_stride};
+}
+
+// shares of a row's keys: four blocks for each compute unit in all, and at least 128 keys a share
+int splits_for(const pi_cache* c, int batch, int heads) {
+  const int group = heads / c->kv_heads;
+  const int64_t rows = (int64_t)batch * c->kv_heads * up_div(group, 16);
+  const int64_t most = up_div((int64_t)c->max_pages * c->page, 128);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({up_div(1024, rows), most, 64}));
+}
+
+struct Ws {
+  size_t stat, total;
+};
+Ws ws_of(const pi_cache* c, int batch, int heads) {
+  const size_t rows = (size_t)batch * heads * splits_for(c, batch, heads);
+  Ws w{};
+  w.stat = ws_align(sizeof(float) * rows * c->dim);
+  w.total = w.stat + ws_align(sizeof(float) * 2 * rows);
+  return w;
+}
+
+pi_status check_batch(const pi_cache* c, int32_t batch, int32_t heads) {
+  pi_status s;
+  if ((s = check_cache(c)) != PI_OK) return s;
+  if (batch < 1) return PI_EINVAL;
+  if ((s = check_shape(heads, c->kv_heads, c->dim, c->dtype)) != PI_OK) return s;
+  return batch > 4096 ? PI_EUNSUPPORTED : PI_OK;
+}
+
+// f(a value of the element type, a constant of the padded dim)
+template <class F>
+void with_type(int dtype, int dim, F f) {
+  auto by_dim = [&](auto t) {
+    if (dim <= 64) f(t, std::integral_constant<int, 64>());
+    else if (dim <= 96) f(t, std::integral_constant<int, 96>());
+    else if (dim <= 128) f(t, std::integral_constant<int, 128>());
+    else f(t, std::integral_constant<int, 256>());
+  };
+  if (dtype == PI_F16) by_dim(pit::H16());
+  else by_dim(pit::B16());
+}
+
+}  // namespace
+
+pi_status pih::check_heads(const pi_heads* h, int32_t tokens) {
+  if (!h || (!h->p && tokens > 0) || !on(h->p, 16)) return PI_EINVAL;
+  return h->token_stride % 8 != 0 || h->head_stride % 8 != 0 ? PI_EINVAL : PI_OK;
+}
+
+extern "C" {
+
+pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v, const pi_heads* out, int32_t tokens,
+                         int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype, const int32_t* cu, int32_t n,
+                         float scale, void* stream) {
+  pi_status s;
+  if ((s = check_shape(heads, kv_heads, dim, dtype)) != PI_OK) return s;
+  if (tokens < 0 || n < 1 || !cu || !on(cu, 4)) return PI_EINVAL;
+  for (const pi_heads* h : {q, k, v, out})
+    if ((s = check_heads(h, tokens)) != PI_OK) return s;
+  float c;
+  if (!scale_of(scale, dim, &c)) return PI_EINVAL;
+  if (tokens == 0) return PI_OK;
+  // a tile of each sequence may be short
+  const int64_t blocks = (up_div(tokens, pia::PT_Q) + std::min(n, tokens)) * heads;
+  if (blocks > INT32_MAX) return PI_EUNSUPPORTED;
+  (void)hipGetLastError();
+  with_type(dtype, dim, [&](auto t, auto d) {
+    hipLaunchKernelGGL((pia::k_attn_prompt<decltype(t), decltype(d)::value>), dim3((unsigned)blocks),
+                       dim3(pia::PT_WAVES * pia::WAVE), 0, static_cast<hipStream_t>(stream), rows_of(q), rows_of(k),
+                       rows_of(v), static_cast<uint16_t*>(out->p), out->token_stride, out->head_stride, cu, n, tokens,
+                       heads, heads / kv_heads, dim, c);
+  });
+  return launched();
+}
+
+size_t pi_attn_workspace_bytes(const pi_cache* c, int32_t batch, int32_t heads) {
+  return check_batch(c, batch, heads) == PI_OK ? ws_of(c, batch, heads).total : 0;
+}
+
+pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q, const pi_heads* out, int32_t batch,
+                         int32_t heads, const int32_t* seqs, const int32_t* prefix, float scale, void* ws,
+                         size_t ws_bytes, void* stream) {
+  pi_status s;
+  if ((s = check_batch(cache, batch, heads)) != PI_OK) return s;
+  if (layer < 0 || layer >= cache->layers || !on(seqs, 4) || !on(prefix, 4)) return PI_EINVAL;
+  if (!seqs && batch > cache->slots) return PI_EINVAL;
+  if ((s = check_heads(q, batch)) != PI_OK || (s = check_heads(out, batch)) != PI_OK) return s;
+  float c;
+  if (!scale_of(scale, cache->dim, &c)) return PI_EINVAL;
+  const Ws W = ws_of(cache, batch, heads);
+  if (!ws || ws_bytes < W.total || !on(ws, kWsAlign)) return PI_EWORKSPACE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int splits = splits_for(cache, batch, heads), group = heads / cache->kv_heads, dim = cache->dim;
+  float* part = static_cast<float*>(ws);
+  float* stat = reinterpret_cast<float*>(static_cast<char*>(ws) + W.stat);
+  const int64_t at = (int64_t)layer * cache->pages * cache->kv_heads * cache->page * dim;
+  int32_t* lens = cache->meta + (int64_t)cache->slots * cache->max_pages;
+  const pia::Pages pg{static_cast<const uint16_t*>(cache->k) + at,
+                      static_cast<const uint16_t*>(cache->v) + at,
+                      cache->meta,
+                      lens,
+                      lens + cache->slots + 2 * (int64_t)cache->pages + 1,
+                      cache->pages,
+                      cache->page,
+                      cache->max_pages,
+                      cache->slots};
+  (void)hipGetLastError();
+  with_type(cache->dtype, dim, [&](auto t, auto d) {
+    using T = decltype(t);
+    uint16_t* o = static_cast<uint16_t*>(out->p);
+    hipLaunchKernelGGL((pia::k_attn_decode<T, decltype(d)::value>),
+                       dim3(splits, (unsigned)(cache->kv_heads * up_div(group, 16)), batch),
+                       dim3(pia::DC_WAVES * pia::WAVE), 0, st, pg, rows_of(q), o, out->token_stride, out->head_stride,
+                       seqs, heads, cache->kv_heads, dim, splits, c, part, stat);
+    if (splits > 1)
+      hipLaunchKernelGGL((pia::k_attn_join<T>), dim3((unsigned)(batch * heads)), dim3(dim <= 64 ? 64 : 128), 0, st,
+                         part, stat, o, out->token_stride, out->head_stride, heads, dim, splits, c);
+  });
+  return launched();
+}
+
+}  // extern "C"

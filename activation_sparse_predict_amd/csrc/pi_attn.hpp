@@ -1,0 +1,476 @@
+// Device code of the attention operators for gfx950.
+//
+// For a query row q and the keys j it sees, with c = scale log2(e):
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c (s_j - m)),  s_j = q . k_j
+// with m the largest s_j so far; when m grows, what was summed is multiplied by
+// 2^(c (m_old - m)).  Scores, m, the sums and o are float32.  The unnormalised
+// p_j are rounded to the inputs' type for the second product (as the type's
+// matrix instruction takes them): at most half a step each, relative to values
+// in (0, 1], and independent between keys, so the output is off by less than
+// its own rounding to that type.  sum_j p_j adds the unrounded values.
+//
+// Both kernels compute S^T = K Q^T and O^T = V^T P^T, so that a lane holds all
+// its scores for one query: softmax statistics need one or two cross-lane
+// steps, and the D registers of the first product, rounded, are the B operand
+// of the second (the order of the keys inside a matrix instruction is free).
+#pragma once
+#include "pi.h"
+#include "pi_tile.hpp"
+
+#include <type_traits>
+
+namespace pia {
+
+using namespace pit;
+
+// A [tokens][heads][dim] tensor with its strides in elements (dim is contiguous).
+struct Rows {
+  const uint16_t* p;
+  int64_t token, head;
+  __device__ __forceinline__ const uint16_t* at(int64_t t, int h) const { return p + t * token + h * head; }
+};
+
+constexpr float NEG_INF = -__builtin_inff();
+
+// ------------------------------------------------------- attention over prompts
+constexpr int PT_WAVES = 4;              // waves of a block
+constexpr int PT_Q = 32 * PT_WAVES;      // query rows of a block
+constexpr int PT_K = 64;                 // keys of a tile
+
+// LDS rows of a tile: a power of two of 16-byte chunks, so that a row starts on
+// a fixed bank, and chunk c of row r lies at position c ^ swz(r).  The 32 rows
+// one operand read touches, and the 4 rows x 64 bytes that half a wave reads
+// transposed, then cover every bank equally.
+template <int D> struct Tile {
+  static constexpr int NC = D <= 64 ? 8 : D <= 128 ? 16 : 32;   // chunks of a row in LDS
+  static constexpr int KS = D / 16;                             // k steps of Q K^T
+  static constexpr int DT = D / 32;                             // 32-wide tiles of the output
+  static __device__ __forceinline__ int swz(int r) {
+    if constexpr (NC == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    else return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+  static __device__ __forceinline__ int chunk(int r, int c) { return r * NC + (c ^ swz(r)); }
+};
+
+// The block's sequence and its query tile: tiles are numbered sequence by
+// sequence, the last (longest) tile of a sequence first.
+struct Place {
+  int start, len, tile;                  // first token, tokens, tile; len = 0: nothing to do
+};
+__device__ __forceinline__ Place find_tile(const int32_t* cu, int n, int tokens, int idx) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  for (int base = 0; base < n; base += WAVE) {
+    const int i = base + lane;
+    int a = 0, b = 0;
+    if (i < n) {
+      a = min(max(cu[i], 0), tokens);
+      b = min(max(cu[i + 1], a), tokens);
+    }
+    const int t = (b - a + PT_Q - 1) / PT_Q;
+    const int upto = scan64(t);
+    const uint64_t hit = __ballot(upto > idx);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int st = __builtin_amdgcn_readlane(a, l), en = __builtin_amdgcn_readlane(b, l);
+      const int last = __builtin_amdgcn_readlane(upto, l) - 1;
+      return Place{st, en - st, last - idx};
+    }
+    idx -= __builtin_amdgcn_readlane(upto, WAVE - 1);
+  }
+  return Place{0, 0, 0};
+}
+
+// One block: 128 query rows of one sequence and head, 32 for each wave, over
+// the keys up to the last row in tiles of 64 from the last one down.  A wave's
+// rows lie in one 64-aligned span, so exactly the first tile it computes is
+// partly masked.
+template <class T, int D>
+__global__ void __launch_bounds__(PT_WAVES * WAVE)
+k_attn_prompt(Rows q, Rows k, Rows v, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head,
+              const int32_t* __restrict__ cu, int n, int tokens, int heads, int group, int dim, float c) {
+  using L = Tile<D>;
+  constexpr int NT = PT_WAVES * WAVE;
+  constexpr int LD = PT_K * L::NC / NT;            // chunks of a tile per thread
+  __shared__ u4 sk[PT_K * L::NC];
+  __shared__ u4 sv[PT_K * L::NC];
+
+  const int head = blockIdx.x % heads;
+  const Place pl = find_tile(cu, n, tokens, blockIdx.x / heads);
+  if (pl.len == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hi = lane >> 5, col = lane & 31;
+  const int row0 = pl.tile * PT_Q + 32 * w;        // the wave's first row in the sequence
+  const int row = row0 + col;
+  const int nchunk = dim / 8;
+
+  // Q^T as B operand, in registers for the whole block
+  u4 qf[L::KS];
+  {
+    const uint16_t* src = q.at(pl.start + min(row, pl.len - 1), head);
+#pragma unroll
+    for (int s = 0; s < L::KS; ++s) {
+      const int ch = 2 * s + hi;
+      qf[s] = ch < nchunk ? *reinterpret_cast<const u4*>(src + 8 * ch) : u4{0, 0, 0, 0};
+    }
+  }
+  f16v o[L::DT];
+#pragma unroll
+  for (int t = 0; t < L::DT; ++t) o[t] = (f16v)(0.f);
+  float m = NEG_INF, l = 0.f;
+
+  const int kv = head / group;
+  const int key_end = min(pl.len, (pl.tile + 1) * PT_Q);
+  const int my_tile = (row0 + 31) / PT_K;          // the wave's last (masked) tile
+  for (int kt = (key_end - 1) / PT_K; kt >= 0; --kt) {
+    __syncthreads();                               // the tile before this one has been read
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int e = i * NT + tid, r = e / L::NC, ch = e % L::NC;
+      const int64_t tok = pl.start + min(kt * PT_K + r, pl.len - 1);
+      u4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+      if (ch < nchunk) {
+        a = *reinterpret_cast<const u4*>(k.at(tok, kv) + 8 * ch);
+        b = *reinterpret_cast<const u4*>(v.at(tok, kv) + 8 * ch);
+      }
+      sk[L::chunk(r, ch)] = a;
+      sv[L::chunk(r, ch)] = b;
+    }
+    __syncthreads();
+    if (kt > my_tile) continue;                    // every key lies behind the wave's rows
+
+    // S^T: two tiles of 32 keys
+    f16v s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[h] = (f16v)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < L::KS; ++ks)
+        s[h] = T::mma32(sk[L::chunk(32 * h + col, 2 * ks + hi)], qf[ks], s[h]);
+    }
+    const bool masked = kt == my_tile;
+    if (masked) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = kt * PT_K + 32 * h + 8 * (i / 4) + 4 * hi + i % 4;
+          if (key > row) s[h][i] = NEG_INF;
+        }
+    }
+    float mt = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, fmaxf(s[0][i], s[1][i]));
+    const float mn = fmaxf(m, max32(mt));
+    // rows whose scores so far are all -inf keep m = -inf; 0 stands in for it in the differences
+    const float mc = mn == NEG_INF ? 0.f : mn * c;
+    const float alpha = exp2_fast(fmaf(m, c, -mc));
+    m = mn;
+    uint32_t pw[16];
+    float ls = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float a = exp2_fast(fmaf(s[h][i], c, -mc)), b = exp2_fast(fmaf(s[h][i + 1], c, -mc));
+        ls += a + b;
+        pw[8 * h + i / 2] = T::pack(a, b);
+      }
+    l = fmaf(l, alpha, ls);
+#pragma unroll
+    for (int t = 0; t < L::DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
+    // V^T as A operand: transposing LDS reads, each giving a lane 4 keys of one output dimension
+    auto vfrag = [&](int step, int t) {            // keys 16 step.., dims 32 t..
+      const int j = lane & 15, cc = 4 * t + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+      u4 f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * step + 8 * e + 4 * hi + (j >> 2);
+        const char* at = reinterpret_cast<const char*>(&sv[L::chunk(r, cc)]) + 8 * (j & 1);
+        const u2 x = __builtin_bit_cast(
+            u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at));
+        f[2 * e] = x[0];
+        f[2 * e + 1] = x[1];
+      }
+      return f;
+    };
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+      const u4 pf = {pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]};
+#pragma unroll
+      for (int t = 0; t < L::DT; ++t) o[t] = T::mma32(vfrag(st, t), pf, o[t]);
+    }
+    if (masked) {
+      // 0 times an infinity or NaN of a masked key is NaN.  This is the wave's first tile
+      // (o held nothing before it), so where any value came out non-finite the tile's sum
+      // is taken again key by key, adding only to the rows that see the key.
+      float bad = 0.f;
+#pragma unroll
+      for (int t = 0; t < L::DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad = fmaf(o[t][i], 0.f, bad);
+      if (__ballot(bad != bad)) {
+#pragma unroll
+        for (int t = 0; t < L::DT; ++t) {
+          o[t] = (f16v)(0.f);
+          for (int key = 0; key < PT_K; ++key) {
+            const int st = key >> 4, e = (key & 3) + 4 * ((key >> 3) & 1);
+            const bool mine = ((key >> 2) & 1) == hi;
+            const u4 vf = vfrag(st, t);
+            u4 va, pa;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t keep = mine && x == e / 2 ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+              va[x] = vf[x] & keep;
+              pa[x] = (st == 0 ? pw[x] : st == 1 ? pw[4 + x] : st == 2 ? pw[8 + x] : pw[12 + x]) & keep;
+            }
+            const f16v one = T::mma32(va, pa, (f16v)(0.f));
+            if (kt * PT_K + key <= row)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[t][i] += one[i];
+          }
+        }
+      }
+    }
+  }
+  if (row0 >= pl.len) return;
+  l = sum32(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;      // no weight at all (every score -inf): zero
+  uint16_t* dst = out + (pl.start + row) * out_token + head * out_head;
+#pragma unroll
+  for (int t = 0; t < L::DT; ++t)
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {                  // 16 dims: the lane halves trade so that each stores 8
+      const int i = 8 * g;
+      const uint32_t a0 = T::pack(o[t][i] * inv, o[t][i + 1] * inv), a1 = T::pack(o[t][i + 2] * inv, o[t][i + 3] * inv);
+      const uint32_t b0 = T::pack(o[t][i + 4] * inv, o[t][i + 5] * inv), b1 = T::pack(o[t][i + 6] * inv, o[t][i + 7] * inv);
+      const auto r0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+      const auto r1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+      const int ch = 4 * t + 2 * g + hi;
+      if (row < pl.len && ch < nchunk) *reinterpret_cast<u4*>(dst + 8 * ch) = u4{r0[0], r1[0], r0[1], r1[1]};
+    }
+}
+
+// ------------------------------------------------ attention of single new tokens
+// What a decode kernel sees of a cache's layer.
+struct Pages {
+  const uint16_t *k, *v;                 // the layer's pages [pages][kv_heads][page][dim]
+  const int32_t *table, *lens;           // [slots][max_pages], [slots]
+  int32_t* flags;                        // the cache's error word
+  int pages, page, max_pages, slots;
+};
+
+constexpr int DC_WAVES = 4;
+constexpr int DC_K = 32;                 // keys of a wave's step
+
+// O^T of the 16x16x32 product: a lane's A operand row l % 16 stands for VW
+// consecutive output dims (VW operands), so V is loaded with VW elements per
+// lane, whole rows of the page by 16 lanes, and transposed in registers.
+template <int D> struct Vec {
+  static constexpr int W = D <= 64 ? 4 : 8;        // dims per lane and load
+  static constexpr int G = D <= 128 ? 1 : D / 128; // such groups of 16 W dims
+  static constexpr int KS = (D + 31) / 32;         // k steps of Q K^T
+};
+
+// The slot of batch row b, or -1.
+__device__ __forceinline__ int slot_of(const int32_t* seqs, int b, int slots) {
+  const int s = seqs ? seqs[b] : b;
+  return (unsigned)s < (unsigned)slots ? s : -1;
+}
+
+// One block: the query heads [16 rt, 16 rt + 16) of a key head's group, one
+// batch row, and one of `splits` shares of its keys; the waves take steps of 32
+// keys in turn and join their sums through LDS.  Partial results (or, with one
+// share, the output) are written per query head.
+template <class T, int D>
+__global__ void __launch_bounds__(DC_WAVES * WAVE)
+k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head,
+              const int32_t* __restrict__ seqs, int heads, int kv_heads, int dim, int splits, float c,
+              float* __restrict__ part, float* __restrict__ stat) {
+  using V = Vec<D>;
+  constexpr int NF = V::W * V::G;                  // operands of the second product
+  __shared__ float sm[DC_WAVES][2][16];
+  __shared__ float so[DC_WAVES][16][16 * NF + 4];
+
+  const int b = blockIdx.z, split = blockIdx.x, group = heads / kv_heads;
+  const int rts = (group + 15) / 16, g = blockIdx.y / rts, rt = blockIdx.y % rts;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, kg = lane >> 4;
+  const int slot = slot_of(seqs, b, pg.slots);
+  int len = slot >= 0 ? pg.lens[slot] : 0;
+  if (slot < 0 || len < 0 || len > (int64_t)pg.max_pages * pg.page) {
+    if (tid == 0) atomicOr(pg.flags, slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
+    len = 0;
+  }
+  const int steps = (len + DC_K - 1) / DC_K;
+  const int first = (int)((int64_t)steps * split / splits), last = (int)((int64_t)steps * (split + 1) / splits);
+  const int nchunk = dim / 8;
+
+  const int head = g * group + 16 * rt + min(r, group - 16 * rt - 1);
+  u4 qf[V::KS];
+#pragma unroll
+  for (int s = 0; s < V::KS; ++s) {
+    const int ch = 4 * s + kg;
+    qf[s] = ch < nchunk ? *reinterpret_cast<const u4*>(q.at(b, head) + 8 * ch) : u4{0, 0, 0, 0};
+  }
+  f4 o[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) o[f] = (f4)(0.f);
+  float m = NEG_INF, l = 0.f;
+  const int32_t* row = pg.table + (int64_t)max(slot, 0) * pg.max_pages;
+  const int64_t head_stride = (int64_t)pg.page * dim, page_stride = head_stride * kv_heads;
+
+  for (int st = first + w; st < last; st += DC_WAVES) {
+    // the two halves of 16 keys lie in one page each (pages hold multiples of 16 tokens)
+    const uint16_t *kp[2], *vp[2];
+    int seen[2];                                   // keys of the half that exist
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = st * DC_K + 16 * h;
+      seen[h] = max(0, min(16, len - key));
+      const int place = min(key / pg.page, pg.max_pages - 1);
+      int id = row[place];
+      if ((unsigned)id >= (unsigned)pg.pages) {    // a broken table: its keys are not seen
+        if (seen[h] && lane == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
+        seen[h] = 0;
+        id = 0;
+      }
+      const int64_t at = id * page_stride + g * head_stride + (int64_t)(key % pg.page) * dim;
+      kp[h] = pg.k + at;
+      vp[h] = pg.v + at;
+    }
+    f4 s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[h] = (f4)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < V::KS; ++ks) {
+        const int ch = 4 * ks + kg;
+        u4 a = {0, 0, 0, 0};
+        if (ch < nchunk) a = *reinterpret_cast<const u4*>(kp[h] + r * dim + 8 * ch);
+        s[h] = T::mma16(a, qf[ks], s[h]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * kg + i >= seen[h]) s[h][i] = NEG_INF;
+    }
+    float mt = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mt = fmaxf(mt, fmaxf(s[0][i], s[1][i]));
+    const float mn = fmaxf(m, max16(mt));
+    const float mc = mn == NEG_INF ? 0.f : mn * c;   // see k_attn_prompt
+    const float alpha = exp2_fast(fmaf(m, c, -mc));
+    m = mn;
+    float p[8], ls = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = exp2_fast(fmaf(s[i / 4][i % 4], c, -mc));
+      ls += p[i];
+    }
+    l = fmaf(l, alpha, ls);
+    const u4 pf = {T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
+    // V: keys 4 kg + 0..3 of both halves; rows that do not exist count as zeros, whatever is stored there
+#pragma unroll
+    for (int gr = 0; gr < V::G; ++gr) {
+      uint32_t x[8][V::W / 2];
+      const int d0 = (16 * gr + r) * V::W;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int key = 4 * kg + i % 4;
+#pragma unroll
+        for (int e = 0; e < V::W / 2; ++e) x[i][e] = 0;
+        if (key < seen[i / 4] && d0 < dim) {
+          const uint16_t* src = vp[i / 4] + key * dim + d0;
+          if constexpr (V::W == 8) {
+            const u4 y = *reinterpret_cast<const u4*>(src);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[i][e] = y[e];
+          } else {
+            const u2 y = *reinterpret_cast<const u2*>(src);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[i][e] = y[e];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < V::W / 2; ++e) {
+        const u4 a = {lows(x[0][e], x[1][e]), lows(x[2][e], x[3][e]), lows(x[4][e], x[5][e]), lows(x[6][e], x[7][e])};
+        const u4 z = {highs(x[0][e], x[1][e]), highs(x[2][e], x[3][e]), highs(x[4][e], x[5][e]),
+                      highs(x[6][e], x[7][e])};
+        const int f = gr * V::W + 2 * e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[f][i] *= alpha;
+          o[f + 1][i] *= alpha;
+        }
+        o[f] = T::mma16(a, pf, o[f]);
+        o[f + 1] = T::mma16(z, pf, o[f + 1]);
+      }
+    }
+  }
+  l = sum16(l);
+
+  // join the waves: o[f][i] belongs to dim (16 gr + 4 kg + i) W + f % W of query r
+  if (lane < 16) {
+    sm[w][0][r] = m;
+    sm[w][1][r] = l;
+  }
+#pragma unroll
+  for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int f = 0; f < V::W; ++f) so[w][r][(16 * gr + 4 * kg + i) * V::W + f] = o[gr * V::W + f][i];
+  __syncthreads();
+  for (int e = tid; e < 16 * dim; e += DC_WAVES * WAVE) {
+    const int qr = e / dim, d = e % dim;
+    if (16 * rt + qr >= group) break;
+    float mm = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < DC_WAVES; ++i) mm = fmaxf(mm, sm[i][0][qr]);
+    const float mc = mm == NEG_INF ? 0.f : mm * c;
+    float ll = 0.f, oo = 0.f;
+#pragma unroll
+    for (int i = 0; i < DC_WAVES; ++i) {
+      const float a = exp2_fast(fmaf(sm[i][0][qr], c, -mc));
+      ll = fmaf(sm[i][1][qr], a, ll);
+      oo = fmaf(so[i][qr][d], a, oo);
+    }
+    const int h = g * group + 16 * rt + qr;
+    if (splits == 1) {
+      const float y = ll == 0.f ? 0.f : oo / ll;   // a row that sees no key is zero
+      out[b * out_token + h * out_head + d] = (uint16_t)T::pack(y, 0.f);
+    } else {
+      const int64_t at = ((int64_t)b * heads + h) * splits + split;
+      part[at * dim + d] = oo;
+      if (d == 0) {
+        stat[2 * at] = mm;
+        stat[2 * at + 1] = ll;
+      }
+    }
+  }
+}
+
+// Join a row's shares: one block per (batch row, query head).
+template <class T>
+__global__ void __launch_bounds__(256)
+k_attn_join(const float* __restrict__ part, const float* __restrict__ stat, uint16_t* __restrict__ out,
+            int64_t out_token, int64_t out_head, int heads, int dim, int splits, float c) {
+  const int b = blockIdx.x / heads, h = blockIdx.x % heads;
+  const float* st = stat + 2 * (int64_t)blockIdx.x * splits;
+  float mm = NEG_INF;
+  for (int i = 0; i < splits; ++i) mm = fmaxf(mm, st[2 * i]);
+  const float mc = mm == NEG_INF ? 0.f : mm * c;
+  for (int d = threadIdx.x; d < dim; d += blockDim.x) {
+    float ll = 0.f, oo = 0.f;
+    for (int i = 0; i < splits; ++i) {
+      const float a = exp2_fast(fmaf(st[2 * i], c, -mc));
+      ll = fmaf(st[2 * i + 1], a, ll);
+      oo = fmaf(part[((int64_t)blockIdx.x * splits + i) * dim + d], a, oo);
+    }
+    out[b * out_token + h * out_head + d] = (uint16_t)T::pack(ll == 0.f ? 0.f : oo / ll, 0.f);
+  }
+}
+
+}  // namespace pia

@@ -1,0 +1,354 @@
+// Device code of the paged key/value cache for gfx950: page accounting (one
+// block each, so that its result does not depend on timing) and page copies.
+//
+// The accounting kernels check everything they read before they write: a call
+// that cannot be carried out whole sets a bit of the cache's error word and
+// leaves the tables as they were.
+#pragma once
+#include "pi.h"
+#include "pi_tile.hpp"
+
+namespace pic {
+
+using namespace pit;
+
+constexpr int PL_T = 1024;               // threads of an accounting block
+constexpr int MAX_N = 4096;              // slots one call may name
+
+// The parts of pi_cache.meta.
+struct Meta {
+  int32_t *table, *lens, *ref, *free, *words;
+  int slots, max_pages, pages, page;
+};
+
+__device__ __forceinline__ int pages_of(int64_t tokens, int page) { return (int)((tokens + page - 1) / page); }
+
+// Exclusive prefix sum over the block's threads and the total, by waves.
+__device__ __forceinline__ int block_scan(int v, int& total) {
+  __shared__ int part[PL_T / WAVE];
+  const int w = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
+  const int up = scan64(v);
+  __syncthreads();
+  if (lane == WAVE - 1) part[w] = up;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+  for (int i = 0; i < (int)(blockDim.x / WAVE); ++i) {
+    if (i < w) before += part[i];
+    total += part[i];
+  }
+  return before + up - v;
+}
+
+// Whether a thread's `bad` is set anywhere in the block; if so the bits go to the error word.
+__device__ __forceinline__ bool refuse(int bad, int32_t* words) {
+  if (bad) atomicOr(&words[1], bad);
+  return __syncthreads_or(bad) != 0;
+}
+
+// slots[i] equal to an earlier one (the list lies in LDS)
+__device__ __forceinline__ bool twice(const int* slots, int i) {
+  for (int j = 0; j < i; ++j)
+    if (slots[j] == slots[i]) return true;
+  return false;
+}
+
+// The pages that `need` pops take from the stack: free, in range, and as many as there are.
+__device__ __forceinline__ int stack_errors(const Meta& m, int total) {
+  const int top = m.words[0];
+  if (top < 0 || top > m.pages) return PI_CACHE_EPAGE;
+  if (total > top) return PI_CACHE_EFULL;
+  for (int i = threadIdx.x; i < total; i += blockDim.x) {
+    const int p = m.free[top - 1 - i];
+    if ((unsigned)p >= (unsigned)m.pages || m.ref[p] != 0) return PI_CACHE_EPAGE;
+  }
+  return 0;
+}
+
+// Room for counts[i] more tokens in slot seqs[i]: pages from the stack, in the order of the list.
+__global__ void __launch_bounds__(PL_T)
+k_cache_extend(Meta m, const int32_t* __restrict__ seqs, const int32_t* __restrict__ counts, int n) {
+  __shared__ int slot[MAX_N];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) slot[i] = seqs[i];
+  __syncthreads();
+  int bad = 0, carry = 0;
+  for (int base = 0; base < n; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    int need = 0;
+    if (i < n) {
+      if ((unsigned)slot[i] >= (unsigned)m.slots || twice(slot, i)) {
+        bad |= PI_CACHE_ESLOT;
+      } else {
+        const int64_t len = m.lens[slot[i]], now = len + counts[i];
+        if (len < 0 || counts[i] < 0 || now > (int64_t)m.max_pages * m.page) bad |= PI_CACHE_ELENGTH;
+        else need = pages_of(now, m.page) - pages_of(len, m.page);
+      }
+    }
+    int total;
+    block_scan(need, total);
+    carry = min(carry + total, m.pages + 1);       // more than there are is all the same
+  }
+  bad |= stack_errors(m, carry);
+  if (refuse(bad, m.words)) return;
+  const int top = m.words[0];
+  int at = 0;
+  for (int base = 0; base < n; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    int need = 0, have = 0, len = 0;
+    if (i < n) {
+      len = m.lens[slot[i]];
+      have = pages_of(len, m.page);
+      need = pages_of((int64_t)len + counts[i], m.page) - have;
+    }
+    int total;
+    const int before = at + block_scan(need, total);
+    for (int j = 0; j < need; ++j) {
+      const int p = m.free[top - 1 - before - j];
+      m.table[(int64_t)slot[i] * m.max_pages + have + j] = p;
+      m.ref[p] = 1;
+    }
+    if (i < n) m.lens[slot[i]] = len + counts[i];
+    at += total;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) m.words[0] = top - at;
+}
+
+// The last counts tokens of each listed slot go to their pages: thread per 16 bytes of a key and a value.
+__global__ void __launch_bounds__(256)
+k_cache_append(Meta m, uint16_t* __restrict__ kl, uint16_t* __restrict__ vl, int kv_heads, int dim,
+               const uint16_t* __restrict__ k, int64_t k_token, int64_t k_head, const uint16_t* __restrict__ v,
+               int64_t v_token, int64_t v_head, const int32_t* __restrict__ cu, const int32_t* __restrict__ seqs,
+               int n, int tokens) {
+  const int per = kv_heads * (dim / 8);
+  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int t = (int)(e / per), head = (int)(e % per) / (dim / 8), ch = (int)(e % per) % (dim / 8);
+  if (t >= tokens || t < cu[0] || t >= cu[n]) return;
+  int lo = 0, up = n;                              // cu[lo] <= t < cu[up]
+  while (up - lo > 1) {
+    const int mid = (lo + up) / 2;
+    if (cu[mid] <= t) lo = mid;
+    else up = mid;
+  }
+  const int slot = seqs[lo];
+  int bad = 0;
+  if ((unsigned)slot >= (unsigned)m.slots) {
+    bad = PI_CACHE_ESLOT;
+  } else {
+    const int64_t pos = (int64_t)m.lens[slot] - cu[lo + 1] + t;
+    if (pos < 0 || pos >= (int64_t)m.max_pages * m.page) {
+      bad = PI_CACHE_ELENGTH;
+    } else {
+      const int p = m.table[(int64_t)slot * m.max_pages + pos / m.page];
+      if ((unsigned)p >= (unsigned)m.pages) {
+        bad = PI_CACHE_EPAGE;
+      } else {
+        const int64_t at = (((int64_t)p * kv_heads + head) * m.page + pos % m.page) * dim + 8 * ch;
+        *reinterpret_cast<u4*>(kl + at) = *reinterpret_cast<const u4*>(k + t * k_token + head * k_head + 8 * ch);
+        *reinterpret_cast<u4*>(vl + at) = *reinterpret_cast<const u4*>(v + t * v_token + head * v_head + 8 * ch);
+      }
+    }
+  }
+  if (bad) atomicOr(&m.words[1], bad);
+}
+
+// The pages a call copies: count, then the sources and the targets, each `cap` long.
+struct Plan {
+  int32_t *count, *src, *dst;
+};
+
+// children[i] becomes a copy of parents[i]: it shares the whole pages and gets a page of its own for a
+// last page that is not full, whose copy the plan asks for.  Parents are read as they were before the call.
+__global__ void __launch_bounds__(PL_T)
+k_cache_fork(Meta m, const int32_t* __restrict__ parents, const int32_t* __restrict__ children, int n, Plan plan) {
+  __shared__ int kid[MAX_N], len_of[MAX_N];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) kid[i] = children[i];
+  if (threadIdx.x == 0) *plan.count = 0;
+  __syncthreads();
+  int bad = 0, all = 0;
+  for (int base = 0; base < n; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    int part = 0;
+    if (i < n) {
+      const int p = parents[i];
+      if ((unsigned)kid[i] >= (unsigned)m.slots || (unsigned)p >= (unsigned)m.slots || twice(kid, i) ||
+          m.lens[kid[i]] != 0) {
+        bad |= PI_CACHE_ESLOT;
+      } else {
+        const int len = m.lens[p];
+        if (len < 0 || len > (int64_t)m.max_pages * m.page) {
+          bad |= PI_CACHE_ELENGTH;
+        } else {
+          len_of[i] = len;
+          part = len % m.page != 0;
+        }
+      }
+    }
+    int total;
+    block_scan(part, total);
+    all += total;
+  }
+  if (refuse(bad, m.words)) return;
+  // every page of every parent, a wave for each
+  const int w = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1), waves = blockDim.x / WAVE;
+  for (int i = w; i < n; i += waves) {
+    const int32_t* row = m.table + (int64_t)parents[i] * m.max_pages;
+    for (int j = lane; j < pages_of(len_of[i], m.page); j += WAVE)
+      if ((unsigned)row[j] >= (unsigned)m.pages || m.ref[row[j]] <= 0) bad |= PI_CACHE_EPAGE;
+  }
+  bad |= stack_errors(m, all);
+  if (refuse(bad, m.words)) return;
+  const int top = m.words[0];
+  int at = 0;
+  for (int base = 0; base < n; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    const int part = i < n && len_of[i] % m.page != 0;
+    int total;
+    const int before = at + block_scan(part, total);
+    if (part) {
+      const int whole = len_of[i] / m.page, p = m.free[top - 1 - before];
+      plan.src[before] = m.table[(int64_t)parents[i] * m.max_pages + whole];
+      plan.dst[before] = p;
+      m.table[(int64_t)kid[i] * m.max_pages + whole] = p;
+      m.ref[p] = 1;
+    }
+    at += total;
+  }
+  __syncthreads();
+  for (int i = w; i < n; i += waves) {
+    const int32_t* row = m.table + (int64_t)parents[i] * m.max_pages;
+    int32_t* to = m.table + (int64_t)kid[i] * m.max_pages;
+    for (int j = lane; j < len_of[i] / m.page; j += WAVE) {
+      to[j] = row[j];
+      atomicAdd(&m.ref[row[j]], 1);
+    }
+    if (lane == 0) m.lens[kid[i]] = len_of[i];
+  }
+  if (threadIdx.x == 0) {
+    m.words[0] = top - at;
+    *plan.count = at;
+  }
+}
+
+// Whole pages from src to dst, in every layer of both pools: blockIdx.y is layer * 2 + pool.
+__global__ void __launch_bounds__(256)
+k_cache_copy(u4* __restrict__ k, u4* __restrict__ v, int64_t layer_chunks, int page_chunks, Plan plan) {
+  u4* pool = ((blockIdx.y & 1) ? v : k) + (int64_t)(blockIdx.y >> 1) * layer_chunks;
+  const int count = *plan.count;
+  for (int i = blockIdx.x; i < count; i += gridDim.x) {
+    const u4* from = pool + (int64_t)plan.src[i] * page_chunks;
+    u4* to = pool + (int64_t)plan.dst[i] * page_chunks;
+    for (int e = threadIdx.x; e < page_chunks; e += blockDim.x) to[e] = from[e];
+  }
+}
+
+// A count of uses, read past the first-level cache (other waves of the block changed it by atomics).
+__device__ __forceinline__ int uses(const int32_t* ref) {
+  return __hip_atomic_load(ref, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The listed slots become empty; pages that no slot uses any more go to the stack, the lowest on top.
+// Until they are collected such pages carry a count of -1, so that their order does not depend on timing.
+__global__ void __launch_bounds__(PL_T) k_cache_release(Meta m, const int32_t* __restrict__ seqs, int n) {
+  __shared__ int slot[MAX_N];
+  for (int i = threadIdx.x; i < n; i += blockDim.x) slot[i] = seqs[i];
+  __syncthreads();
+  int bad = 0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    if ((unsigned)slot[i] >= (unsigned)m.slots || twice(slot, i)) bad |= PI_CACHE_ESLOT;
+    else if (m.lens[slot[i]] < 0 || m.lens[slot[i]] > (int64_t)m.max_pages * m.page) bad |= PI_CACHE_ELENGTH;
+  }
+  const int top = m.words[0];
+  if (top < 0 || top > m.pages) bad |= PI_CACHE_EPAGE;
+  if (refuse(bad, m.words)) return;
+  const int w = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1), waves = blockDim.x / WAVE;
+  for (int i = w; i < n; i += waves) {
+    const int32_t* row = m.table + (int64_t)slot[i] * m.max_pages;
+    for (int j = lane; j < pages_of(m.lens[slot[i]], m.page); j += WAVE)
+      if ((unsigned)row[j] >= (unsigned)m.pages) bad |= PI_CACHE_EPAGE;
+  }
+  if (refuse(bad, m.words)) return;
+  for (int i = w; i < n; i += waves) {
+    const int32_t* row = m.table + (int64_t)slot[i] * m.max_pages;
+    for (int j = lane; j < pages_of(m.lens[slot[i]], m.page); j += WAVE) {
+      const int was = atomicSub(&m.ref[row[j]], 1);
+      if (was == 1) {
+        atomicExch(&m.ref[row[j]], -1);
+      } else if (was <= 0) {                       // held more often than it was counted
+        atomicAdd(&m.ref[row[j]], 1);
+        atomicOr(&m.words[1], PI_CACHE_EPAGE);
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) m.lens[slot[i]] = 0;
+  int at = top;
+  for (int base = 0; base < m.pages; base += blockDim.x) {
+    const int p = m.pages - 1 - (base + (int)threadIdx.x);
+    const int mine = p >= 0 && uses(&m.ref[p]) == -1;
+    int total;
+    const int pos = at + block_scan(mine, total);
+    if (mine) {
+      m.ref[p] = 0;
+      if (pos < m.pages) m.free[pos] = p;
+    }
+    at += total;
+  }
+  if (threadIdx.x == 0) m.words[0] = min(at, m.pages);
+}
+
+// The pages in use move to the front of the pool: the i-th page in use at or behind place `used` goes to the
+// i-th unused place before it.  to[p] is where page p went (itself if it did not move), -1 if it was not in use.
+__global__ void __launch_bounds__(PL_T) k_cache_compact(Meta m, Plan plan, int32_t* __restrict__ to) {
+  int used = 0;
+  for (int base = 0; base < m.pages; base += blockDim.x) {
+    const int p = base + threadIdx.x;
+    int total;
+    block_scan(p < m.pages && m.ref[p] > 0, total);
+    used += total;
+  }
+  int holes = 0, movers = 0;
+  for (int base = 0; base < m.pages; base += blockDim.x) {
+    const int p = base + threadIdx.x;
+    const bool in = p < m.pages, live = in && m.ref[p] > 0;
+    int total;
+    const int h = in && !live && p < used, mv = live && p >= used;
+    // a place is a hole or a mover, not both: one scan holds both counts (pages < 2^20, 1024 a round)
+    const int at = block_scan(h + (mv << 16), total);
+    if (h) plan.dst[holes + (at & 0xffff)] = p;
+    if (mv) plan.src[movers + (at >> 16)] = p;
+    if (in) to[p] = live ? p : -1;
+    holes += total & 0xffff;
+    movers += total >> 16;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < movers; i += blockDim.x) {
+    to[plan.src[i]] = plan.dst[i];
+    m.ref[plan.dst[i]] = m.ref[plan.src[i]];
+  }
+  __syncthreads();
+  for (int p = used + threadIdx.x; p < m.pages; p += blockDim.x) {
+    m.ref[p] = 0;
+    m.free[m.pages - 1 - p] = p;                   // the lowest on top
+  }
+  if (threadIdx.x == 0) {
+    m.words[0] = m.pages - used;
+    m.words[2] = used;
+    *plan.count = movers;
+  }
+}
+
+// The tables after a compaction: one thread per entry.
+__global__ void __launch_bounds__(256) k_cache_remap(Meta m, const int32_t* __restrict__ to, int32_t* __restrict__ moved) {
+  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (moved && e < m.pages) moved[e] = to[e];
+  if (e >= (int64_t)m.slots * m.max_pages) return;
+  const int slot = (int)(e / m.max_pages), place = (int)(e % m.max_pages);
+  if ((int64_t)place * m.page >= m.lens[slot]) return;
+  const int p = m.table[e];
+  const int now = (unsigned)p < (unsigned)m.pages ? to[p] : -1;
+  if (now < 0) atomicOr(&m.words[1], PI_CACHE_EPAGE);
+  else m.table[e] = now;
+}
+
+}  // namespace pic

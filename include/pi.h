@@ -67,7 +67,9 @@ typedef enum {
   PI_EHIP = 4           /* a kernel launch failed */
 } pi_status;
 
-typedef enum { PI_F32 = 0, PI_F16 = 1, PI_Q4_0 = 2 } pi_dtype;
+/* PI_BF16 (bfloat16) is a type of the attention operators' tensors and of
+ * pi_matvec's vectors; layers and predictors do not take it. */
+typedef enum { PI_F32 = 0, PI_F16 = 1, PI_Q4_0 = 2, PI_BF16 = 3 } pi_dtype;
 
 /* ReLU: h = max(b + W_up x, 0).  ReGLU: h = max(b + W_gate x, 0) * (W_up x).
  * Squared ReLU: h = max(b + W_up x, 0)^2.
@@ -217,6 +219,123 @@ pi_status pi_ffn_stack(const pi_layer* layers, int32_t n_layers, const float* x,
 pi_status pi_ffn_stack_static(const pi_layer* layers, int32_t n_layers, const float* x, int32_t batch,
                               float* out, int32_t* counts, int32_t* nz_counts, const pi_trace* trace,
                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder layer: a paged key/value cache, attention
+ * over whole prompts and of single new tokens, and products with Q4_0
+ * matrices (the projections around the attention).  The conventions at the
+ * top of this file hold, and further:
+ *  - Attention and cache tensors are PI_F16 or PI_BF16 (else PI_EUNSUPPORTED),
+ *    with 8 <= dim <= 256 and dim % 8 == 0; scores, softmax statistics and
+ *    sums are float32.
+ *  - heads % kv_heads == 0; query head h reads key head h / (heads / kv_heads).
+ *  - What only the device knows (lengths, slot and page numbers) is checked
+ *    there: nothing outside the tensors is ever read or written for it.  An
+ *    accounting call (extend, fork, release) that cannot be carried out whole
+ *    changes nothing but the cache's error word.
+ */
+
+/* A [tokens][heads][dim] tensor: strides in elements, the innermost dimension
+ * contiguous; p 16-byte aligned, strides multiples of 8. */
+typedef struct {
+  void* p;
+  int64_t token_stride, head_stride;
+} pi_heads;
+
+/* Bits of the cache's error word, set by kernels and never cleared by them. */
+#define PI_CACHE_ESLOT 1   /* a slot out of range, named twice, or a child that is not empty */
+#define PI_CACHE_EPAGE 2   /* a page number or use count that cannot be (a broken table or stack) */
+#define PI_CACHE_EFULL 4   /* not enough free pages */
+#define PI_CACHE_ELENGTH 8 /* a negative length, or one beyond the slot's table row */
+
+/* A paged key/value cache of `slots` sequences.
+ *  k, v:  [layers][pages][kv_heads][page][dim], 16-byte aligned; page a
+ *         multiple of 16, at most 4096; pages <= 2^20.
+ *  meta:  int32, pi_cache_meta_words(slots, max_pages, pages) of them:
+ *           table [slots][max_pages]  pages of a sequence, in order
+ *           lens  [slots]             its tokens
+ *           ref   [pages]             how many sequences use a page
+ *           free  [pages]             stack of the free pages (entries below the top)
+ *           words [4]                 top of the stack; error word; pages in
+ *                                     use, as counted by the last compaction; 0
+ * A new cache has meta zeroed but for the stack, free[i] = pages - 1 - i, and
+ * its top, pages.  slots <= 4096 in one call. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t* meta;
+  int32_t layers, pages, kv_heads, page, dim, dtype, slots, max_pages;
+} pi_cache;
+
+/* Words of pi_cache.meta (0 if a size is not positive). */
+size_t pi_cache_meta_words(int32_t slots, int32_t max_pages, int32_t pages);
+/* Workspace of pi_cache_fork and pi_cache_compact (0 if the cache is invalid). */
+size_t pi_cache_workspace_bytes(const pi_cache* cache);
+
+/* Room for counts[i] more tokens in slot seqs[i], i < n <= 4096: lens grows and
+ * new pages come from the stack, in the order of the list. */
+pi_status pi_cache_extend(const pi_cache* cache, const int32_t* seqs, const int32_t* counts, int32_t n, void* stream);
+
+/* The keys and values of one layer of tokens that a slot has room for: rows
+ * cu[i] .. cu[i + 1] - 1 of k and v become the LAST tokens of slot seqs[i].
+ * cu: [n + 1] ascending; rows outside cu[0] .. cu[n] - 1 are ignored. */
+pi_status pi_cache_append(const pi_cache* cache, int32_t layer, const pi_heads* k, const pi_heads* v, int32_t tokens,
+                          const int32_t* cu, const int32_t* seqs, int32_t n, void* stream);
+
+/* The empty slot children[i] becomes a copy of slot parents[i], i < n <= 4096
+ * (as the parents were before the call): whole pages are shared, a last page
+ * that is not full is copied, in every layer, into a page from the stack. */
+pi_status pi_cache_fork(const pi_cache* cache, const int32_t* parents, const int32_t* children, int32_t n, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* The listed slots become empty; pages that no slot uses any more are free. */
+pi_status pi_cache_release(const pi_cache* cache, const int32_t* seqs, int32_t n, void* stream);
+
+/* The pages in use move to places 0 .. used - 1 of the pool (pages already
+ * there stay; the others fill the gaps in ascending order), the tables follow,
+ * and the stack holds the rest, the lowest on top.  moved: [pages] or NULL,
+ * the new place of each page, -1 where it was not in use. */
+pi_status pi_cache_compact(const pi_cache* cache, int32_t* moved, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * pi_attn_prompt -- causal attention over packed sequences: rows
+ * cu[i] .. cu[i + 1] - 1 of q, k, v and out are sequence i < n, and
+ *   out_t = sum_{j <= t} p_tj v_j,  p_t = softmax_j(scale q_t . k_j)
+ * within it.  scale 0 = 1 / sqrt(dim); otherwise finite and positive
+ * (PI_EINVAL).  cu: [n + 1] int32, ascending, within 0 .. tokens; rows that no
+ * sequence holds are not written.  Keys a row does not see leave no trace in
+ * it, infinities and NaN included.
+ */
+pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v, const pi_heads* out, int32_t tokens,
+                         int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype, const int32_t* cu, int32_t n,
+                         float scale, void* stream);
+
+/*
+ * pi_attn_decode -- attention of one query row per batch row over the tokens
+ * its slot holds in one layer of the cache: slot seqs[b], or b where seqs is
+ * NULL (then batch <= slots).  A slot without tokens gives zeros.
+ * prefix: NULL, or one int32 on the device: how many leading pages all the
+ * batch's slots that are not empty have in common, page for page.  These are
+ * read once for the whole batch.  The pages of a slot that is too short to
+ * hold them do not count as common.
+ */
+size_t pi_attn_workspace_bytes(const pi_cache* cache, int32_t batch, int32_t heads);
+pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q, const pi_heads* out, int32_t batch,
+                         int32_t heads, const int32_t* seqs, const int32_t* prefix, float scale, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
+ * pi_matvec -- y_b = W x_b + bias for 1 <= batch <= 32 rows, W a Q4_0 matrix
+ * [rows][cols] (pi_mat, 16-byte aligned nibbles, 2-byte aligned scales),
+ * cols % 32 == 0, bias [rows] float32 or NULL.  x [batch][ldx] and
+ * y [batch][ldy] are PI_F32, PI_F16 or PI_BF16 each, aligned to their type,
+ * ldx >= cols and ldy >= rows (elements).  Products and sums carry float32's
+ * precision whatever the types are.
+ */
+size_t pi_matvec_workspace_bytes(int32_t rows, int32_t cols, int32_t batch);
+pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* bias, const void* x, int32_t x_dtype,
+                    int64_t ldx, void* y, int32_t y_dtype, int64_t ldy, int32_t batch, void* ws, size_t ws_bytes,
+                    void* stream);
 
 const char* pi_status_str(pi_status s);
 int32_t pi_abi_version(void);
