@@ -324,6 +324,12 @@ def _need(ok: bool, what: str):
         raise PiError(PI_EINVAL, what)
 
 
+def _gpu(what: str, *tensors):
+    """All tensors (None aside) lie on one GPU: a kernel cannot follow an address of the host's."""
+    dev = tensors[0].get_device()
+    _need(dev >= 0 and all(t is None or t.get_device() == dev for t in tensors), what)
+
+
 def _ints(t, n: Optional[int], what: str) -> Optional[int]:
     """Address of a contiguous int32 tensor of n elements (any number where n is None), or None for None."""
     import torch
@@ -335,11 +341,10 @@ def _ints(t, n: Optional[int], what: str) -> Optional[int]:
 
 def _heads(t, what: str) -> PiHeads:
     """A [tokens][heads][dim] tensor with strides; the last dimension contiguous."""
-    _need(t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] == 1), what)
+    shape, stride = t.shape, t.stride()
+    _need(len(shape) == 3 and (stride[2] == 1 or shape[2] == 1), what)
     # the stride of a dimension of one element says nothing
-    token = t.stride(0) if t.shape[0] > 1 else 0
-    head = t.stride(1) if t.shape[1] > 1 else 0
-    return PiHeads(t.data_ptr() or None, token, head)
+    return PiHeads(t.data_ptr() or None, stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
 
 
 class Cache:
@@ -361,6 +366,7 @@ class Cache:
         words = self.meta_words(slots, max_pages, pages)
         _need(words > 0 and meta.dtype == torch.int32 and meta.dim() == 1 and meta.is_contiguous()
               and meta.numel() == words, "Cache: meta")
+        _gpu("Cache: tensors of one GPU", k_pool, v_pool, meta)
         self.struct = PiCache(_p(k_pool), _p(v_pool), _p(meta), layers, pages, kv_heads, page, dim,
                               _dtype_of(k_pool), self.slots, self.max_pages)
         self._ref = ctypes.byref(self.struct)
@@ -395,6 +401,7 @@ class Cache:
     def extend(self, seqs, counts, stream=None):
         """Room for counts[i] more tokens in slot seqs[i]."""
         n = seqs.numel()
+        _gpu("extend: tensors of one GPU", self.meta, seqs, counts)
         _check(lib().pi_cache_extend(self._ref, _ints(seqs, n, "extend: seqs"), _ints(counts, n, "extend: counts"), n,
                                      _stream(stream)), "pi_cache_extend")
 
@@ -404,6 +411,7 @@ class Cache:
         _need(k.shape == v.shape and tuple(k.shape[1:]) == want and k.dtype == v.dtype == self.k_pool.dtype,
               "append: k, v")
         n = seqs.numel()
+        _gpu("append: tensors of one GPU", self.meta, k, v, cu, seqs)
         kh, vh = _heads(k, "append: k"), _heads(v, "append: v")
         _check(lib().pi_cache_append(self._ref, layer, ctypes.byref(kh), ctypes.byref(vh), k.shape[0],
                                      _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
@@ -412,17 +420,20 @@ class Cache:
     def fork(self, parents, children, stream=None):
         """The empty slot children[i] becomes a copy of slot parents[i]."""
         n = parents.numel()
+        _gpu("fork: tensors of one GPU", self.meta, parents, children)
         _check(lib().pi_cache_fork(self._ref, _ints(parents, n, "fork: parents"), _ints(children, n, "fork: children"),
                                    n, _p(self.ws), self.ws.numel(), _stream(stream)), "pi_cache_fork")
 
     def release(self, seqs, stream=None):
         """The listed slots become empty."""
         n = seqs.numel()
+        _gpu("release: tensors of one GPU", self.meta, seqs)
         _check(lib().pi_cache_release(self._ref, _ints(seqs, n, "release: seqs"), n, _stream(stream)),
                "pi_cache_release")
 
     def compact(self, moved=None, stream=None):
         """The pages in use move to the front of the pool; moved [pages]: the new place of each."""
+        _gpu("compact: tensors of one GPU", self.meta, moved)
         _check(lib().pi_cache_compact(self._ref, _ints(moved, self.pages, "compact: moved"), _p(self.ws),
                                       self.ws.numel(), _stream(stream)), "pi_cache_compact")
 
@@ -435,6 +446,8 @@ class Cache:
         if (batch, heads) not in self._attn_ws:
             n = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
             _need(n > 0, "attn_decode: batch, heads")
+            # memory taken while a graph is captured belongs to that graph
+            _need(not torch.cuda.is_current_stream_capturing(), "attn_decode: first call of these sizes inside a capture")
             self._attn_ws[batch, heads] = torch.empty(n, dtype=torch.uint8, device=self.k_pool.device)
         return self._attn_ws[batch, heads]
 
@@ -445,9 +458,12 @@ def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
     q, out: [tokens][heads][dim]; k, v: [tokens][kv_heads][dim]; scale 0: 1 / sqrt(dim)."""
     _need(q.shape == out.shape and k.shape == v.shape and q.dim() == k.dim() == 3 and q.shape[0] == k.shape[0]
           and q.shape[2] == k.shape[2] and q.dtype == k.dtype == v.dtype == out.dtype, "attn_prompt: q, k, v, out")
+    _need(cu.numel() > 1, "attn_prompt: cu")
     h = [_heads(t, "attn_prompt: strides") for t in (q, k, v, out)]
+    offsets = _ints(cu, None, "attn_prompt: cu")
+    _gpu("attn_prompt: tensors of one GPU", q, k, v, out, cu)
     _check(lib().pi_attn_prompt(*(ctypes.byref(x) for x in h), q.shape[0], q.shape[1], k.shape[1], q.shape[2],
-                                _dtype_of(q), _ints(cu, None, "attn_prompt: cu"), cu.numel() - 1, scale,
+                                _dtype_of(q), offsets, cu.numel() - 1, scale,
                                 _stream(stream)), "pi_attn_prompt")
 
 
@@ -458,6 +474,7 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
     leading pages the slots that are not empty have in common.  ws: as Cache.attn_workspace."""
     _need(q.shape == out.shape and q.dim() == 3 and q.shape[2] == cache.dim
           and q.dtype == out.dtype == cache.k_pool.dtype, "attn_decode: q, out")
+    _gpu("attn_decode: tensors of one GPU", cache.meta, q, out, prefix, seqs, ws)
     batch, heads = q.shape[:2]
     ws = cache.attn_workspace(batch, heads) if ws is None else ws
     hq, ho = _heads(q, "attn_decode: q"), _heads(out, "attn_decode: out")
@@ -480,10 +497,11 @@ class Q4Matrix:
               and tuple(scales.shape) == (self.rows, self.cols // 32), "Q4Matrix: scales")
         _need(bias is None or (bias.dtype == torch.float32 and bias.is_contiguous()
                                and tuple(bias.shape) == (self.rows,)), "Q4Matrix: bias")
-        self.nibbles, self.scales, self.bias = nibbles, scales, bias
-        self.struct = PiMat(_p(nibbles), _p(scales))
         n = int(lib().pi_matvec_workspace_bytes(self.rows, self.cols, self.batch))
         _need(n > 0, "Q4Matrix: rows, cols, batch")
+        _gpu("Q4Matrix: tensors of one GPU", nibbles, scales, bias)
+        self.nibbles, self.scales, self.bias = nibbles, scales, bias
+        self.struct = PiMat(_p(nibbles), _p(scales))
         self.ws = torch.empty(n, dtype=torch.uint8, device=nibbles.device)
 
     @classmethod
@@ -500,6 +518,7 @@ def matvec(mat: Q4Matrix, x, y, stream=None):
     """y[b] = W x[b] + bias; x [batch][cols], y [batch][rows], float32, float16 or bfloat16 each."""
     _need(x.dim() == y.dim() == 2 and x.shape[0] == y.shape[0] <= mat.batch and x.shape[1] == mat.cols
           and y.shape[1] == mat.rows and x.stride(1) == 1 and (y.stride(1) == 1 or mat.rows == 1), "matvec: x, y")
+    _gpu("matvec: tensors of one GPU", mat.nibbles, x, y)
     batch = x.shape[0]
     ldx, ldy = (x.stride(0), y.stride(0)) if batch > 1 else (mat.cols, mat.rows)
     _check(lib().pi_matvec(ctypes.byref(mat.struct), mat.rows, mat.cols, _p(mat.bias), _p(x), _dtype_of(x), ldx, _p(y),

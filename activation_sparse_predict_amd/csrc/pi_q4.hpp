@@ -59,10 +59,10 @@ __device__ __forceinline__ u4 q4_unpack(uint32_t w) {
   return r;
 }
 
-// The power of two that brings a row with largest value `big` into [2^14, 2^15): 1 for zero, infinities and NaN.
+// The power of two that brings a row with largest finite value `big` into [2^14, 2^15): 1 for zero.
 __device__ __forceinline__ float row_scale(float big) {
   const int e = (int)(__float_as_uint(big) >> 23) & 255;
-  if (e == 255 || big == 0.f) return 1.f;
+  if (big == 0.f) return 1.f;
   return __uint_as_float((uint32_t)min(max(127 + 14 - (e - 127), 1), 254) << 23);
 }
 
@@ -77,13 +77,10 @@ k_mv_operand(const void* __restrict__ x, int64_t ldx, int batch, int cols, int t
   float s = 1.f;
   if (b < batch) {
     float big = 0.f;
-    bool odd = false;                              // NaN, which no maximum shows
     for (int k = tid; k < cols; k += 256) {
       const float v = fabsf(x_at<X>(x, b * ldx + k));
-      odd |= v != v;
-      big = fmaxf(big, v);
+      if (v < __builtin_inff()) big = fmaxf(big, v);   // infinities and NaN are what they are at any scale
     }
-    if (odd) big = __builtin_inff();
     for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
     if ((tid & 63) == 0) part[tid >> 6] = big;
     __syncthreads();
