@@ -36,6 +36,7 @@ constexpr float NEG_INF = -__builtin_inff();
 constexpr int PT_WAVES = 4;              // waves of a block
 constexpr int PT_Q = 32 * PT_WAVES;      // query rows of a block
 constexpr int PT_K = 64;                 // keys of a tile
+constexpr float RISE = 8.f;              // powers of two that a p_j may grow to before the sums are multiplied
 
 // LDS rows of a tile: a power of two of 16-byte chunks, so that a row starts on
 // a fixed bank, and chunk c of row r lies at position c ^ swz(r).  The 32 rows
@@ -80,21 +81,191 @@ __device__ __forceinline__ Place find_tile(const int32_t* cu, int n, int tokens,
   return Place{0, 0, 0};
 }
 
-// One block: 128 query rows of one sequence and head, 32 for each wave, over
-// the keys up to the last row in tiles of 64 from the last one down.  A wave's
-// rows lie in one 64-aligned span, so exactly the first tile it computes is
-// partly masked.
+// 16 bytes per lane from memory into LDS, past the registers: lane i of the wave to dst + 16 i.
+__device__ __forceinline__ void to_lds(const uint16_t* src, u4* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// Byte offsets of a lane's operand reads inside a tile in LDS.  The swizzle takes its bits from the lane alone, so
+// the remaining row numbers are multiples of 16 rows that go into the instructions' offsets.
+template <int D> struct Reads {
+  using L = Tile<D>;
+  static constexpr int VT = L::NC == 8 ? 2 : L::NC == 16 ? 4 : 8;   // 64-byte columns of a row
+  uint32_t k[L::KS], v[2][VT];
+
+  __device__ __forceinline__ explicit Reads(int lane) {
+    const int hi = lane >> 5, col = lane & 31;
+#pragma unroll
+    for (int s = 0; s < L::KS; ++s) k[s] = 16 * L::chunk(col, 2 * s + hi);
+    const int j = lane & 15, cc = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int t = 0; t < L::DT; ++t) v[e][t] = 16 * L::chunk(8 * e + 4 * hi + (j >> 2), 4 * t + cc) + 8 * (j & 1);
+  }
+  // K as A operand: keys 32 h .., dims 16 s ..
+  __device__ __forceinline__ u4 kfrag(const u4* sk, int h, int s) const {
+    return *reinterpret_cast<const u4*>(reinterpret_cast<const char*>(sk) + k[s] + 32 * 16 * L::NC * h);
+  }
+  // V^T as A operand, keys 16 step .., dims 32 t ..: transposing reads, each giving a lane 4 keys of one dimension
+  __device__ __forceinline__ u4 vfrag(const u4* sv, int step, int t) const {
+    u4 f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const char* at = reinterpret_cast<const char*>(sv) + v[e][t] + 16 * 16 * L::NC * step;
+      const u2 x =
+          __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at));
+      f[2 * e] = x[0];
+      f[2 * e + 1] = x[1];
+    }
+    return f;
+  }
+};
+
+// A wave's sums for 32 queries: o, l, and mc, the reference point of the exponents (c times a score, or -inf).
+template <class T, int D> struct Sums {
+  using L = Tile<D>;
+  f16v o[L::DT];
+  float mc, l;
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < L::DT; ++t) o[t] = (f16v)(0.f);
+    mc = NEG_INF, l = 0.f;
+  }
+
+  // Scores of one tile of 64 keys in LDS: register i of s[h] is key 32 h + 8 (i / 4) + 4 (lane / 32) + i % 4.
+  static __device__ __forceinline__ void scores(const u4* sk, const u4* qf, const Reads<D>& rd, f16v* s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[h] = (f16v)(0.f);
+#pragma unroll
+      for (int ks = 0; ks < L::KS; ++ks) s[h] = T::mma32(rd.kfrag(sk, h, ks), qf[ks], s[h]);
+    }
+  }
+
+  // The weights of a tile's scores, rounded, and their part of l.
+  __device__ __forceinline__ void weigh(const f16v* s, float c, uint32_t* pw) {
+    // rows whose scores so far are all -inf keep mc = -inf; 0 stands in for it in the differences
+    const float base = mc == NEG_INF ? 0.f : mc;
+    float x[32], top = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = fmaf(s[i / 16][i % 16], c, -base);
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
+    top = max32(top);
+    // mc may lag behind the largest score: p stays below 2^RISE, and o is seldom multiplied
+    if (__ballot(top > RISE || mc == NEG_INF)) {
+      const bool none = mc == NEG_INF;
+      const float up = none ? (top == NEG_INF ? 0.f : top) : fmaxf(top, 0.f), alpha = exp2_fast(-up);
+      mc = none && top == NEG_INF ? NEG_INF : base + up;
+      if (!none) {                                 // else o and l are zero
+        l *= alpha;
+#pragma unroll
+        for (int t = 0; t < L::DT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] -= up;
+    }
+    float ls = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float a = exp2_fast(x[i]), b = exp2_fast(x[i + 1]);
+      ls += a;
+      ls += b;
+      pw[i / 2] = T::pack(a, b);
+    }
+    l += ls;
+  }
+
+  __device__ __forceinline__ void add(const u4* sv, const uint32_t* pw, const Reads<D>& rd) {
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+      const u4 pf = {pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]};
+#pragma unroll
+      for (int t = 0; t < L::DT; ++t) o[t] = T::mma32(rd.vfrag(sv, st, t), pf, o[t]);
+    }
+  }
+
+  // A tile that every row sees whole.
+  __device__ __forceinline__ void next(const u4* sk, const u4* sv, const u4* qf, float c, const Reads<D>& rd) {
+    f16v s[2];
+    scores(sk, qf, rd, s);
+    uint32_t pw[16];
+    weigh(s, c, pw);
+    add(sv, pw, rd);
+  }
+
+  // A tile of which a row sees only the first `seen` keys, as the wave's first (o holds nothing yet).
+  __device__ __forceinline__ void first(const u4* sk, const u4* sv, const u4* qf, float c, int seen,
+                                        const Reads<D>& rd) {
+    const int hi = (threadIdx.x & 63) >> 5;
+    f16v s[2];
+    scores(sk, qf, rd, s);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (32 * h + 8 * (i / 4) + 4 * hi + i % 4 >= seen) s[h][i] = NEG_INF;
+    uint32_t pw[16];
+    weigh(s, c, pw);
+    add(sv, pw, rd);
+    // 0 times an infinity or NaN of a key that is not seen is NaN: where any value came out non-finite the tile's sum
+    // is taken again key by key, adding only to the rows that see the key
+    float bad = 0.f;
+#pragma unroll
+    for (int t = 0; t < L::DT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) bad = fmaf(o[t][i], 0.f, bad);
+    if (!__ballot(bad != bad)) return;
+#pragma unroll
+    for (int t = 0; t < L::DT; ++t) {
+      o[t] = (f16v)(0.f);
+#pragma unroll
+      for (int st = 0; st < 4; ++st) {
+        const u4 vf = rd.vfrag(sv, st, t);
+#pragma unroll 1
+        for (int y = 0; y < 16; ++y) {             // key 16 st + y: element e of the lanes of half y / 4 % 2
+          const int e = (y & 3) + 4 * (y >> 3);
+          const bool mine = ((y >> 2) & 1) == hi;
+          u4 va, pa;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t keep = mine && x == e / 2 ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+            va[x] = vf[x] & keep;
+            pa[x] = pw[4 * st + x] & keep;
+          }
+          const f16v one = T::mma32(va, pa, (f16v)(0.f));
+          if (16 * st + y < seen)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[t][i] += one[i];
+        }
+      }
+    }
+  }
+};
+
+// One block: 32 query rows of one sequence and head for each wave, over the
+// keys up to the last row in tiles of 64 from the last one down.  A wave's rows
+// lie in one 64-aligned span, so exactly the first tile it computes is partly
+// masked.  K and V tiles go to LDS past the registers, one tile ahead of the
+// products, into two buffers (separate arrays, so that a read of one does not
+// wait for the loads into the other).
 template <class T, int D>
-__global__ void __launch_bounds__(PT_WAVES * WAVE)
+__global__ void __launch_bounds__(PT_WAVES * WAVE, 2)
 k_attn_prompt(Rows q, Rows k, Rows v, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head,
               const int32_t* __restrict__ cu, int n, int tokens, int heads, int group, int dim, float c) {
   using L = Tile<D>;
   constexpr int NT = PT_WAVES * WAVE;
   constexpr int LD = PT_K * L::NC / NT;            // chunks of a tile per thread
-  __shared__ u4 sk[PT_K * L::NC];
-  __shared__ u4 sv[PT_K * L::NC];
+  __shared__ u4 sk0[PT_K * L::NC], sk1[PT_K * L::NC], sv0[PT_K * L::NC], sv1[PT_K * L::NC];
 
-  const int head = blockIdx.x % heads;
+  // neighbouring heads, which may share keys, run on the same die (block b runs on die b % 8)
+  int head = blockIdx.x % heads;
+  if (heads % 8 == 0) head = (head % 8) * (heads / 8) + head / 8;
   const Place pl = find_tile(cu, n, tokens, blockIdx.x / heads);
   if (pl.len == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -113,138 +284,72 @@ k_attn_prompt(Rows q, Rows k, Rows v, uint16_t* __restrict__ out, int64_t out_to
       qf[s] = ch < nchunk ? *reinterpret_cast<const u4*>(src + 8 * ch) : u4{0, 0, 0, 0};
     }
   }
-  f16v o[L::DT];
-#pragma unroll
-  for (int t = 0; t < L::DT; ++t) o[t] = (f16v)(0.f);
-  float m = NEG_INF, l = 0.f;
-
+  if (nchunk < L::NC) {                            // chunks that no load fills
+    for (int e = tid; e < PT_K * L::NC; e += NT) sk0[e] = sk1[e] = sv0[e] = sv1[e] = u4{0, 0, 0, 0};
+    __syncthreads();
+  }
+  Sums<T, D> sum;
+  sum.clear();
   const int kv = head / group;
   const int key_end = min(pl.len, (pl.tile + 1) * PT_Q);
   const int my_tile = (row0 + 31) / PT_K;          // the wave's last (masked) tile
-  for (int kt = (key_end - 1) / PT_K; kt >= 0; --kt) {
-    __syncthreads();                               // the tile before this one has been read
+  auto load = [&](int kt, u4* dk, u4* dv) {
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const int e = i * NT + tid, r = e / L::NC, ch = e % L::NC;
+      const int e = i * NT + tid, r = e / L::NC, ch = (e % L::NC) ^ L::swz(r);
       const int64_t tok = pl.start + min(kt * PT_K + r, pl.len - 1);
-      u4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
       if (ch < nchunk) {
-        a = *reinterpret_cast<const u4*>(k.at(tok, kv) + 8 * ch);
-        b = *reinterpret_cast<const u4*>(v.at(tok, kv) + 8 * ch);
+        to_lds(k.at(tok, kv) + 8 * ch, dk + i * NT + 64 * w);
+        to_lds(v.at(tok, kv) + 8 * ch, dv + i * NT + 64 * w);
       }
-      sk[L::chunk(r, ch)] = a;
-      sv[L::chunk(r, ch)] = b;
     }
+  };
+  int kt = (key_end - 1) / PT_K;
+  if (kt & 1) load(kt, sk1, sv1);
+  else load(kt, sk0, sv0);
+  // Tiles with an even number lie in the first buffer.  Every wave passes the same barriers, one a tile: those before
+  // its masked tile, the masked one, and the rest.
+  const Reads<D> rd(lane);
+  auto arrive = [&](u4* nk, u4* nv) {              // tile kt has come, and tile kt + 1 has been read
     __syncthreads();
-    if (kt > my_tile) continue;                    // every key lies behind the wave's rows
-
-    // S^T: two tiles of 32 keys
-    f16v s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s[h] = (f16v)(0.f);
-#pragma unroll
-      for (int ks = 0; ks < L::KS; ++ks)
-        s[h] = T::mma32(sk[L::chunk(32 * h + col, 2 * ks + hi)], qf[ks], s[h]);
-    }
-    const bool masked = kt == my_tile;
-    if (masked) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = kt * PT_K + 32 * h + 8 * (i / 4) + 4 * hi + i % 4;
-          if (key > row) s[h][i] = NEG_INF;
-        }
-    }
-    float mt = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-    for (int i = 1; i < 16; ++i) mt = fmaxf(mt, fmaxf(s[0][i], s[1][i]));
-    const float mn = fmaxf(m, max32(mt));
-    // rows whose scores so far are all -inf keep m = -inf; 0 stands in for it in the differences
-    const float mc = mn == NEG_INF ? 0.f : mn * c;
-    const float alpha = exp2_fast(fmaf(m, c, -mc));
-    m = mn;
-    uint32_t pw[16];
-    float ls = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float a = exp2_fast(fmaf(s[h][i], c, -mc)), b = exp2_fast(fmaf(s[h][i + 1], c, -mc));
-        ls += a + b;
-        pw[8 * h + i / 2] = T::pack(a, b);
-      }
-    l = fmaf(l, alpha, ls);
-#pragma unroll
-    for (int t = 0; t < L::DT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
-    // V^T as A operand: transposing LDS reads, each giving a lane 4 keys of one output dimension
-    auto vfrag = [&](int step, int t) {            // keys 16 step.., dims 32 t..
-      const int j = lane & 15, cc = 4 * t + 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
-      u4 f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 16 * step + 8 * e + 4 * hi + (j >> 2);
-        const char* at = reinterpret_cast<const char*>(&sv[L::chunk(r, cc)]) + 8 * (j & 1);
-        const u2 x = __builtin_bit_cast(
-            u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at));
-        f[2 * e] = x[0];
-        f[2 * e + 1] = x[1];
-      }
-      return f;
-    };
-#pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      const u4 pf = {pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]};
-#pragma unroll
-      for (int t = 0; t < L::DT; ++t) o[t] = T::mma32(vfrag(st, t), pf, o[t]);
-    }
-    if (masked) {
-      // 0 times an infinity or NaN of a masked key is NaN.  This is the wave's first tile
-      // (o held nothing before it), so where any value came out non-finite the tile's sum
-      // is taken again key by key, adding only to the rows that see the key.
-      float bad = 0.f;
-#pragma unroll
-      for (int t = 0; t < L::DT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) bad = fmaf(o[t][i], 0.f, bad);
-      if (__ballot(bad != bad)) {
-#pragma unroll
-        for (int t = 0; t < L::DT; ++t) {
-          o[t] = (f16v)(0.f);
-          for (int key = 0; key < PT_K; ++key) {
-            const int st = key >> 4, e = (key & 3) + 4 * ((key >> 3) & 1);
-            const bool mine = ((key >> 2) & 1) == hi;
-            const u4 vf = vfrag(st, t);
-            u4 va, pa;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t keep = mine && x == e / 2 ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
-              va[x] = vf[x] & keep;
-              pa[x] = (st == 0 ? pw[x] : st == 1 ? pw[4 + x] : st == 2 ? pw[8 + x] : pw[12 + x]) & keep;
-            }
-            const f16v one = T::mma32(va, pa, (f16v)(0.f));
-            if (kt * PT_K + key <= row)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[t][i] += one[i];
-          }
-        }
-      }
-    }
+    if (kt > 0) load(kt - 1, nk, nv);
+  };
+  for (; kt > my_tile; --kt) {
+    if (kt & 1) arrive(sk0, sv0);
+    else arrive(sk1, sv1);
+  }
+  const int seen = row - kt * PT_K + 1;
+  if (kt & 1) {
+    arrive(sk0, sv0);
+    sum.first(sk1, sv1, qf, c, seen, rd);
+    --kt;
+  }
+  if (kt >= 0) {
+    arrive(sk1, sv1);
+    if (kt == my_tile) sum.first(sk0, sv0, qf, c, seen, rd);
+    else sum.next(sk0, sv0, qf, c, rd);
+    --kt;
+  }
+  while (kt >= 0) {
+    arrive(sk0, sv0);
+    sum.next(sk1, sv1, qf, c, rd);
+    --kt;
+    arrive(sk1, sv1);
+    sum.next(sk0, sv0, qf, c, rd);
+    --kt;
   }
   if (row0 >= pl.len) return;
-  l = sum32(l);
+  const float l = sum32(sum.l);
   const float inv = l == 0.f ? 0.f : 1.f / l;      // no weight at all (every score -inf): zero
   uint16_t* dst = out + (pl.start + row) * out_token + head * out_head;
 #pragma unroll
   for (int t = 0; t < L::DT; ++t)
 #pragma unroll
     for (int g = 0; g < 2; ++g) {                  // 16 dims: the lane halves trade so that each stores 8
+      const f16v& o = sum.o[t];
       const int i = 8 * g;
-      const uint32_t a0 = T::pack(o[t][i] * inv, o[t][i + 1] * inv), a1 = T::pack(o[t][i + 2] * inv, o[t][i + 3] * inv);
-      const uint32_t b0 = T::pack(o[t][i + 4] * inv, o[t][i + 5] * inv), b1 = T::pack(o[t][i + 6] * inv, o[t][i + 7] * inv);
+      const uint32_t a0 = T::pack(o[i] * inv, o[i + 1] * inv), a1 = T::pack(o[i + 2] * inv, o[i + 3] * inv);
+      const uint32_t b0 = T::pack(o[i + 4] * inv, o[i + 5] * inv), b1 = T::pack(o[i + 6] * inv, o[i + 7] * inv);
       const auto r0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
       const auto r1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
       const int ch = 4 * t + 2 * g + hi;
