@@ -87,16 +87,27 @@ pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v
     if ((s = check_heads(h, tokens)) != PI_OK) return s;
   float c;
   if (!scale_of(scale, dim, &c)) return PI_EINVAL;
+  for (const pi_heads* h : {k, v})                 // byte offsets inside a tile are 32-bit
+    if (h->token_stride < 0 || h->token_stride > (1 << 24)) return PI_EUNSUPPORTED;
   if (tokens == 0) return PI_OK;
+  // heads of a block: as many of those that share their keys as 4 waves take
+  const int group = heads / kv_heads;
+  const int hg = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1, rows = 128 / hg;
   // a tile of each sequence may be short
-  const int64_t blocks = (up_div(tokens, pia::PT_Q) + std::min(n, tokens)) * heads;
+  const int64_t blocks = (up_div(tokens, rows) + std::min(n, tokens)) * (heads / hg);
   if (blocks > INT32_MAX) return PI_EUNSUPPORTED;
   (void)hipGetLastError();
   with_type(dtype, dim, [&](auto t, auto d) {
-    hipLaunchKernelGGL((pia::k_attn_prompt<decltype(t), decltype(d)::value>), dim3((unsigned)blocks),
-                       dim3(pia::PT_WAVES * pia::WAVE), 0, static_cast<hipStream_t>(stream), rows_of(q), rows_of(k),
-                       rows_of(v), static_cast<uint16_t*>(out->p), out->token_stride, out->head_stride, cu, n, tokens,
-                       heads, heads / kv_heads, dim, c);
+    using T = decltype(t);
+    constexpr int D = decltype(d)::value;
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), rows_of(q),
+                         rows_of(k), rows_of(v), static_cast<uint16_t*>(out->p), out->token_stride, out->head_stride,
+                         cu, n, tokens, heads, group, dim, c);
+    };
+    if (hg == 4) go(pia::k_attn_prompt<T, D, 4>);
+    else if (hg == 2) go(pia::k_attn_prompt<T, D, 2>);
+    else go(pia::k_attn_prompt<T, D, 1>);
   });
   return launched();
 }

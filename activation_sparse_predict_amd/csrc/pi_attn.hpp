@@ -33,8 +33,6 @@ struct Rows {
 constexpr float NEG_INF = -__builtin_inff();
 
 // ------------------------------------------------------- attention over prompts
-constexpr int PT_WAVES = 4;              // waves of a block
-constexpr int PT_Q = 32 * PT_WAVES;      // query rows of a block
 constexpr int PT_K = 64;                 // keys of a tile
 constexpr float RISE = 8.f;              // powers of two that a p_j may grow to before the sums are multiplied
 
@@ -58,6 +56,7 @@ template <int D> struct Tile {
 struct Place {
   int start, len, tile;                  // first token, tokens, tile; len = 0: nothing to do
 };
+template <int ROWS>
 __device__ __forceinline__ Place find_tile(const int32_t* cu, int n, int tokens, int idx) {
   const int lane = threadIdx.x & (WAVE - 1);
   for (int base = 0; base < n; base += WAVE) {
@@ -67,7 +66,7 @@ __device__ __forceinline__ Place find_tile(const int32_t* cu, int n, int tokens,
       a = min(max(cu[i], 0), tokens);
       b = min(max(cu[i + 1], a), tokens);
     }
-    const int t = (b - a + PT_Q - 1) / PT_Q;
+    const int t = (b - a + ROWS - 1) / ROWS;
     const int upto = scan64(t);
     const uint64_t hit = __ballot(upto > idx);
     if (hit) {
@@ -81,18 +80,24 @@ __device__ __forceinline__ Place find_tile(const int32_t* cu, int n, int tokens,
   return Place{0, 0, 0};
 }
 
-// 16 bytes per lane from memory into LDS, past the registers: lane i of the wave to dst + 16 i.
-__device__ __forceinline__ void to_lds(const uint16_t* src, u4* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// 16 bytes per lane from memory (base plus the lane's byte offset) into LDS, past the registers: lane i's go to
+// byte lds + 16 i.  Written out because the compiler, which cannot tell buffers of one array apart, would wait for
+// every such load before any read of LDS; `Ring` counts and waits for them.
+__device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+
+// All but the wave's last N loads have come, its LDS reads are done, and so for every wave of the block.
+template <int N> __device__ __forceinline__ void arrive() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // Byte offsets of a lane's operand reads inside a tile in LDS.  The swizzle takes its bits from the lane alone, so
 // the remaining row numbers are multiples of 16 rows that go into the instructions' offsets.
 template <int D> struct Reads {
   using L = Tile<D>;
-  static constexpr int VT = L::NC == 8 ? 2 : L::NC == 16 ? 4 : 8;   // 64-byte columns of a row
-  uint32_t k[L::KS], v[2][VT];
+  uint32_t k[L::KS], v[2][L::DT];
 
   __device__ __forceinline__ explicit Reads(int lane) {
     const int hi = lane >> 5, col = lane & 31;
@@ -105,15 +110,15 @@ template <int D> struct Reads {
       for (int t = 0; t < L::DT; ++t) v[e][t] = 16 * L::chunk(8 * e + 4 * hi + (j >> 2), 4 * t + cc) + 8 * (j & 1);
   }
   // K as A operand: keys 32 h .., dims 16 s ..
-  __device__ __forceinline__ u4 kfrag(const u4* sk, int h, int s) const {
-    return *reinterpret_cast<const u4*>(reinterpret_cast<const char*>(sk) + k[s] + 32 * 16 * L::NC * h);
+  __device__ __forceinline__ u4 kfrag(const char* sk, int h, int s) const {
+    return *reinterpret_cast<const u4*>(sk + k[s] + 32 * 16 * L::NC * h);
   }
   // V^T as A operand, keys 16 step .., dims 32 t ..: transposing reads, each giving a lane 4 keys of one dimension
-  __device__ __forceinline__ u4 vfrag(const u4* sv, int step, int t) const {
+  __device__ __forceinline__ u4 vfrag(const char* sv, int step, int t) const {
     u4 f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const char* at = reinterpret_cast<const char*>(sv) + v[e][t] + 16 * 16 * L::NC * step;
+      const char* at = sv + v[e][t] + 16 * 16 * L::NC * step;
       const u2 x =
           __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at));
       f[2 * e] = x[0];
@@ -123,7 +128,16 @@ template <int D> struct Reads {
   }
 };
 
-// A wave's sums for 32 queries: o, l, and mc, the reference point of the exponents (c times a score, or -inf).
+// Tiles of K and V in LDS, S of each; tile j lies in place j % S.  NT threads fill them.
+template <int D, int S, int NT> struct Ring {
+  using L = Tile<D>;
+  static constexpr int BYTES = PT_K * L::NC * 16;               // of a tile
+  static constexpr int LD = PT_K * L::NC / NT;                  // loads of a thread for a tile
+  static constexpr int RN = NT / L::NC;                         // rows that the block loads at once
+  static constexpr int NV = RN < 16 ? 16 / RN : 1;              // such loads until the swizzle repeats
+};
+
+// A wave's sums for 32 queries: o, l, and the reference point mc of the exponents (c times a score, or -inf).
 template <class T, int D> struct Sums {
   using L = Tile<D>;
   f16v o[L::DT];
@@ -136,13 +150,23 @@ template <class T, int D> struct Sums {
   }
 
   // Scores of one tile of 64 keys in LDS: register i of s[h] is key 32 h + 8 (i / 4) + 4 (lane / 32) + i % 4.
-  static __device__ __forceinline__ void scores(const u4* sk, const u4* qf, const Reads<D>& rd, f16v* s) {
+  static __device__ __forceinline__ void scores(const char* sk, const u4* qf, const Reads<D>& rd, f16v* s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       s[h] = (f16v)(0.f);
 #pragma unroll
       for (int ks = 0; ks < L::KS; ++ks) s[h] = T::mma32(rd.kfrag(sk, h, ks), qf[ks], s[h]);
     }
+  }
+
+  // Of a tile's scores, those of keys that a row does not see: it sees the first `seen`.
+  static __device__ __forceinline__ void mask(f16v* s, int seen) {
+    const int hi = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (32 * h + 8 * (i / 4) + 4 * hi + i % 4 >= seen) s[h][i] = NEG_INF;
   }
 
   // The weights of a tile's scores, rounded, and their part of l.
@@ -158,15 +182,15 @@ template <class T, int D> struct Sums {
     // mc may lag behind the largest score: p stays below 2^RISE, and o is seldom multiplied
     if (__ballot(top > RISE || mc == NEG_INF)) {
       const bool none = mc == NEG_INF;
-      const float up = none ? (top == NEG_INF ? 0.f : top) : fmaxf(top, 0.f), alpha = exp2_fast(-up);
-      mc = none && top == NEG_INF ? NEG_INF : base + up;
-      if (!none) {                                 // else o and l are zero
-        l *= alpha;
+      const float up = none ? (top == NEG_INF ? 0.f : top) : fmaxf(top, 0.f);
+      // where there was no score yet o and l are zero, whatever they are multiplied by
+      const float alpha = none ? 1.f : exp2_fast(-up);
+      mc = none ? top : mc + up;
+      l *= alpha;
 #pragma unroll
-        for (int t = 0; t < L::DT; ++t)
+      for (int t = 0; t < L::DT; ++t)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
-      }
+        for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] -= up;
     }
@@ -181,40 +205,19 @@ template <class T, int D> struct Sums {
     l += ls;
   }
 
-  __device__ __forceinline__ void add(const u4* sv, const uint32_t* pw, const Reads<D>& rd) {
+  __device__ __forceinline__ void add(const char* sv, const uint32_t* pw, const Reads<D>& rd) {
 #pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      const u4 pf = {pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]};
+    for (int st = 0; st < 4; ++st)
 #pragma unroll
-      for (int t = 0; t < L::DT; ++t) o[t] = T::mma32(rd.vfrag(sv, st, t), pf, o[t]);
-    }
+      for (int t = 0; t < L::DT; ++t)
+        o[t] = T::mma32(rd.vfrag(sv, st, t), u4{pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]}, o[t]);
   }
 
-  // A tile that every row sees whole.
-  __device__ __forceinline__ void next(const u4* sk, const u4* sv, const u4* qf, float c, const Reads<D>& rd) {
-    f16v s[2];
-    scores(sk, qf, rd, s);
-    uint32_t pw[16];
-    weigh(s, c, pw);
-    add(sv, pw, rd);
-  }
-
-  // A tile of which a row sees only the first `seen` keys, as the wave's first (o holds nothing yet).
-  __device__ __forceinline__ void first(const u4* sk, const u4* sv, const u4* qf, float c, int seen,
-                                        const Reads<D>& rd) {
+  // After the wave's first tile was added, of which a row saw the first `seen` keys: 0 times an infinity or NaN of a
+  // key that is not seen is NaN.  Where any value came out non-finite the tile's sum is taken again key by key, adding
+  // only to the rows that see the key (o held nothing before).
+  __device__ __forceinline__ void mend(const char* sv, const uint32_t* pw, int seen, const Reads<D>& rd) {
     const int hi = (threadIdx.x & 63) >> 5;
-    f16v s[2];
-    scores(sk, qf, rd, s);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (32 * h + 8 * (i / 4) + 4 * hi + i % 4 >= seen) s[h][i] = NEG_INF;
-    uint32_t pw[16];
-    weigh(s, c, pw);
-    add(sv, pw, rd);
-    // 0 times an infinity or NaN of a key that is not seen is NaN: where any value came out non-finite the tile's sum
-    // is taken again key by key, adding only to the rows that see the key
     float bad = 0.f;
 #pragma unroll
     for (int t = 0; t < L::DT; ++t)
@@ -233,10 +236,10 @@ template <class T, int D> struct Sums {
           const bool mine = ((y >> 2) & 1) == hi;
           u4 va, pa;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t keep = mine && x == e / 2 ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
-            va[x] = vf[x] & keep;
-            pa[x] = pw[4 * st + x] & keep;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t keep = mine && i == e / 2 ? (e & 1 ? 0xffff0000u : 0xffffu) : 0u;
+            va[i] = vf[i] & keep;
+            pa[i] = pw[4 * st + i] & keep;
           }
           const f16v one = T::mma32(va, pa, (f16v)(0.f));
           if (16 * st + y < seen)
@@ -246,115 +249,130 @@ template <class T, int D> struct Sums {
       }
     }
   }
+
+  // The rows' results: rows of `out` from `dst` on for the lane's query, where `live`.
+  __device__ __forceinline__ void store(uint16_t* dst, bool live, int nchunk) const {
+    const int hi = (threadIdx.x & 63) >> 5;
+    const float total = sum32(l);
+    const float inv = total == 0.f ? 0.f : 1.f / total;   // no weight at all (every score -inf): zero
+#pragma unroll
+    for (int t = 0; t < L::DT; ++t)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {                // 16 dims: the lane halves trade so that each stores 8
+        const int i = 8 * g;
+        const uint32_t a0 = T::pack(o[t][i] * inv, o[t][i + 1] * inv);
+        const uint32_t a1 = T::pack(o[t][i + 2] * inv, o[t][i + 3] * inv);
+        const uint32_t b0 = T::pack(o[t][i + 4] * inv, o[t][i + 5] * inv);
+        const uint32_t b1 = T::pack(o[t][i + 6] * inv, o[t][i + 7] * inv);
+        const auto s0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+        const int at = 4 * t + 2 * g + hi;
+        if (live && at < nchunk) *reinterpret_cast<u4*>(dst + 8 * at) = u4{s0[0], s1[0], s0[1], s1[1]};
+      }
+  }
 };
 
-// One block: 32 query rows of one sequence and head for each wave, over the
-// keys up to the last row in tiles of 64 from the last one down.  A wave's rows
-// lie in one 64-aligned span, so exactly the first tile it computes is partly
-// masked.  K and V tiles go to LDS past the registers, one tile ahead of the
-// products, into two buffers (separate arrays, so that a read of one does not
-// wait for the loads into the other).
-template <class T, int D>
-__global__ void __launch_bounds__(PT_WAVES * WAVE, 2)
+// One block of 4 waves: 32 query rows for each, of HG heads that share their
+// keys and 128 / HG tokens of one sequence, over the keys up to the last row in
+// tiles of 64 from the last one down.  A wave's rows lie in one 64-aligned span,
+// so exactly the first tile it computes is partly masked.  K and V tiles go to
+// LDS past the registers, one tile ahead of the products.
+//
+// At 8192 tokens and 56 heads of 128 the matrix cores are busy for half of the
+// cycles and the card lowers its clock from 2.3 to 1.9 GHz (zeros in place of
+// random data take 803 us, not 985): tiles three ahead, 8 waves a block, the
+// products of one tile interleaved with the exponentials of another or in
+// phases of their own, and other wave priorities all took as long or longer.
+// Packing the heads of a key head into a block: 188 -> 169 us for 13 prompts of
+// 6151 tokens, 128 heads on 8, 64 wide; four blocks a CU there: 164 us.
+template <class T, int D, int HG>
+__global__ void __launch_bounds__(4 * WAVE, D <= 64 ? 4 : D <= 128 ? 2 : 1)
 k_attn_prompt(Rows q, Rows k, Rows v, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head,
               const int32_t* __restrict__ cu, int n, int tokens, int heads, int group, int dim, float c) {
   using L = Tile<D>;
-  constexpr int NT = PT_WAVES * WAVE;
-  constexpr int LD = PT_K * L::NC / NT;            // chunks of a tile per thread
-  __shared__ u4 sk0[PT_K * L::NC], sk1[PT_K * L::NC], sv0[PT_K * L::NC], sv1[PT_K * L::NC];
+  constexpr int NT = 4 * WAVE, ROWS = 128 / HG, S = 2;
+  using R = Ring<D, S, NT>;
+  __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES];   // K tiles, then V tiles
 
-  // neighbouring heads, which may share keys, run on the same die (block b runs on die b % 8)
-  int head = blockIdx.x % heads;
-  if (heads % 8 == 0) head = (head % 8) * (heads / 8) + head / 8;
-  const Place pl = find_tile(cu, n, tokens, blockIdx.x / heads);
+  const int sets = heads / HG;
+  int set = blockIdx.x % sets;
+  // neighbouring sets of heads, which may share keys too, run on the same die (block b runs on die b % 8)
+  if (sets % 8 == 0) set = (set % 8) * (sets / 8) + set / 8;
+  const Place pl = find_tile<ROWS>(cu, n, tokens, blockIdx.x / sets);
   if (pl.len == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int hi = lane >> 5, col = lane & 31;
-  const int row0 = pl.tile * PT_Q + 32 * w;        // the wave's first row in the sequence
-  const int row = row0 + col;
+  const int head = set * HG + w % HG;
+  const int row0 = ROWS * pl.tile + 32 * (w / HG);  // the wave's first row in the sequence
+  const int row = row0 + (lane & 31), hi = lane >> 5;
   const int nchunk = dim / 8;
-
-  // Q^T as B operand, in registers for the whole block
+  if (nchunk < L::NC) {
+    for (int e = tid; e < 2 * S * R::BYTES / 16; e += NT) reinterpret_cast<u4*>(ring)[e] = u4{0, 0, 0, 0};
+    __syncthreads();
+  }
+  // A tile's rows into LDS, RN of them at once.  A chunk's place there follows from its thread; what it holds, from the
+  // swizzle, which repeats after 16 rows.  Only a sequence's last tile can be short: its missing rows repeat the last.
+  const int kv = head / group, r0 = tid / L::NC;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * w;
+  int ch[R::NV];
+#pragma unroll
+  for (int i = 0; i < R::NV; ++i) ch[i] = (tid % L::NC) ^ L::swz(r0 + i * R::RN);
+  auto load = [&](const Rows& x, int tile, uint32_t lds) {
+    const uint16_t* base = x.at(pl.start + (int64_t)tile * PT_K, kv);
+    const int left = pl.len - tile * PT_K;
+    const uint32_t stride = 2 * (uint32_t)x.token;
+#pragma unroll
+    for (int i = 0; i < R::LD; ++i) {
+      if (ch[i % R::NV] >= nchunk) continue;
+      if (left >= PT_K)
+        to_lds(reinterpret_cast<const char*>(base) + (int64_t)i * R::RN * stride, r0 * stride + 16 * ch[i % R::NV],
+               lds + i * 16 * NT);
+      else
+        to_lds(base, min(i * R::RN + r0, left - 1) * stride + 16 * ch[i % R::NV], lds + i * 16 * NT);
+    }
+  };
+  auto fetch = [&](int j) {
+    load(k, j, lds0 + j % S * R::BYTES);
+    load(v, j, lds0 + (S + j % S) * R::BYTES);
+  };
+  const int last = (min(pl.len, (pl.tile + 1) * ROWS) - 1) / PT_K;
+  fetch(last);
   u4 qf[L::KS];
   {
     const uint16_t* src = q.at(pl.start + min(row, pl.len - 1), head);
 #pragma unroll
     for (int s = 0; s < L::KS; ++s) {
-      const int ch = 2 * s + hi;
-      qf[s] = ch < nchunk ? *reinterpret_cast<const u4*>(src + 8 * ch) : u4{0, 0, 0, 0};
+      const int at = 2 * s + hi;
+      qf[s] = at < nchunk ? *reinterpret_cast<const u4*>(src + 8 * at) : u4{0, 0, 0, 0};
     }
   }
-  if (nchunk < L::NC) {                            // chunks that no load fills
-    for (int e = tid; e < PT_K * L::NC; e += NT) sk0[e] = sk1[e] = sv0[e] = sv1[e] = u4{0, 0, 0, 0};
-    __syncthreads();
-  }
+  const Reads<D> rd(lane);
   Sums<T, D> sum;
   sum.clear();
-  const int kv = head / group;
-  const int key_end = min(pl.len, (pl.tile + 1) * PT_Q);
-  const int my_tile = (row0 + 31) / PT_K;          // the wave's last (masked) tile
-  auto load = [&](int kt, u4* dk, u4* dv) {
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int e = i * NT + tid, r = e / L::NC, ch = (e % L::NC) ^ L::swz(r);
-      const int64_t tok = pl.start + min(kt * PT_K + r, pl.len - 1);
-      if (ch < nchunk) {
-        to_lds(k.at(tok, kv) + 8 * ch, dk + i * NT + 64 * w);
-        to_lds(v.at(tok, kv) + 8 * ch, dv + i * NT + 64 * w);
-      }
-    }
+  f16v s[2];
+  uint32_t pw[16];
+  const int mine = row0 / PT_K, seen = row - mine * PT_K + 1;
+  int j = last;
+  auto turn = [&] {
+    arrive<0>();
+    if (j > 0) fetch(j - 1);
   };
-  int kt = (key_end - 1) / PT_K;
-  if (kt & 1) load(kt, sk1, sv1);
-  else load(kt, sk0, sv0);
-  // Tiles with an even number lie in the first buffer.  Every wave passes the same barriers, one a tile: those before
-  // its masked tile, the masked one, and the rest.
-  const Reads<D> rd(lane);
-  auto arrive = [&](u4* nk, u4* nv) {              // tile kt has come, and tile kt + 1 has been read
-    __syncthreads();
-    if (kt > 0) load(kt - 1, nk, nv);
-  };
-  for (; kt > my_tile; --kt) {
-    if (kt & 1) arrive(sk0, sv0);
-    else arrive(sk1, sv1);
+  for (; j > mine; --j) turn();
+  if (j == mine) {
+    turn();
+    sum.scores(ring + j % S * R::BYTES, qf, rd, s);
+    sum.mask(s, seen);
+    sum.weigh(s, c, pw);
+    sum.add(ring + (S + j % S) * R::BYTES, pw, rd);
+    sum.mend(ring + (S + j % S) * R::BYTES, pw, seen, rd);
+    --j;
   }
-  const int seen = row - kt * PT_K + 1;
-  if (kt & 1) {
-    arrive(sk0, sv0);
-    sum.first(sk1, sv1, qf, c, seen, rd);
-    --kt;
+  for (; j >= 0; --j) {
+    turn();
+    sum.scores(ring + j % S * R::BYTES, qf, rd, s);
+    sum.weigh(s, c, pw);
+    sum.add(ring + (S + j % S) * R::BYTES, pw, rd);
   }
-  if (kt >= 0) {
-    arrive(sk1, sv1);
-    if (kt == my_tile) sum.first(sk0, sv0, qf, c, seen, rd);
-    else sum.next(sk0, sv0, qf, c, rd);
-    --kt;
-  }
-  while (kt >= 0) {
-    arrive(sk0, sv0);
-    sum.next(sk1, sv1, qf, c, rd);
-    --kt;
-    arrive(sk1, sv1);
-    sum.next(sk0, sv0, qf, c, rd);
-    --kt;
-  }
-  if (row0 >= pl.len) return;
-  const float l = sum32(sum.l);
-  const float inv = l == 0.f ? 0.f : 1.f / l;      // no weight at all (every score -inf): zero
-  uint16_t* dst = out + (pl.start + row) * out_token + head * out_head;
-#pragma unroll
-  for (int t = 0; t < L::DT; ++t)
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {                  // 16 dims: the lane halves trade so that each stores 8
-      const f16v& o = sum.o[t];
-      const int i = 8 * g;
-      const uint32_t a0 = T::pack(o[i] * inv, o[i + 1] * inv), a1 = T::pack(o[i + 2] * inv, o[i + 3] * inv);
-      const uint32_t b0 = T::pack(o[i + 4] * inv, o[i + 5] * inv), b1 = T::pack(o[i + 6] * inv, o[i + 7] * inv);
-      const auto r0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
-      const auto r1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
-      const int ch = 4 * t + 2 * g + hi;
-      if (row < pl.len && ch < nchunk) *reinterpret_cast<u4*>(dst + 8 * ch) = u4{r0[0], r1[0], r0[1], r1[1]};
-    }
+  if (row0 < pl.len) sum.store(out + (pl.start + row) * out_token + head * out_head, row < pl.len, nchunk);
 }
 
 // ------------------------------------------------ attention of single new tokens

@@ -304,7 +304,8 @@ pi_status pi_cache_compact(const pi_cache* cache, int32_t* moved, void* ws, size
  * within it.  scale 0 = 1 / sqrt(dim); otherwise finite and positive
  * (PI_EINVAL).  cu: [n + 1] int32, ascending, within 0 .. tokens; rows that no
  * sequence holds are not written.  Keys a row does not see leave no trace in
- * it, infinities and NaN included.
+ * it, infinities and NaN included.  The token strides of k and v are at most
+ * 2^24 (PI_EUNSUPPORTED).
  */
 pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v, const pi_heads* out, int32_t tokens,
                          int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype, const int32_t* cu, int32_t n,

@@ -126,6 +126,13 @@ def test_prompt_arguments(pi, kw, status):
                                    a["scale"], None) == status
 
 
+@pytest.mark.parametrize("token", [(1 << 24) + 8, -8])
+def test_prompt_strides_of_keys_and_values(pi, token):
+    good, bad = ctypes.byref(heads(pi)), ctypes.byref(heads(pi, token=token))
+    for k, v in ((bad, good), (good, bad)):
+        assert pi.lib().pi_attn_prompt(good, k, v, good, 5, 4, 2, 64, pi.PI_F16, FAKE, 1, 0.0, None) == EUNSUPPORTED
+
+
 def test_prompt_of_no_tokens_enqueues_nothing(pi):
     h = ctypes.byref(heads(pi, p=None))
     assert pi.lib().pi_attn_prompt(h, h, h, h, 0, 4, 2, 64, pi.PI_BF16, FAKE, 3, 0.0, None) == 0
