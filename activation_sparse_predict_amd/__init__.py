@@ -310,11 +310,22 @@ def ffn_stack_static(layers, x, out, counts=None, trace=None, batch: int = 1, st
 
 
 # ------------------------------------------ the attention half of a decoder layer
+# A call on a few tokens takes the GPU less time than its checks take the host, so these are kept short:
+# each attribute of a tensor is asked for once, and the current stream without an object for it.
+_KINDS = None
+
+
+def _torch_names():
+    global _KINDS
+    import torch
+    _KINDS = {torch.float32: PI_F32, torch.float16: PI_F16, torch.bfloat16: PI_BF16, torch.int32: "int32"}
+    return _KINDS
+
+
 def _dtype_of(t) -> int:
     """pi_dtype of a float tensor (other types: PI_EINVAL)."""
-    import torch
-    kind = {torch.float32: PI_F32, torch.float16: PI_F16, torch.bfloat16: PI_BF16}.get(t.dtype)
-    if kind is None:
+    kind = (_KINDS or _torch_names()).get(t.dtype)
+    if kind is None or kind == "int32":
         raise PiError(PI_EINVAL, f"tensor of {t.dtype}")
     return kind
 
@@ -324,27 +335,43 @@ def _need(ok: bool, what: str):
         raise PiError(PI_EINVAL, what)
 
 
-def _gpu(what: str, *tensors):
-    """All tensors (None aside) lie on one GPU: a kernel cannot follow an address of the host's."""
-    dev = tensors[0].get_device()
-    _need(dev >= 0 and all(t is None or t.get_device() == dev for t in tensors), what)
+def _gpu(what: str, first, *tensors) -> int:
+    """The GPU on which all tensors (None aside) lie: a kernel cannot follow an address of the host's."""
+    dev = first.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise PiError(PI_EINVAL, what)
+    if dev < 0:
+        raise PiError(PI_EINVAL, what)
+    return dev
+
+
+def _stream_on(dev: int, stream):
+    """The handle of a stream, or of the current stream of a GPU."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _ints(t, n: Optional[int], what: str) -> Optional[int]:
     """Address of a contiguous int32 tensor of n elements (any number where n is None), or None for None."""
-    import torch
     if t is None:
         return None
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and (n is None or t.numel() == n), what)
+    shape = t.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n) or not t.is_contiguous() \
+            or (_KINDS or _torch_names()).get(t.dtype) != "int32":
+        raise PiError(PI_EINVAL, what)
     return t.data_ptr()
 
 
-def _heads(t, what: str) -> PiHeads:
-    """A [tokens][heads][dim] tensor with strides; the last dimension contiguous."""
-    shape, stride = t.shape, t.stride()
-    _need(len(shape) == 3 and (stride[2] == 1 or shape[2] == 1), what)
+def _heads(t, shape, what: str):
+    """Reference to the pi_heads of a [tokens][heads][dim] tensor with strides; the last dimension contiguous."""
+    token, head, one = t.stride()
+    if one != 1 and shape[2] != 1:
+        raise PiError(PI_EINVAL, what)
     # the stride of a dimension of one element says nothing
-    return PiHeads(t.data_ptr() or None, stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0)
+    return ctypes.byref(PiHeads(t.data_ptr() or None, token if shape[0] > 1 else 0, head if shape[1] > 1 else 0))
 
 
 class Cache:
@@ -378,7 +405,9 @@ class Cache:
         n = int(lib().pi_cache_workspace_bytes(self._ref))
         if n == 0:                                   # say which rule it is
             _check(lib().pi_cache_release(self._ref, None, 1, None), "Cache")
+        self.dtype, self._lib = k_pool.dtype, lib()
         self.ws = torch.empty(n, dtype=torch.uint8, device=k_pool.device)
+        self._ws, self._ws_bytes = self.ws.data_ptr(), n
         self._attn_ws = {}
 
     @staticmethod
@@ -401,70 +430,72 @@ class Cache:
     def extend(self, seqs, counts, stream=None):
         """Room for counts[i] more tokens in slot seqs[i]."""
         n = seqs.numel()
-        _gpu("extend: tensors of one GPU", self.meta, seqs, counts)
-        _check(lib().pi_cache_extend(self._ref, _ints(seqs, n, "extend: seqs"), _ints(counts, n, "extend: counts"), n,
-                                     _stream(stream)), "pi_cache_extend")
+        dev = _gpu("extend: tensors of one GPU", self.meta, seqs, counts)
+        _check(self._lib.pi_cache_extend(self._ref, _ints(seqs, n, "extend: seqs"), _ints(counts, n, "extend: counts"),
+                                         n, _stream_on(dev, stream)), "pi_cache_extend")
 
     def append(self, layer: int, k, v, cu, seqs, stream=None):
         """Rows cu[i] .. cu[i + 1] - 1 of k and v [tokens][kv_heads][dim] become the last tokens of slot seqs[i]."""
-        want = (self.kv_heads, self.dim)
-        _need(k.shape == v.shape and tuple(k.shape[1:]) == want and k.dtype == v.dtype == self.k_pool.dtype,
-              "append: k, v")
+        shape = k.shape
+        _need(len(shape) == 3 and shape == v.shape and shape[1] == self.kv_heads and shape[2] == self.dim
+              and k.dtype == v.dtype == self.dtype, "append: k, v")
         n = seqs.numel()
-        _gpu("append: tensors of one GPU", self.meta, k, v, cu, seqs)
-        kh, vh = _heads(k, "append: k"), _heads(v, "append: v")
-        _check(lib().pi_cache_append(self._ref, layer, ctypes.byref(kh), ctypes.byref(vh), k.shape[0],
-                                     _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
-                                     _stream(stream)), "pi_cache_append")
+        dev = _gpu("append: tensors of one GPU", self.meta, k, v, cu, seqs)
+        _check(self._lib.pi_cache_append(self._ref, layer, _heads(k, shape, "append: k"), _heads(v, shape, "append: v"),
+                                         shape[0], _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
+                                         _stream_on(dev, stream)), "pi_cache_append")
 
     def fork(self, parents, children, stream=None):
         """The empty slot children[i] becomes a copy of slot parents[i]."""
         n = parents.numel()
-        _gpu("fork: tensors of one GPU", self.meta, parents, children)
-        _check(lib().pi_cache_fork(self._ref, _ints(parents, n, "fork: parents"), _ints(children, n, "fork: children"),
-                                   n, _p(self.ws), self.ws.numel(), _stream(stream)), "pi_cache_fork")
+        dev = _gpu("fork: tensors of one GPU", self.meta, parents, children)
+        _check(self._lib.pi_cache_fork(self._ref, _ints(parents, n, "fork: parents"),
+                                       _ints(children, n, "fork: children"), n, self._ws, self._ws_bytes,
+                                       _stream_on(dev, stream)), "pi_cache_fork")
 
     def release(self, seqs, stream=None):
         """The listed slots become empty."""
         n = seqs.numel()
-        _gpu("release: tensors of one GPU", self.meta, seqs)
-        _check(lib().pi_cache_release(self._ref, _ints(seqs, n, "release: seqs"), n, _stream(stream)),
+        dev = _gpu("release: tensors of one GPU", self.meta, seqs)
+        _check(self._lib.pi_cache_release(self._ref, _ints(seqs, n, "release: seqs"), n, _stream_on(dev, stream)),
                "pi_cache_release")
 
     def compact(self, moved=None, stream=None):
         """The pages in use move to the front of the pool; moved [pages]: the new place of each."""
-        _gpu("compact: tensors of one GPU", self.meta, moved)
-        _check(lib().pi_cache_compact(self._ref, _ints(moved, self.pages, "compact: moved"), _p(self.ws),
-                                      self.ws.numel(), _stream(stream)), "pi_cache_compact")
+        dev = _gpu("compact: tensors of one GPU", self.meta, moved)
+        _check(self._lib.pi_cache_compact(self._ref, _ints(moved, self.pages, "compact: moved"), self._ws,
+                                          self._ws_bytes, _stream_on(dev, stream)), "pi_cache_compact")
 
     def errors(self) -> int:
         """The error word (waits for the device)."""
         return int(self.words[1])
 
     def attn_workspace(self, batch: int, heads: int):
-        import torch
-        if (batch, heads) not in self._attn_ws:
+        """The workspace of attn_decode for these sizes."""
+        ws = self._attn_ws.get((batch, heads))
+        if ws is None:
+            import torch
             n = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
             _need(n > 0, "attn_decode: batch, heads")
             # memory taken while a graph is captured belongs to that graph
             _need(not torch.cuda.is_current_stream_capturing(), "attn_decode: first call of these sizes inside a capture")
-            self._attn_ws[batch, heads] = torch.empty(n, dtype=torch.uint8, device=self.k_pool.device)
-        return self._attn_ws[batch, heads]
+            ws = self._attn_ws[batch, heads] = torch.empty(n, dtype=torch.uint8, device=self.k_pool.device)
+        return ws
 
 
 def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
     """Causal attention over packed sequences, rows cu[i] .. cu[i + 1] - 1 each.
 
     q, out: [tokens][heads][dim]; k, v: [tokens][kv_heads][dim]; scale 0: 1 / sqrt(dim)."""
-    _need(q.shape == out.shape and k.shape == v.shape and q.dim() == k.dim() == 3 and q.shape[0] == k.shape[0]
-          and q.shape[2] == k.shape[2] and q.dtype == k.dtype == v.dtype == out.dtype, "attn_prompt: q, k, v, out")
-    _need(cu.numel() > 1, "attn_prompt: cu")
-    h = [_heads(t, "attn_prompt: strides") for t in (q, k, v, out)]
-    offsets = _ints(cu, None, "attn_prompt: cu")
-    _gpu("attn_prompt: tensors of one GPU", q, k, v, out, cu)
-    _check(lib().pi_attn_prompt(*(ctypes.byref(x) for x in h), q.shape[0], q.shape[1], k.shape[1], q.shape[2],
-                                _dtype_of(q), offsets, cu.numel() - 1, scale,
-                                _stream(stream)), "pi_attn_prompt")
+    qs, ks, n = q.shape, k.shape, cu.numel() - 1
+    _need(len(qs) == len(ks) == 3 and qs == out.shape and ks == v.shape and qs[0] == ks[0] and qs[2] == ks[2]
+          and q.dtype == k.dtype == v.dtype == out.dtype, "attn_prompt: q, k, v, out")
+    _need(n > 0, "attn_prompt: cu")
+    offsets, what = _ints(cu, None, "attn_prompt: cu"), "attn_prompt: strides"
+    dev = _gpu("attn_prompt: tensors of one GPU", q, k, v, out, cu)
+    _check((_lib or lib()).pi_attn_prompt(_heads(q, qs, what), _heads(k, ks, what), _heads(v, ks, what),
+                                          _heads(out, qs, what), qs[0], qs[1], ks[1], qs[2], _dtype_of(q), offsets, n,
+                                          scale, _stream_on(dev, stream)), "pi_attn_prompt")
 
 
 def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale: float = 0.0, ws=None, stream=None):
@@ -472,15 +503,16 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
 
     seqs: the slots (None: row b is slot b).  prefix: an int32 tensor of one element, how many
     leading pages the slots that are not empty have in common.  ws: as Cache.attn_workspace."""
-    _need(q.shape == out.shape and q.dim() == 3 and q.shape[2] == cache.dim
-          and q.dtype == out.dtype == cache.k_pool.dtype, "attn_decode: q, out")
-    _gpu("attn_decode: tensors of one GPU", cache.meta, q, out, prefix, seqs, ws)
-    batch, heads = q.shape[:2]
+    shape = q.shape
+    _need(len(shape) == 3 and shape == out.shape and shape[2] == cache.dim and q.dtype == out.dtype == cache.dtype,
+          "attn_decode: q, out")
+    dev = _gpu("attn_decode: tensors of one GPU", cache.meta, q, out, prefix, seqs, ws)
+    batch, heads, _ = shape
     ws = cache.attn_workspace(batch, heads) if ws is None else ws
-    hq, ho = _heads(q, "attn_decode: q"), _heads(out, "attn_decode: out")
-    _check(lib().pi_attn_decode(cache._ref, layer, ctypes.byref(hq), ctypes.byref(ho), batch, heads,
-                                _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,
-                                _p(ws), ws.numel(), _stream(stream)), "pi_attn_decode")
+    what = "attn_decode: strides"
+    _check(cache._lib.pi_attn_decode(cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch, heads,
+                                     _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"),
+                                     scale, ws.data_ptr(), ws.numel(), _stream_on(dev, stream)), "pi_attn_decode")
 
 
 class Q4Matrix:
@@ -503,6 +535,8 @@ class Q4Matrix:
         self.nibbles, self.scales, self.bias = nibbles, scales, bias
         self.struct = PiMat(_p(nibbles), _p(scales))
         self.ws = torch.empty(n, dtype=torch.uint8, device=nibbles.device)
+        self._args = ctypes.byref(self.struct), self.rows, self.cols, _p(bias)
+        self._ws, self._ws_bytes, self._lib = self.ws.data_ptr(), n, lib()
 
     @classmethod
     def upload(cls, mat, bias=None, batch: int = 1, device="cuda") -> "Q4Matrix":
@@ -516,13 +550,17 @@ class Q4Matrix:
 
 def matvec(mat: Q4Matrix, x, y, stream=None):
     """y[b] = W x[b] + bias; x [batch][cols], y [batch][rows], float32, float16 or bfloat16 each."""
-    _need(x.dim() == y.dim() == 2 and x.shape[0] == y.shape[0] <= mat.batch and x.shape[1] == mat.cols
-          and y.shape[1] == mat.rows and x.stride(1) == 1 and (y.stride(1) == 1 or mat.rows == 1), "matvec: x, y")
-    _gpu("matvec: tensors of one GPU", mat.nibbles, x, y)
-    batch = x.shape[0]
-    ldx, ldy = (x.stride(0), y.stride(0)) if batch > 1 else (mat.cols, mat.rows)
-    _check(lib().pi_matvec(ctypes.byref(mat.struct), mat.rows, mat.cols, _p(mat.bias), _p(x), _dtype_of(x), ldx, _p(y),
-                           _dtype_of(y), ldy, batch, _p(mat.ws), mat.ws.numel(), _stream(stream)), "pi_matvec")
+    xs, ys = x.shape, y.shape
+    _need(len(xs) == len(ys) == 2 and xs[0] == ys[0] <= mat.batch and xs[1] == mat.cols and ys[1] == mat.rows,
+          "matvec: x, y")
+    (ldx, x1), (ldy, y1), batch = x.stride(), y.stride(), xs[0]
+    _need(x1 == 1 and (y1 == 1 or ys[1] == 1), "matvec: strides")
+    if batch == 1:                                     # a row's stride says nothing there
+        ldx, ldy = xs[1], ys[1]
+    dev = _gpu("matvec: tensors of one GPU", mat.nibbles, x, y)
+    _check(mat._lib.pi_matvec(*mat._args, x.data_ptr(), _dtype_of(x), ldx, y.data_ptr(), _dtype_of(y), ldy, batch,
+                              mat._ws, mat._ws_bytes, _stream_on(dev, stream)), "pi_matvec")
+
 
 
 # ------------------------------------------------------- HIP runtime plumbing
