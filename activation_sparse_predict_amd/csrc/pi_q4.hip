@@ -1,6 +1,7 @@
 // Host side of the products with Q4_0 matrices (pi.h): checks, workspace, launches.
 #include "pi_q4.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pi_host.hpp"
@@ -8,6 +9,9 @@
 using namespace pih;
 
 namespace {
+
+// 12288 float32 values; with the sums of the waves (9 KB) a block keeps to 64 KB
+constexpr size_t kOperandLds = 48 << 10;
 
 // the operand made of x, of the largest number of columns a type of x takes, and a row's scale
 struct Ws {
@@ -60,15 +64,35 @@ pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* 
   (void)hipGetLastError();
   with_dtype(x_dtype, [&](auto xt) {
     constexpr int X = decltype(xt)::value, P = piq::parts<X>();
-    const int tiles = (int)up_div(P * batch, 16);
-    hipLaunchKernelGGL((piq::k_mv_operand<X>), dim3(16 * tiles / P), dim3(256), 0, st, x, ldx, batch, cols, tiles, xo,
-                       inv);
+    const int columns = P * batch;
+    // few columns whose operand fits beside another block's in LDS: each block makes it for itself
+    const size_t lds = (size_t)2 * columns * cols;
+    const bool few = columns <= 16 && lds <= kOperandLds;
+    const int tiles = (int)up_div(columns, 16);
+    if (!few)
+      hipLaunchKernelGGL((piq::k_mv_operand<X>), dim3(16 * tiles / P, (unsigned)std::min<int64_t>(16, up_div(cols, 1024))),
+                         dim3(256), 0, st, x, ldx, batch, cols, tiles, xo, inv);
     with_dtype(y_dtype, [&](auto yt) {
       constexpr int Y = decltype(yt)::value;
+      auto w_of = static_cast<const uint8_t*>(mat->w);
+      if (few) {
+        auto go = [&](auto ma) {
+          // as many blocks as fit at once (up to four a compute unit), each with an even share of the row tiles
+          const int64_t fit = std::min<int64_t>(4, (160 << 10) / (int64_t)(lds + (10 << 10)));
+          hipLaunchKernelGGL((piq::k_matvec_few<X, Y, decltype(ma)::value>),
+                             dim3((unsigned)std::min(up_div(rows, piq::MV_ROWS), 256 * fit)),
+                             dim3(piq::MV_WAVES * piq::WAVE), lds, st, w_of, mat->scale, bias, rows, cols, x, ldx,
+                             batch, y, ldy);
+        };
+        if (columns <= 4) go(std::integral_constant<int, 1>());
+        else if (columns <= 8) go(std::integral_constant<int, 2>());
+        else go(std::integral_constant<int, 4>());
+        return;
+      }
       auto go = [&](auto mt) {
-        hipLaunchKernelGGL((piq::k_matvec<X, Y, decltype(mt)::value>), dim3((unsigned)up_div(rows, piq::MV_ROWS)),
-                           dim3(piq::MV_WAVES * piq::WAVE), 0, st, static_cast<const uint8_t*>(mat->w), mat->scale,
-                           bias, rows, cols, xo, inv, batch, y, ldy);
+        hipLaunchKernelGGL((piq::k_matvec<X, Y, decltype(mt)::value>),
+                           dim3((unsigned)up_div(rows, piq::MV_ROWS)), dim3(piq::MV_WAVES * piq::WAVE), 0, st, w_of,
+                           mat->scale, bias, rows, cols, xo, inv, batch, y, ldy);
       };
       if (tiles == 1) go(std::integral_constant<int, 1>());
       else if (tiles == 2) go(std::integral_constant<int, 2>());

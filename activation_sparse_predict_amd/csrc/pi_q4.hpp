@@ -4,13 +4,17 @@
 //
 // A 16x16x32 matrix instruction takes one 32-weight block of 16 rows.  Its
 // weights are q - 8 in binary16 (exact), and the block's product is multiplied
-// by the block's scale in float32, so no weight is rounded.  x goes in as
-// binary16 after multiplication by a power of two that puts its row's largest
-// value into [2^14, 2^15): one column for binary16 and bfloat16 rows (their
-// significands fit), two for float32 rows, the rounded value and 2^11 times
-// what it leaves, which together are x within 2^-24 relative, half a step of
-// float32.  Values below 2^-39 of their row's largest lose bits to binary16's
-// range; they are under 2^-24 of any sum they could show in by then.
+// by the block's scale in float32, so no weight is rounded.  Rows of x in
+// binary16 go in as they are.  Others go in as binary16 after multiplication by
+// a power of two that puts the row's largest finite value into [2^14, 2^15):
+// one column for bfloat16 rows (their significands fit), two for float32 rows,
+// the rounded value and 2^11 times what it leaves, which together are x within
+// 2^-23 relative.  Values below 2^-39 of their row's largest lose bits to
+// binary16's range; they are under 2^-24 of any sum they could show in by then.
+//
+// What bounds the products is the read of the matrix, 18 bytes for 32 weights;
+// unpacking them takes about 13 vector instructions for 288 bytes, a quarter of
+// that time.
 #pragma once
 #include "pi.h"
 #include "pi_tile.hpp"
@@ -19,14 +23,39 @@ namespace piq {
 
 using namespace pit;
 
-constexpr int MV_ROWS = 16;              // matrix rows of a block's tile
-constexpr int MV_WAVES = 4;
+constexpr int MV_ROWS = 16;              // matrix rows of a tile
+constexpr int MV_G = 8;                  // 32-blocks of a group: 128 bytes of a row's nibbles, one cache line
+constexpr int MV_WAVES = 8;              // waves of a block
+constexpr int MV_AHEAD = 3;              // groups of a wave on their way
 
 // Load one element of x, stored as dtype X (pi_dtype), as float32.
 template <int X> __device__ __forceinline__ float x_at(const void* p, int64_t i) {
   if constexpr (X == PI_F32) return static_cast<const float*>(p)[i];
   else if constexpr (X == PI_F16) return (float)static_cast<const _Float16*>(p)[i];
   else return (float)static_cast<const __bf16*>(p)[i];
+}
+// Four elements from i on, whatever their alignment.
+struct __attribute__((packed, aligned(4))) Four32 {
+  float v[4];
+};
+struct __attribute__((packed, aligned(2))) Four16 {
+  uint16_t v[4];
+};
+template <int X> __device__ __forceinline__ f4 x_four(const void* p, int64_t i) {
+  f4 r;
+  if constexpr (X == PI_F32) {
+    const Four32 a = *reinterpret_cast<const Four32*>(static_cast<const float*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = a.v[j];
+  } else {
+    const Four16 a = *reinterpret_cast<const Four16*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (X == PI_F16) r[j] = (float)__builtin_bit_cast(_Float16, a.v[j]);
+      else r[j] = __uint_as_float((uint32_t)a.v[j] << 16);
+    }
+  }
+  return r;
 }
 template <int Y> __device__ __forceinline__ void y_to(void* p, int64_t i, float v) {
   if constexpr (Y == PI_F32) static_cast<float*>(p)[i] = v;
@@ -66,7 +95,43 @@ __device__ __forceinline__ float row_scale(float big) {
   return __uint_as_float((uint32_t)min(max(127 + 14 - (e - 127), 1), 254) << 23);
 }
 
-// x -> operand [block][column tile][lane][8] and, per row, 1 / scale.  One block per column pair row.
+// The largest finite |x| of a row, by all threads of a block (NT of them; part: LDS, NT / 64 floats).
+template <int X, int NT>
+__device__ __forceinline__ float row_max(const void* x, int64_t at, int cols, float* part) {
+  const int tid = threadIdx.x;
+  float big = 0.f;
+#pragma unroll 8
+  for (int k = 4 * tid; k < cols; k += 4 * NT) {
+    const f4 v = x_four<X>(x, at + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (fabsf(v[j]) < __builtin_inff()) big = fmaxf(big, fabsf(v[j]));   // others are what they are at any scale
+  }
+  for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
+  __syncthreads();
+  if ((tid & 63) == 0) part[tid >> 6] = big;
+  __syncthreads();
+  big = part[0];
+#pragma unroll
+  for (int i = 1; i < NT / 64; ++i) big = fmaxf(big, part[i]);
+  return big;
+}
+
+// The operand's columns of a value: binary16 bits of part p of it.
+__device__ __forceinline__ uint32_t x_part(float v, int p) {
+  const _Float16 h = (_Float16)v;
+  if (p == 0) return __builtin_bit_cast(uint16_t, h);
+  // an infinite or NaN value leaves nothing
+  const float rest = fabsf(v) <= 65504.f ? (v - (float)h) * 2048.f : 0.f;
+  return __builtin_bit_cast(uint16_t, (_Float16)rest);
+}
+
+// Elements 4 a .. 4 a + 3 of a 32-block, a < 8, lie at words `at(a)` and `at(a) + 2` of the block's 16, elements
+// 0 and 2 in the first (the order of slot_k).
+__device__ __forceinline__ int word_of(int a) { return 4 * (a & 3) + (a >> 2); }
+
+// x -> operand [block][column tile][lane][8] and, per row, 1 / scale.  Block (b, i): a share of x row b's blocks.
+// Rows from `batch` on are the columns that fill up the last tile.
 template <int X>
 __global__ void __launch_bounds__(256)
 k_mv_operand(const void* __restrict__ x, int64_t ldx, int batch, int cols, int tiles, uint16_t* __restrict__ xo,
@@ -76,97 +141,276 @@ k_mv_operand(const void* __restrict__ x, int64_t ldx, int batch, int cols, int t
   constexpr int P = parts<X>();
   float s = 1.f;
   if (b < batch) {
-    float big = 0.f;
-    for (int k = tid; k < cols; k += 256) {
-      const float v = fabsf(x_at<X>(x, b * ldx + k));
-      if (v < __builtin_inff()) big = fmaxf(big, v);   // infinities and NaN are what they are at any scale
-    }
-    for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
-    if ((tid & 63) == 0) part[tid >> 6] = big;
-    __syncthreads();
-    s = row_scale(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
-    if (tid == 0) inv[b] = 1.f / s;
+    if constexpr (X != PI_F16) s = row_scale(row_max<X, 256>(x, b * ldx, cols, part));
+    if (tid == 0 && blockIdx.y == 0) inv[b] = 1.f / s;
   }
-  for (int e = tid; e < cols; e += 256) {          // operand elements of this row's columns
-    const int kb = e / 32, kg = (e / 8) % 4, i = e % 8;
-    const float v = b < batch ? x_at<X>(x, b * ldx + 32 * kb + slot_k(kg, i)) * s : 0.f;
-    const _Float16 h = (_Float16)v;
+  for (int e = 4 * (blockIdx.y * 256 + tid); e < cols; e += 4 * 256 * gridDim.y) {
+    f4 v = (f4)(0.f);
+    if (b < batch) v = x_four<X>(x, b * ldx + e) * s;
+    const int kb = e / 32, wd = word_of(e / 4 % 8);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = P * b + p;
       if (c >= 16 * tiles) break;
-      // an infinite or NaN value leaves nothing
-      const float rest = fabsf(v) <= 65504.f ? (v - (float)h) * 2048.f : 0.f;
-      const _Float16 y = p ? (_Float16)rest : h;
-      const int lane = 16 * kg + col_row(c % 16);
-      xo[((int64_t)(kb * tiles + c / 16) * 64 + lane) * 8 + i] = __builtin_bit_cast(uint16_t, y);
+      uint32_t* to = reinterpret_cast<uint32_t*>(xo) +
+                     ((int64_t)(kb * tiles + c / 16) * 64 + 16 * (wd / 4) + col_row(c % 16)) * 4 + wd % 4;
+      to[0] = x_part(v[0], p) | x_part(v[2], p) << 16;
+      to[2] = x_part(v[1], p) | x_part(v[3], p) << 16;
     }
   }
 }
 
-// One block: 16 matrix rows, the waves taking groups of four 32-blocks in turn.
-// Lane (r, kg) loads block 4 j + kg of row r whole; 4 swaps of lane groups
-// leave it word kg of each of the four blocks.
+// A lane's share of a group of 8 blocks of one row tile: lane (r, kg) holds blocks 8 j + 2 kg and + 1 of row r, and
+// the scales of all eight.
+struct Group {
+  u4 q[2], s;
+};
+
+// Scales lie on 2 bytes; they are read 16 bytes at once all the same, which global memory allows.
+struct __attribute__((packed, aligned(2))) Scales {
+  u4 v;
+};
+
+// `left`: blocks of the row from the group on.  A group that is not whole is read block by block, and what lies
+// behind it has scale 0 (its operand is 0 too).
+__device__ __forceinline__ Group load_group(const uint8_t* q, const uint16_t* s, int kg, int left) {
+  Group g;
+  if (left >= MV_G) {
+    g.q[0] = *reinterpret_cast<const u4*>(q + 32 * kg);
+    g.q[1] = *reinterpret_cast<const u4*>(q + 32 * kg + 16);
+    g.s = reinterpret_cast<const Scales*>(s)->v;
+  } else {
+    g.q[0] = *reinterpret_cast<const u4*>(q + 16 * min(2 * kg, left - 1));
+    g.q[1] = *reinterpret_cast<const u4*>(q + 16 * min(2 * kg + 1, left - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = 2 * i < left ? s[2 * i] : 0, b = 2 * i + 1 < left ? s[2 * i + 1] : 0;
+      g.s[i] = a | b << 16;
+    }
+  }
+  return g;
+}
+
+// Word kg of each of four blocks, from the lanes that hold the blocks whole: block i comes to w[i].
+__device__ __forceinline__ void spread(u4 c, uint32_t* w) {
+  const auto a = __builtin_amdgcn_permlane16_swap(c[0], c[1], false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(c[2], c[3], false, false);
+  const auto e = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const auto o = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  w[0] = e[0], w[1] = o[0], w[2] = e[1], w[3] = o[1];
+}
+
+__device__ __forceinline__ float scale_at(u4 s, int i) {
+  const uint32_t w = s[i / 2];
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+}
+
+// Products of few columns (parts<X>() * batch = PB <= 16): every block makes the
+// operand for itself, in LDS, while its first weights are on their way, and then
+// takes row tiles in turn.  The waves take groups of 8 blocks in turn and join
+// their sums through LDS.  Columns go to operand rows such that D registers
+// 0 .. MA - 1 hold them (col_row).
+//
+// 36864 x 12288, one float32 row: 60 us, 4.2 TB/s; 74 us with 4 waves a block,
+// 61 to 63 us with 2 or 4 groups ahead, 77 us with a branch at each block of a
+// whole group.  4096 x 4096: 6.2 us a call.
+template <int X, int Y, int MA>
+__global__ void __launch_bounds__(MV_WAVES * WAVE)
+k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, const float* __restrict__ bias,
+             int rows, int cols, const void* __restrict__ x, int64_t ldx, int batch, void* __restrict__ y,
+             int64_t ldy) {
+  constexpr int P = parts<X>(), W = MV_WAVES, NT = W * WAVE;
+  extern __shared__ __attribute__((aligned(16))) char lds[];   // the operand [block][column][32]
+  constexpr int RB = MA < 4 ? 2 : 1;               // a second buffer for the sums, while the operand leaves room for it
+  __shared__ float red[RB][W][4 * MA][MV_ROWS + 1], part[W], inv[16];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+            kg = lane >> 4;
+  const int blocks = cols / 32, groups = (blocks + MV_G - 1) / MV_G, PB = P * batch;
+  const int tiles = (rows + MV_ROWS - 1) / MV_ROWS;
+  // this block's tiles, and this wave's groups of each: w, w + W, ..
+  const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+  Group buf[MV_AHEAD];                                  // groups on their way
+  int ta = w < groups ? t0 : t1, ga = w;           // the next one to load
+  auto ahead = [&](Group& to) {
+    if (ta >= t1) return;
+    const int row = min(ta * MV_ROWS + r, rows - 1);
+    to = load_group(q + (int64_t)row * (cols / 2) + 128 * ga, scale + (int64_t)row * blocks + MV_G * ga, kg,
+                    blocks - MV_G * ga);
+    ga += W;
+    if (ga >= groups) ga = w, ++ta;
+  };
+#pragma unroll
+  for (int i = 0; i < MV_AHEAD; ++i) ahead(buf[i]);
+
+  uint32_t* xo = reinterpret_cast<uint32_t*>(lds);
+  for (int b = 0; b < batch; ++b) {
+    float s = 1.f;
+    if constexpr (X != PI_F16) s = row_scale(row_max<X, NT>(x, b * ldx, cols, part));
+    if (tid == 0) inv[b] = 1.f / s;
+#pragma unroll 4
+    for (int e = 4 * tid; e < cols; e += 4 * NT) {
+      const f4 v = x_four<X>(x, b * ldx + e) * s;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        uint32_t* to = xo + (e / 32 * PB + P * b + p) * 16 + word_of(e / 4 % 8);
+        to[0] = x_part(v[0], p) | x_part(v[2], p) << 16;
+        to[2] = x_part(v[1], p) | x_part(v[3], p) << 16;
+      }
+    }
+  }
+  __syncthreads();
+  // the operand row's column; rows beyond hold copies
+  const char* xl = lds + 64 * (col_row(r) % PB) + 16 * kg;
+
+  f4 acc = (f4)(0.f);
+  auto add = [&](const Group& now, int g) {
+    uint32_t wd[2][4];
+    spread(now.q[0], wd[0]);
+    spread(now.q[1], wd[1]);
+    const char* at = xl + 64 * PB * MV_G * g;
+    auto block = [&](int j) {
+      const u4 xf = *reinterpret_cast<const u4*>(at + 64 * PB * j);
+      const f4 d = H16::mma16(xf, q4_unpack(wd[j & 1][j >> 1]), (f4)(0.f));
+      const float sf = scale_at(now.s, j);
+#pragma unroll
+      for (int m = 0; m < MA; ++m) acc[m] = fmaf(sf, d[m], acc[m]);
+    };
+    if (MV_G * (g + 1) <= blocks) {                // without branches, so that the blocks overlap
+#pragma unroll
+      for (int j = 0; j < MV_G; ++j) block(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < MV_G; ++j)
+        if (MV_G * g + j < blocks) block(j);
+    }
+  };
+  auto join = [&](int t) {                         // the waves' sums of tile t
+    auto& rd = red[t % RB];
+#pragma unroll
+    for (int m = 0; m < MA; ++m) rd[w][4 * m + kg][r] = acc[m];   // operand row 4 kg + m is column 4 m + kg
+    acc = (f4)(0.f);
+    __syncthreads();
+    for (int e = tid; e < batch * MV_ROWS; e += NT) {
+      const int b = e / MV_ROWS, row = t * MV_ROWS + e % MV_ROWS;
+      if (row >= rows) continue;
+      float v = 0.f, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        v += rd[i][P * b][e % MV_ROWS];
+        if constexpr (P == 2) z += rd[i][P * b + 1][e % MV_ROWS];
+      }
+      if constexpr (P == 2) v = fmaf(z, 1.f / 2048.f, v);
+      v *= inv[b];
+      if (bias) v += bias[row];
+      y_to<Y>(y, b * ldy + row, v);
+    }
+    if (RB == 1) __syncthreads();
+  };
+  int t = t0, g = w;
+  if (w >= groups) {                               // a wave without groups only joins
+    for (; t < t1; ++t) join(t);
+    return;
+  }
+  while (t < t1) {
+#pragma unroll
+    for (int i = 0; i < MV_AHEAD; ++i) {
+      if (t >= t1) break;
+      const Group now = buf[i];
+      ahead(buf[i]);
+      add(now, g);
+      g += W;
+      if (g >= groups) join(t++), g = w;
+    }
+  }
+}
+
+// Products of many columns: one block takes 16 rows, the waves taking groups of
+// 8 blocks in turn; the operand comes from memory (in its second-level cache).
 template <int X, int Y, int MT>
 __global__ void __launch_bounds__(MV_WAVES * WAVE)
 k_matvec(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, const float* __restrict__ bias, int rows,
          int cols, const uint16_t* __restrict__ xo, const float* __restrict__ inv, int batch, void* __restrict__ y,
          int64_t ldy) {
+  constexpr int RT = 1, W = MV_WAVES;
   constexpr int P = parts<X>();
-  __shared__ float red[MV_WAVES][MT * 16][MV_ROWS + 1];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r = lane & 15, kg = lane >> 4;
-  const int row0 = blockIdx.x * MV_ROWS, row = min(row0 + r, rows - 1), blocks = cols / 32;
-  const uint8_t* qr = q + (int64_t)row * (cols / 2);
-  const uint16_t* sr = scale + (int64_t)row * blocks;
+  __shared__ float red[W][MT * 16][MV_ROWS + 1];
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
+            kg = lane >> 4;
+  const int row0 = blockIdx.x * MV_ROWS * RT, blocks = cols / 32, groups = (blocks + MV_G - 1) / MV_G;
   const u4* xl = reinterpret_cast<const u4*>(xo) + lane;
-  f4 acc[MT];
+  f4 acc[RT][MT];
+  Group buf[RT];
+  auto ahead = [&](int g) {
+    if (g >= groups) return;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = (f4)(0.f);
-  for (int j = 4 * w; j < blocks; j += 4 * MV_WAVES) {
-    const int mine = min(j + kg, blocks - 1);
-    const u4 c = *reinterpret_cast<const u4*>(qr + 16 * mine);
-    const uint32_t sc = sr[mine];
-    const auto a = __builtin_amdgcn_permlane16_swap(c[0], c[1], false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(c[2], c[3], false, false);
-    const auto e = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
-    const auto o = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
-    const auto s0 = __builtin_amdgcn_permlane16_swap(sc, sc, false, false);
-    const auto s1 = __builtin_amdgcn_permlane32_swap(s0[0], s0[0], false, false);
-    const auto s2 = __builtin_amdgcn_permlane32_swap(s0[1], s0[1], false, false);
-    const uint32_t wd[4] = {e[0], o[0], e[1], o[1]};
-    const uint32_t sd[4] = {s1[0], s2[0], s1[1], s2[1]};
+    for (int i = 0; i < RT; ++i) {
+      const int row = min(row0 + MV_ROWS * i + r, rows - 1);
+      buf[i] = load_group(q + (int64_t)row * (cols / 2) + 128 * g, scale + (int64_t)row * blocks + MV_G * g, kg,
+                          blocks - MV_G * g);
+    }
+  };
+  ahead(w);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (j + i >= blocks) break;
-      const u4 wf = q4_unpack(wd[i]);
-      const float sf = (float)__builtin_bit_cast(_Float16, (uint16_t)sd[i]);
-      const int kb = j + i;
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const f4 d = H16::mma16(xl[(int64_t)(kb * MT + t) * 64], wf, (f4)(0.f));
+    for (int t = 0; t < MT; ++t) acc[i][t] = (f4)(0.f);
+  for (int g = w; g < groups; g += W) {
+    uint32_t wd[RT][2][4];
+    u4 sc[RT];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) acc[t][m] = fmaf(sf, d[m], acc[t][m]);
+    for (int i = 0; i < RT; ++i) {
+      spread(buf[i].q[0], wd[i][0]);
+      spread(buf[i].q[1], wd[i][1]);
+      sc[i] = buf[i].s;
+    }
+    ahead(g + W);
+    auto block = [&](int j) {
+      u4 xf[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) xf[t] = xl[(int64_t)((MV_G * g + j) * MT + t) * 64];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const u4 wf = q4_unpack(wd[i][j & 1][j >> 1]);
+        const float sf = scale_at(sc[i], j);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const f4 d = H16::mma16(xf[t], wf, (f4)(0.f));
+#pragma unroll
+          for (int m = 0; m < 4; ++m) acc[i][t][m] = fmaf(sf, d[m], acc[i][t][m]);
+        }
       }
+    };
+    if (MV_G * (g + 1) <= blocks) {                // without branches, so that the blocks overlap
+#pragma unroll
+      for (int j = 0; j < MV_G; ++j) block(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < MV_G; ++j)
+        if (MV_G * g + j < blocks) block(j);
     }
   }
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int i = 0; i < RT; ++i) {
+    if (i) __syncthreads();
 #pragma unroll
-    for (int m = 0; m < 4; ++m) red[w][16 * t + 4 * m + kg][r] = acc[t][m];   // operand row 4 kg + m is column 4 m + kg
-  __syncthreads();
-  for (int e = tid; e < batch * MV_ROWS; e += MV_WAVES * WAVE) {
-    const int b = e / MV_ROWS, n = e % MV_ROWS;
-    if (row0 + n >= rows) continue;
-    float v = 0.f, z = 0.f;
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int i = 0; i < MV_WAVES; ++i) {
-      v += red[i][P * b][n];
-      if constexpr (P == 2) z += red[i][P * b + 1][n];
+      for (int m = 0; m < 4; ++m) red[w][16 * t + 4 * m + kg][r] = acc[i][t][m];
+    __syncthreads();
+    for (int e = tid; e < batch * MV_ROWS; e += W * WAVE) {
+      const int b = e / MV_ROWS, n = e % MV_ROWS, row = row0 + MV_ROWS * i + n;
+      if (row >= rows) continue;
+      float v = 0.f, z = 0.f;
+#pragma unroll
+      for (int x = 0; x < W; ++x) {
+        v += red[x][P * b][n];
+        if constexpr (P == 2) z += red[x][P * b + 1][n];
+      }
+      if constexpr (P == 2) v = fmaf(z, 1.f / 2048.f, v);
+      v *= inv[b];
+      if (bias) v += bias[row];
+      y_to<Y>(y, b * ldy + row, v);
     }
-    if constexpr (P == 2) v = fmaf(z, 1.f / 2048.f, v);
-    v *= inv[b];
-    if (bias) v += bias[row0 + n];
-    y_to<Y>(y, b * ldy + row0 + n, v);
   }
 }
 
