@@ -28,21 +28,37 @@ pia::Rows rows_of(const pi_heads* h) {
   return pia::Rows{static_cast<const uint16_t*>(h->p), h->token_stride, h->head_stride};
 }
 
-// shares of a row's keys: four blocks for each compute unit in all, and at least 128 keys a share
-int splits_for(const pi_cache* c, int batch, int heads) {
+// How a decode call is cut up.
+struct Cut {
+  int tiles;      // 16-query tiles of a key head's group, over all key heads
+  int free;       // shares of the rows' keys to deal, beside one for each row; 0: one block a row and tile
+  int blocks;     // for each such tile
+  int qtiles;     // 128-query tiles of a key head over the whole batch, for the common keys
+  int shares;     // of the common keys at most
+};
+Cut cut_of(const pi_cache* c, int batch, int heads) {
+  Cut u{};
   const int group = heads / c->kv_heads;
-  const int64_t rows = (int64_t)batch * c->kv_heads * up_div(group, 16);
-  const int64_t most = up_div((int64_t)c->max_pages * c->page, 128);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({up_div(1024, rows), most, 64}));
+  u.tiles = c->kv_heads * (int)up_div(group, 16);
+  // two blocks for each compute unit, beside a row's first
+  u.free = (int64_t)batch * u.tiles >= pia::DC_ROWS ? 0 : (int)up_div(512, u.tiles);
+  u.blocks = batch + u.free;
+  u.qtiles = (int)up_div((int64_t)batch * group, 128);
+  u.shares = (int)std::max<int64_t>(1, std::min<int64_t>(64, 512 / ((int64_t)u.qtiles * c->kv_heads)));
+  return u;
 }
 
 struct Ws {
-  size_t stat, total;
+  size_t cpart, cstat, part, stat, total;
 };
 Ws ws_of(const pi_cache* c, int batch, int heads) {
-  const size_t rows = (size_t)batch * heads * splits_for(c, batch, heads);
+  const Cut u = cut_of(c, batch, heads);
+  const size_t crows = (size_t)batch * heads * u.shares, rows = (size_t)u.blocks * u.tiles * 16;
   Ws w{};
-  w.stat = ws_align(sizeof(float) * rows * c->dim);
+  w.cpart = ws_align(sizeof(int4) * batch);
+  w.cstat = w.cpart + ws_align(sizeof(float) * crows * c->dim);
+  w.part = w.cstat + ws_align(sizeof(float) * 2 * crows);
+  w.stat = w.part + ws_align(sizeof(float) * rows * c->dim);
   w.total = w.stat + ws_align(sizeof(float) * 2 * rows);
   return w;
 }
@@ -129,9 +145,10 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
   const Ws W = ws_of(cache, batch, heads);
   if (!ws || ws_bytes < W.total || !on(ws, kWsAlign)) return PI_EWORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int splits = splits_for(cache, batch, heads), group = heads / cache->kv_heads, dim = cache->dim;
-  float* part = static_cast<float*>(ws);
-  float* stat = reinterpret_cast<float*>(static_cast<char*>(ws) + W.stat);
+  const Cut u = cut_of(cache, batch, heads);
+  const int dim = cache->dim;
+  char* base = static_cast<char*>(ws);
+  auto floats = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
   const int64_t at = (int64_t)layer * cache->pages * cache->kv_heads * cache->page * dim;
   int32_t* lens = cache->meta + (int64_t)cache->slots * cache->max_pages;
   const pia::Pages pg{static_cast<const uint16_t*>(cache->k) + at,
@@ -146,14 +163,21 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
   (void)hipGetLastError();
   with_type(cache->dtype, dim, [&](auto t, auto d) {
     using T = decltype(t);
-    uint16_t* o = static_cast<uint16_t*>(out->p);
-    hipLaunchKernelGGL((pia::k_attn_decode<T, decltype(d)::value>),
-                       dim3(splits, (unsigned)(cache->kv_heads * up_div(group, 16)), batch),
-                       dim3(pia::DC_WAVES * pia::WAVE), 0, st, pg, rows_of(q), o, out->token_stride, out->head_stride,
-                       seqs, heads, cache->kv_heads, dim, splits, c, part, stat);
-    if (splits > 1)
-      hipLaunchKernelGGL((pia::k_attn_join<T>), dim3((unsigned)(batch * heads)), dim3(dim <= 64 ? 64 : 128), 0, st,
-                         part, stat, o, out->token_stride, out->head_stride, heads, dim, splits, c);
+    constexpr int D = decltype(d)::value;
+    if (prefix)
+      hipLaunchKernelGGL((pia::k_attn_common<T, D>),
+                         dim3((unsigned)(8 * up_div((int64_t)cache->kv_heads * u.shares, 8) * u.qtiles)), dim3(256), 0,
+                         st, pg, rows_of(q), seqs, prefix, batch, heads, cache->kv_heads, dim, u.shares, u.qtiles, c,
+                         floats(W.cpart), floats(W.cstat));
+    hipLaunchKernelGGL((pia::k_attn_decode<T, D>), dim3((unsigned)u.blocks, (unsigned)u.tiles),
+                       dim3(pia::DC_WAVES * pia::WAVE), 0, st, pg, rows_of(q), static_cast<uint16_t*>(out->p),
+                       out->token_stride, out->head_stride, seqs, prefix, batch, heads, cache->kv_heads, dim, u.free,
+                       u.shares, c, reinterpret_cast<int4*>(base), floats(W.part), floats(W.stat));
+    if (prefix || u.free)
+      hipLaunchKernelGGL((pia::k_attn_join<T, D <= 128 ? 2 : 4>), dim3((unsigned)up_div((int64_t)batch * heads, 4)),
+                         dim3(256), 0, st, reinterpret_cast<const int4*>(base), floats(W.cpart), floats(W.cstat),
+                         floats(W.part), floats(W.stat), static_cast<uint16_t*>(out->p), out->token_stride,
+                         out->head_stride, batch, heads, cache->kv_heads, dim, u.shares);
   });
   return launched();
 }

@@ -84,8 +84,7 @@ __device__ __forceinline__ Place find_tile(const int32_t* cu, int n, int tokens,
 // byte lds + 16 i.  Written out because the compiler, which cannot tell buffers of one array apart, would wait for
 // every such load before any read of LDS; `Ring` counts and waits for them.
 __device__ __forceinline__ void to_lds(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
 
 // All but the wave's last N loads have come, its LDS reads are done, and so for every wave of the block.
@@ -384,8 +383,222 @@ struct Pages {
   int pages, page, max_pages, slots;
 };
 
+// The slot of batch row b, or -1.
+__device__ __forceinline__ int slot_of(const int32_t* seqs, int b, int slots) {
+  const int s = seqs ? seqs[b] : b;
+  return (unsigned)s < (unsigned)slots ? s : -1;
+}
+
+// Tokens of batch row b; none where the slot or its length cannot be.
+__device__ __forceinline__ int len_of(const Pages& pg, const int32_t* seqs, int b) {
+  const int slot = slot_of(seqs, b, pg.slots);
+  const int len = slot >= 0 ? pg.lens[slot] : 0;
+  return len < 0 || len > (int64_t)pg.max_pages * pg.page ? 0 : len;
+}
+
+// A prefix that no table row can hold is none.
+__device__ __forceinline__ int common_tokens(const Pages& pg, const int32_t* prefix) {
+  const int n = prefix ? *prefix : 0;
+  return n > 0 && n <= pg.max_pages ? n * pg.page : 0;
+}
+
+// Shares of the common keys: whole tiles, SH_TILES of them at least, and `most` shares at most.  (4096 common keys, 32
+// rows of 64 heads on 8, 128 wide: 37 us a call; with 2 tiles 49 us, with 8 42 us: more shares, more sums to write and
+// join, or fewer blocks.)
+constexpr int SH_TILES = 4;
+__device__ __forceinline__ int shares_of(int total, int most) {
+  const int tiles = (total + PT_K - 1) / PT_K;
+  return max(1, min(most, tiles / SH_TILES));
+}
+
+// ---- the common keys, for all queries of a key head at once.
+//
+// One block of 4 waves: 32 query rows (batch row, head of the group) for each,
+// over one share of the common keys, in tiles of 64 through LDS as in
+// k_attn_prompt, S - 1 of them ahead.  Tiles are found through the pages; 16
+// keys lie in one page.  24 rows of 128 heads on 8, 64 wide, over 32768 common
+// keys: 51 us, 500 TFLOP/s, bound by the exponentials and the latency of a tile's
+// steps with two waves on a SIMD (17 us without the products and exponentials).
+// part, stat: unnormalised sums, and (reference point, l) of each.
+constexpr int SH_IDS = 256;              // places of 16 keys that are looked up at once: 64 tiles
+
+template <class T, int D>
+__global__ void __launch_bounds__(4 * WAVE, D <= 128 ? 2 : 1)
+k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t* __restrict__ prefix, int batch,
+              int heads, int kv_heads, int dim, int shares, int qtiles, float c, float* __restrict__ part,
+              float* __restrict__ stat) {
+  using L = Tile<D>;
+  constexpr int NT = 4 * WAVE, S = D <= 128 ? 3 : 2;
+  using R = Ring<D, S, NT>;
+  __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES];   // K tiles, then V tiles
+  __shared__ int64_t ids[SH_IDS];                  // first element of 16 keys in the layer's pages, or -1
+
+  // the query tiles of one share run on one die (block b runs on die b % 8)
+  const int pair = blockIdx.x % 8 + 8 * (blockIdx.x / (8 * qtiles)), qt = blockIdx.x / 8 % qtiles;
+  const int g = pair / shares, share = pair % shares;
+  if (g >= kv_heads) return;
+  const int total = common_tokens(pg, prefix);
+  if (total == 0) return;
+  const int n = shares_of(total, shares);
+  if (share >= n) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), hi = lane >> 5;
+  int holder = -1;                                 // a batch row whose table names the pages
+  for (int base = 0; base < batch && holder < 0; base += WAVE) {
+    const int b = base + lane;
+    const uint64_t hit = __ballot(b < batch && len_of(pg, seqs, b) >= total);
+    if (hit) holder = base + __ffsll((unsigned long long)hit) - 1;
+  }
+  if (holder < 0) return;
+  const int32_t* table = pg.table + (int64_t)slot_of(seqs, holder, pg.slots) * pg.max_pages;
+
+  const int group = heads / kv_heads, nchunk = dim / 8;
+  const int row0 = 128 * qt + 32 * w, row = row0 + (lane & 31);
+  const bool live = row0 < batch * group;
+  const int b = min(row / group, batch - 1), head = g * group + row % group;
+  u4 qf[L::KS];
+#pragma unroll
+  for (int s = 0; s < L::KS; ++s) {
+    const int at = 2 * s + hi;
+    qf[s] = at < nchunk ? *reinterpret_cast<const u4*>(q.at(b, head) + 8 * at) : u4{0, 0, 0, 0};
+  }
+  if (nchunk < L::NC) {                            // chunks that no load fills
+    for (int e = tid; e < 2 * S * R::BYTES / 16; e += NT) reinterpret_cast<u4*>(ring)[e] = u4{0, 0, 0, 0};
+  }
+  const int tiles = (total + PT_K - 1) / PT_K;
+  const int first = tiles * share / n, last = tiles * (share + 1) / n;   // 2^25 tiles and 64 shares at most
+  const int r0 = tid / L::NC;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * w;
+  const int per = pg.page / 16;
+  // the places of the tiles from `base` on; whether one of them is broken
+  auto look_up = [&](int base) {
+    bool bad = false;
+    const int at = 4 * base + tid;
+    if (at < 4 * last) {
+      const int x = min(at, total / 16 - 1), id = table[x / per];
+      bad = (unsigned)id >= (unsigned)pg.pages;
+      ids[tid] = bad ? -1 : (((int64_t)id * kv_heads + g) * pg.page + x % per * 16) * dim;
+      if (bad) atomicOr(pg.flags, PI_CACHE_EPAGE);
+    }
+    return __syncthreads_or(bad) != 0;
+  };
+  auto place = [&](int at) {
+    const int64_t v = ids[at];
+    const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)v), h = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (int64_t)((uint64_t)h << 32 | a);
+  };
+  // a tile into LDS; keys of a broken page are zeros
+  auto fetch = [&](int tile, int base) {
+#pragma unroll
+    for (int i = 0; i < R::LD; ++i) {
+      const int r = i * R::RN + r0, ch = (tid % L::NC) ^ L::swz(r);
+      const int rw = i * R::RN + 64 * w / L::NC;   // the wave's first row: its rows lie in one page
+      const int64_t at = place(4 * (tile - base) + rw / 16);
+      const uint32_t to = lds0 + tile % S * R::BYTES + i * 16 * NT;
+      if (at >= 0) {
+        const uint32_t off = 2 * (uint32_t)(r % 16 * dim + 8 * ch);
+        if (ch < nchunk) {
+          to_lds(pg.k + at, off, to);
+          to_lds(pg.v + at, off, to + S * R::BYTES);
+        }
+      } else {
+        char* own = ring + tile % S * R::BYTES + i * 16 * NT + 16 * tid;
+        *reinterpret_cast<u4*>(own) = *reinterpret_cast<u4*>(own + S * R::BYTES) = u4{0, 0, 0, 0};
+      }
+    }
+  };
+  // Tiles are fetched S - 1 ahead.  For each on its way, four bits say which of its 16-key places are seen; the next
+  // tile's are the lowest.
+  int base = first;
+  bool broken = look_up(base), any = broken;
+  uint32_t seen = 0;
+  auto ahead = [&](int t) {                        // the place of tile t - S has been read by every wave
+    if (t - base == SH_IDS / 4) {
+      __syncthreads();                             // as have the ids
+      base = t;
+      broken = look_up(base);
+      any |= broken;
+    }
+    uint32_t bits = 15;
+    if (broken) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (place(4 * (t - base) + i) < 0) bits &= ~(1u << i);
+    }
+    if (total - t * PT_K < PT_K) bits &= (1u << (total - t * PT_K) / 16) - 1;
+    seen |= bits << 4 * (t % S);
+    fetch(t, base);
+  };
+  for (int t = first; t < min(last, first + S - 1); ++t) ahead(t);
+  // what was fetched for the S - 2 tiles behind this one may still be on its way; at the end, and where a broken page's
+  // keys were not loaded, there are fewer
+  auto turn = [&](int t) {
+    if (t + S - 2 < last && !any) arrive<(S - 2) * 2 * R::LD>();
+    else arrive<0>();
+    const uint32_t sees = seen >> 4 * (t % S) & 15;
+    seen &= ~(15u << 4 * (t % S));
+    if (t + S - 1 < last) ahead(t + S - 1);
+    return sees;
+  };
+  if (!live) {                                     // the wave has nothing to do but keep step
+    for (int t = first; t < last; ++t) turn(t);
+    arrive<0>();
+    return;
+  }
+  const Reads<D> rd(lane);
+  Sums<T, D> sum;
+  sum.clear();
+  for (int t = first; t < last; ++t) {
+    const uint32_t sees = turn(t);
+    const char *sk = ring + t % S * R::BYTES, *sv = ring + (S + t % S) * R::BYTES;
+    f16v s[2];
+    uint32_t pw[16];
+    if (sees == 15) {
+      sum.scores(sk, qf, rd, s);
+      sum.weigh(s, c, pw);
+      sum.add(sv, pw, rd);
+    } else {
+      sum.scores(sk, qf, rd, s);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(sees >> (2 * h + i / 8) & 1)) s[h][i] = NEG_INF;
+      sum.weigh(s, c, pw);
+      sum.add(sv, pw, rd);
+    }
+  }
+  // 64 dims at a time through LDS, so that rows are written whole
+  arrive<0>();
+  float* own = reinterpret_cast<float*>(ring) + w * 32 * 68;
+  const int rows = min(32, batch * group - row0);
+  auto place_of = [&](int x) { return ((int64_t)(x / group) * heads + g * group + x % group) * shares + share; };
+#pragma unroll
+  for (int t0 = 0; t0 < L::DT; t0 += 2) {
+#pragma unroll
+    for (int t = t0; t < min(t0 + 2, L::DT); ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<f4*>(own + (lane & 31) * 68 + 32 * (t - t0) + 8 * (i / 4) + 4 * hi) =
+            f4{sum.o[t][i], sum.o[t][i + 1], sum.o[t][i + 2], sum.o[t][i + 3]};
+    __builtin_amdgcn_wave_barrier();
+    const int d = 32 * t0 + 4 * (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = 4 * i + lane / 16;
+      const f4 y = *reinterpret_cast<const f4*>(own + x * 68 + 4 * (lane & 15));
+      if (x < rows && d < dim && 4 * (lane & 15) < 32 * (L::DT - t0)) *reinterpret_cast<f4*>(part + place_of(row0 + x) * dim + d) = y;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  const float l = sum32(sum.l);
+  if (hi == 0 && lane < rows) *reinterpret_cast<float2*>(stat + 2 * place_of(row)) = float2{sum.mc, l};
+}
+
+// ---- the keys of each row's own.
 constexpr int DC_WAVES = 4;
 constexpr int DC_K = 32;                 // keys of a wave's step
+constexpr int DC_MOST = 128;             // shares of a row at most
+constexpr int DC_ROWS = 1024;            // tiles of queries from which on a row has one share
 
 // O^T of the 16x16x32 product: a lane's A operand row l % 16 stands for VW
 // consecutive output dims (VW operands), so V is loaded with VW elements per
@@ -396,38 +609,94 @@ template <int D> struct Vec {
   static constexpr int KS = (D + 31) / 32;         // k steps of Q K^T
 };
 
-// The slot of batch row b, or -1.
-__device__ __forceinline__ int slot_of(const int32_t* seqs, int b, int slots) {
-  const int s = seqs ? seqs[b] : b;
-  return (unsigned)s < (unsigned)slots ? s : -1;
+// A block's batch row, its slot and tokens, and which of how many shares of its own keys the block takes.
+struct Share {
+  int b, slot, len, i, n;                // n = 0: nothing to do
+};
+
+// 128 keys are a unit of work.  `free` shares are dealt to the rows, of `size` units each (the last of a row may be
+// smaller), so that all rows together take no more than one share each beside them.
+__device__ __forceinline__ uint32_t share_size(uint64_t all, int free) {
+  int s = 0;                                       // 32-bit division: what is lost of `all` is made up for
+  while (all >> s >> 31) ++s;
+  return max(1u, ((uint32_t)(all >> s) + free - 1) / free << s) + (s ? 1u << s : 0u);
+}
+__device__ __forceinline__ int deal(int units, uint32_t size) {
+  return max(1, min(DC_MOST, (int)(((uint32_t)units + size - 1) / size)));
+}
+__device__ __forceinline__ int units_of(int keys) { return (keys + DC_WAVES * DC_K - 1) / (DC_WAVES * DC_K); }
+
+__device__ __forceinline__ Share find_share(const Pages& pg, const int32_t* seqs, int batch, int total, int idx, int free) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  int slot = -1, len = 0;                          // of row base + lane
+  auto units = [&](int b) {
+    slot = b < batch ? slot_of(seqs, b, pg.slots) : -1;
+    len = slot >= 0 ? pg.lens[slot] : 0;
+    const int n = len < 0 || len > (int64_t)pg.max_pages * pg.page ? 0 : len;
+    return units_of(n - (n >= total ? total : 0));
+  };
+  // of one row at most 2^24 units: 64 rows fit 32 bits
+  int mine = units(lane);
+  int64_t all = __builtin_amdgcn_readlane(scan64(mine), WAVE - 1);
+  for (int base = WAVE; base < batch; base += WAVE) all += __builtin_amdgcn_readlane(scan64(units(base + lane)), WAVE - 1);
+  const uint32_t size = share_size(all, free);
+  for (int base = 0; base < batch; base += WAVE) {
+    if (batch > WAVE) mine = units(base + lane);
+    const int n = base + lane < batch ? deal(mine, size) : 0;
+    const int upto = scan64(n);
+    const uint64_t hit = __ballot(upto > idx);
+    if (hit) {
+      const int l = __ffsll((unsigned long long)hit) - 1;
+      const int count = __builtin_amdgcn_readlane(n, l);
+      return Share{base + l, __builtin_amdgcn_readlane(slot, l), __builtin_amdgcn_readlane(len, l),
+                   idx - (__builtin_amdgcn_readlane(upto, l) - count), count};
+    }
+    idx -= __builtin_amdgcn_readlane(upto, WAVE - 1);
+  }
+  return Share{0, -1, 0, 0, 0};
 }
 
 // One block: the query heads [16 rt, 16 rt + 16) of a key head's group, one
-// batch row, and one of `splits` shares of its keys; the waves take steps of 32
-// keys in turn and join their sums through LDS.  Partial results (or, with one
-// share, the output) are written per query head.
+// batch row, and one share of the keys behind the common ones; the waves take
+// steps of 32 keys in turn and join their sums through LDS.  Where a row has
+// one share and no common keys its result is written; else the sums go to
+// `part` and `stat` and the row's shares to `plan`, for k_attn_join.  (Joining
+// in the row's last block instead costs more: its loads have to pass the die's
+// cache.  1500 tokens: 16 us, not 13; with an agent-scope fence 52 us.)
+// `free` is 0 where every row has one share: the block's number is the row's.
 template <class T, int D>
-__global__ void __launch_bounds__(DC_WAVES * WAVE)
+__global__ void __launch_bounds__(DC_WAVES * WAVE, D <= 128 ? 2 : 1)
 k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head,
-              const int32_t* __restrict__ seqs, int heads, int kv_heads, int dim, int splits, float c,
-              float* __restrict__ part, float* __restrict__ stat) {
+              const int32_t* __restrict__ seqs, const int32_t* __restrict__ prefix, int batch, int heads, int kv_heads,
+              int dim, int free, int shares, float c, int4* __restrict__ plan, float* __restrict__ part,
+              float* __restrict__ stat) {
   using V = Vec<D>;
   constexpr int NF = V::W * V::G;                  // operands of the second product
+  constexpr int ROW = 16 * NF + 4;
   __shared__ float sm[DC_WAVES][2][16];
-  __shared__ float so[DC_WAVES][16][16 * NF + 4];
+  __shared__ float so[DC_WAVES][16][ROW];
 
-  const int b = blockIdx.z, split = blockIdx.x, group = heads / kv_heads;
-  const int rts = (group + 15) / 16, g = blockIdx.y / rts, rt = blockIdx.y % rts;
+  const int group = heads / kv_heads, rts = (group + 15) / 16, g = blockIdx.y / rts, rt = blockIdx.y % rts;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kg = lane >> 4;
-  const int slot = slot_of(seqs, b, pg.slots);
-  int len = slot >= 0 ? pg.lens[slot] : 0;
+  const int total = common_tokens(pg, prefix);
+  Share me;
+  if (free) {
+    me = find_share(pg, seqs, batch, total, blockIdx.x, free);
+    if (me.n == 0) return;
+  } else {
+    const int slot = slot_of(seqs, blockIdx.x, pg.slots);
+    me = Share{(int)blockIdx.x, slot, slot >= 0 ? pg.lens[slot] : 0, 0, 1};
+  }
+  const int b = me.b, slot = me.slot;
+  int len = me.len;
   if (slot < 0 || len < 0 || len > (int64_t)pg.max_pages * pg.page) {
     if (tid == 0) atomicOr(pg.flags, slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
     len = 0;
   }
-  const int steps = (len + DC_K - 1) / DC_K;
-  const int first = (int)((int64_t)steps * split / splits), last = (int)((int64_t)steps * (split + 1) / splits);
+  const int from = total > 0 && len >= total ? total : 0;
+  const int steps = (len - from + DC_K - 1) / DC_K;
+  const int first = (int)((int64_t)steps * me.i / me.n), last = (int)((int64_t)steps * (me.i + 1) / me.n);
   const int nchunk = dim / 8;
 
   const int head = g * group + 16 * rt + min(r, group - 16 * rt - 1);
@@ -440,7 +709,7 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
   f4 o[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) o[f] = (f4)(0.f);
-  float m = NEG_INF, l = 0.f;
+  float mc = NEG_INF, l = 0.f;                     // mc: c times the largest score so far
   const int32_t* row = pg.table + (int64_t)max(slot, 0) * pg.max_pages;
   const int64_t head_stride = (int64_t)pg.page * dim, page_stride = head_stride * kv_heads;
 
@@ -450,7 +719,7 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
     int seen[2];                                   // keys of the half that exist
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int key = st * DC_K + 16 * h;
+      const int key = from + st * DC_K + 16 * h;
       seen[h] = max(0, min(16, len - key));
       const int place = min(key / pg.page, pg.max_pages - 1);
       int id = row[place];
@@ -463,17 +732,39 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
       kp[h] = pg.k + at;
       vp[h] = pg.v + at;
     }
+    // all of the step's loads are on their way before the first product; keys that do not exist lie in a page all the same
+    u4 kf[2][V::KS];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int ks = 0; ks < V::KS; ++ks) {
+        const int ch = 4 * ks + kg;
+        kf[h][ks] = *reinterpret_cast<const u4*>(kp[h] + r * dim + 8 * min(ch, nchunk - 1));
+        if (ch >= nchunk) kf[h][ks] = u4{0, 0, 0, 0};
+      }
+    uint32_t x[V::G][8][V::W / 2];                 // V: keys 4 kg + 0..3 of both halves
+#pragma unroll
+    for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d0 = (16 * gr + r) * V::W;
+        const uint16_t* src = vp[i / 4] + (4 * kg + i % 4) * dim + (d0 < dim ? d0 : 0);
+        if constexpr (V::W == 8) {
+          const u4 y = *reinterpret_cast<const u4*>(src);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[gr][i][e] = y[e];
+        } else {
+          const u2 y = *reinterpret_cast<const u2*>(src);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[gr][i][e] = y[e];
+        }
+      }
     f4 s[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       s[h] = (f4)(0.f);
 #pragma unroll
-      for (int ks = 0; ks < V::KS; ++ks) {
-        const int ch = 4 * ks + kg;
-        u4 a = {0, 0, 0, 0};
-        if (ch < nchunk) a = *reinterpret_cast<const u4*>(kp[h] + r * dim + 8 * ch);
-        s[h] = T::mma16(a, qf[ks], s[h]);
-      }
+      for (int ks = 0; ks < V::KS; ++ks) s[h] = T::mma16(kf[h][ks], qf[ks], s[h]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (4 * kg + i >= seen[h]) s[h][i] = NEG_INF;
@@ -481,46 +772,36 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
     float mt = NEG_INF;
 #pragma unroll
     for (int i = 0; i < 4; ++i) mt = fmaxf(mt, fmaxf(s[0][i], s[1][i]));
-    const float mn = fmaxf(m, max16(mt));
-    const float mc = mn == NEG_INF ? 0.f : mn * c;   // see k_attn_prompt
-    const float alpha = exp2_fast(fmaf(m, c, -mc));
-    m = mn;
+    const float top = fmaxf(mc, max16(mt) * c);
+    const float base = top == NEG_INF ? 0.f : top;   // rows whose scores so far are all -inf
+    const float alpha = exp2_fast(mc - base);
+    mc = top;
     float p[8], ls = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = exp2_fast(fmaf(s[i / 4][i % 4], c, -mc));
+      p[i] = exp2_fast(fmaf(s[i / 4][i % 4], c, -base));
       ls += p[i];
     }
     l = fmaf(l, alpha, ls);
     const u4 pf = {T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
-    // V: keys 4 kg + 0..3 of both halves; rows that do not exist count as zeros, whatever is stored there
+    // rows that do not exist count as zeros, whatever is stored there
+    if (seen[0] < 16 || seen[1] < 16) {
 #pragma unroll
-    for (int gr = 0; gr < V::G; ++gr) {
-      uint32_t x[8][V::W / 2];
-      const int d0 = (16 * gr + r) * V::W;
+      for (int i = 0; i < 8; ++i)
+        if (4 * kg + i % 4 >= seen[i / 4])
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = 4 * kg + i % 4;
+          for (int gr = 0; gr < V::G; ++gr)
 #pragma unroll
-        for (int e = 0; e < V::W / 2; ++e) x[i][e] = 0;
-        if (key < seen[i / 4] && d0 < dim) {
-          const uint16_t* src = vp[i / 4] + key * dim + d0;
-          if constexpr (V::W == 8) {
-            const u4 y = *reinterpret_cast<const u4*>(src);
+            for (int e = 0; e < V::W / 2; ++e) x[gr][i][e] = 0;
+    }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][e] = y[e];
-          } else {
-            const u2 y = *reinterpret_cast<const u2*>(src);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[i][e] = y[e];
-          }
-        }
-      }
+    for (int gr = 0; gr < V::G; ++gr)
 #pragma unroll
       for (int e = 0; e < V::W / 2; ++e) {
-        const u4 a = {lows(x[0][e], x[1][e]), lows(x[2][e], x[3][e]), lows(x[4][e], x[5][e]), lows(x[6][e], x[7][e])};
-        const u4 z = {highs(x[0][e], x[1][e]), highs(x[2][e], x[3][e]), highs(x[4][e], x[5][e]),
-                      highs(x[6][e], x[7][e])};
+        auto& y = x[gr];
+        const u4 a = {lows(y[0][e], y[1][e]), lows(y[2][e], y[3][e]), lows(y[4][e], y[5][e]), lows(y[6][e], y[7][e])};
+        const u4 z = {highs(y[0][e], y[1][e]), highs(y[2][e], y[3][e]), highs(y[4][e], y[5][e]),
+                      highs(y[6][e], y[7][e])};
         const int f = gr * V::W + 2 * e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -530,13 +811,12 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
         o[f] = T::mma16(a, pf, o[f]);
         o[f + 1] = T::mma16(z, pf, o[f + 1]);
       }
-    }
   }
   l = sum16(l);
 
   // join the waves: o[f][i] belongs to dim (16 gr + 4 kg + i) W + f % W of query r
   if (lane < 16) {
-    sm[w][0][r] = m;
+    sm[w][0][r] = mc;
     sm[w][1][r] = l;
   }
 #pragma unroll
@@ -546,54 +826,107 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
 #pragma unroll
       for (int f = 0; f < V::W; ++f) so[w][r][(16 * gr + 4 * kg + i) * V::W + f] = o[gr * V::W + f][i];
   __syncthreads();
-  for (int e = tid; e < 16 * dim; e += DC_WAVES * WAVE) {
+  const int queries = min(16, group - 16 * rt), common = from > 0 ? shares_of(total, shares) : 0;
+  const bool whole = me.n == 1 && common == 0;
+  const int64_t mine = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;   // this block's place among the parts
+  uint16_t* dst = out + b * out_token + (g * group + 16 * rt) * out_head;
+  for (int e = 2 * tid; e < queries * dim; e += 2 * DC_WAVES * WAVE) {
     const int qr = e / dim, d = e % dim;
-    if (16 * rt + qr >= group) break;
     float mm = NEG_INF;
 #pragma unroll
     for (int i = 0; i < DC_WAVES; ++i) mm = fmaxf(mm, sm[i][0][qr]);
-    const float mc = mm == NEG_INF ? 0.f : mm * c;
-    float ll = 0.f, oo = 0.f;
+    const float base = mm == NEG_INF ? 0.f : mm;
+    float ll = 0.f, oo = 0.f, od = 0.f;
 #pragma unroll
     for (int i = 0; i < DC_WAVES; ++i) {
-      const float a = exp2_fast(fmaf(sm[i][0][qr], c, -mc));
+      const float a = exp2_fast(sm[i][0][qr] - base);
       ll = fmaf(sm[i][1][qr], a, ll);
       oo = fmaf(so[i][qr][d], a, oo);
+      od = fmaf(so[i][qr][d + 1], a, od);
     }
-    const int h = g * group + 16 * rt + qr;
-    if (splits == 1) {
-      const float y = ll == 0.f ? 0.f : oo / ll;   // a row that sees no key is zero
-      out[b * out_token + h * out_head + d] = (uint16_t)T::pack(y, 0.f);
+    if (whole) {
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;   // a row that sees no key is zero
+      *reinterpret_cast<uint32_t*>(dst + qr * out_head + d) = T::pack(oo * inv, od * inv);
     } else {
-      const int64_t at = ((int64_t)b * heads + h) * splits + split;
-      part[at * dim + d] = oo;
-      if (d == 0) {
-        stat[2 * at] = mm;
-        stat[2 * at + 1] = ll;
-      }
+      *reinterpret_cast<float2*>(part + (16 * mine + qr) * dim + d) = float2{oo, od};
+      if (d == 0) *reinterpret_cast<float2*>(stat + 2 * (16 * mine + qr)) = float2{mm, ll};
     }
   }
+  // the row's first share, how many there are (0: the result is written), and those of the common keys
+  if (me.i == 0 && blockIdx.y == 0 && tid == 0) plan[b] = int4{(int)blockIdx.x, whole ? 0 : me.n, common, 0};
 }
 
-// Join a row's shares: one block per (batch row, query head).
-template <class T>
+// Join the shares of a query: one wave each, W dims a lane.
+template <class T, int W>
 __global__ void __launch_bounds__(256)
-k_attn_join(const float* __restrict__ part, const float* __restrict__ stat, uint16_t* __restrict__ out,
-            int64_t out_token, int64_t out_head, int heads, int dim, int splits, float c) {
-  const int b = blockIdx.x / heads, h = blockIdx.x % heads;
-  const float* st = stat + 2 * (int64_t)blockIdx.x * splits;
-  float mm = NEG_INF;
-  for (int i = 0; i < splits; ++i) mm = fmaxf(mm, st[2 * i]);
-  const float mc = mm == NEG_INF ? 0.f : mm * c;
-  for (int d = threadIdx.x; d < dim; d += blockDim.x) {
-    float ll = 0.f, oo = 0.f;
-    for (int i = 0; i < splits; ++i) {
-      const float a = exp2_fast(fmaf(st[2 * i], c, -mc));
-      ll = fmaf(st[2 * i + 1], a, ll);
-      oo = fmaf(part[((int64_t)blockIdx.x * splits + i) * dim + d], a, oo);
-    }
-    out[b * out_token + h * out_head + d] = (uint16_t)T::pack(ll == 0.f ? 0.f : oo / ll, 0.f);
+k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, const float* __restrict__ cstat,
+            const float* __restrict__ part, const float* __restrict__ stat, uint16_t* __restrict__ out,
+            int64_t out_token, int64_t out_head, int batch, int heads, int kv_heads, int dim, int shares) {
+  typedef float Dims __attribute__((ext_vector_type(W)));
+  __shared__ float weight[4][DC_MOST + 64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * 4 + w;
+  if (row >= (int64_t)batch * heads) return;
+  const int b = (int)(row / heads), h = (int)(row % heads), group = heads / kv_heads, rts = (group + 15) / 16;
+  const int4 pl = plan[b];
+  if (pl.y == 0) return;
+  const int tiles = kv_heads * rts, tile = h / group * rts + h % group / 16;
+  const int64_t own0 = ((int64_t)pl.x * tiles + tile) * 16 + h % group % 16, own1 = 16 * (int64_t)tiles;
+  const int n = pl.y, all = n + pl.z;
+  const int d = min(W * lane, dim - W);
+  // the first sums are on their way while the weights are made
+  auto at = [&](int i) {
+    const float* p = i < n ? part + (own0 + i * own1) * dim : cpart + (row * shares + i - n) * dim;
+    return *reinterpret_cast<const Dims*>(p + d);
+  };
+  constexpr int AHEAD = 16;
+  Dims y[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) y[i] = at(min(i, all - 1));
+  constexpr int PER = (DC_MOST + 64) / 64;
+  float2 st[PER];
+  float mm = NEG_INF, ll = 0.f;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = min(64 * j + lane, all - 1);
+    st[j] = *reinterpret_cast<const float2*>(i < n ? stat + 2 * (own0 + i * own1) : cstat + 2 * (row * shares + i - n));
+    mm = fmaxf(mm, st[j].x);
   }
+#pragma unroll
+  for (int x = 32; x; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+  const float base = mm == NEG_INF ? 0.f : mm;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = 64 * j + lane;
+    if (i < all) {
+      const float a = exp2_fast(st[j].x - base);
+      weight[w][i] = a;
+      ll = fmaf(st[j].y, a, ll);
+    }
+  }
+#pragma unroll
+  for (int x = 32; x; x >>= 1) ll += __shfl_xor(ll, x);
+  // a wave reads its own weights only
+  __builtin_amdgcn_wave_barrier();
+  Dims sum = (Dims)(0.f);
+  for (int base_i = 0; base_i < all; base_i += AHEAD) {
+    if (base_i) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) y[i] = at(min(base_i + i, all - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (base_i + i < all) {
+        const float a = weight[w][base_i + i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum[j] = fmaf(y[i][j], a, sum[j]);
+      }
+  }
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;    // a row that sees no key is zero
+  uint16_t* dst = out + b * out_token + h * out_head + d;
+  if (W * lane >= dim) return;
+  if constexpr (W == 4) *reinterpret_cast<u2*>(dst) = u2{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
+  else *reinterpret_cast<uint32_t*>(dst) = T::pack(sum[0] * inv, sum[1] * inv);
 }
 
 }  // namespace pia

@@ -66,8 +66,8 @@ pi_status pih::check_cache(const pi_cache* c) {
   if (c->dim % 8 != 0 || c->page % 16 != 0) return PI_EINVAL;
   if (c->dim > 256 || c->page > 4096 || c->kv_heads > 1024 || c->pages > (1 << 20) || c->layers > 16384)
     return PI_EUNSUPPORTED;
-  // lengths and table entries are 32-bit
-  if ((int64_t)c->max_pages * c->page > INT32_MAX || (int64_t)c->slots * c->max_pages > (int64_t(1) << 30))
+  // lengths, with a tile of keys behind them, and table entries are 32-bit
+  if ((int64_t)c->max_pages * c->page > INT32_MAX - 127 || (int64_t)c->slots * c->max_pages > (int64_t(1) << 30))
     return PI_EUNSUPPORTED;
   return PI_OK;
 }

@@ -250,7 +250,8 @@ typedef struct {
 
 /* A paged key/value cache of `slots` sequences.
  *  k, v:  [layers][pages][kv_heads][page][dim], 16-byte aligned; page a
- *         multiple of 16, at most 4096; pages <= 2^20.
+ *         multiple of 16, at most 4096; pages <= 2^20; max_pages page
+ *         <= 2^31 - 128.
  *  meta:  int32, pi_cache_meta_words(slots, max_pages, pages) of them:
  *           table [slots][max_pages]  pages of a sequence, in order
  *           lens  [slots]             its tokens
@@ -318,7 +319,8 @@ pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v
  * prefix: NULL, or one int32 on the device: how many leading pages all the
  * batch's slots that are not empty have in common, page for page.  These are
  * read once for the whole batch.  The pages of a slot that is too short to
- * hold them do not count as common.
+ * hold them do not count as common, and a number that no table row can hold
+ * counts as 0.
  */
 size_t pi_attn_workspace_bytes(const pi_cache* cache, int32_t batch, int32_t heads);
 pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q, const pi_heads* out, int32_t batch,
