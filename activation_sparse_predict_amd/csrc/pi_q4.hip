@@ -13,14 +13,23 @@ namespace {
 // 12288 float32 values; with the sums of the waves (9 KB) a block keeps to 64 KB
 constexpr size_t kOperandLds = 48 << 10;
 
-// the operand made of x, of the largest number of columns a type of x takes, and a row's scale
+// Shares of the groups of 8 blocks in a product of many columns: two blocks for each compute unit, at most 32 shares.
+int shares_of(int32_t rows, int32_t cols) {
+  const int64_t groups = up_div(cols, 32 * piq::MV_G), blocks = up_div(rows, piq::MV_ROWS * piq::MV_WAVES);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({up_div(512, blocks), groups, 32}));
+}
+
+// the operand made of x, whole groups of it, of the largest number of columns a type of x takes; a row's scale; the
+// shares' sums
 struct Ws {
-  size_t inv, total;
+  size_t inv, part, total;
 };
-Ws ws_of(int32_t cols, int32_t batch) {
+Ws ws_of(int32_t rows, int32_t cols, int32_t batch) {
   Ws w{};
-  w.inv = ws_align((size_t)up_div(2 * batch, 16) * 16 * cols * sizeof(uint16_t));
-  w.total = w.inv + ws_align(sizeof(float) * 32);
+  const size_t padded = (size_t)up_div(cols, 32 * piq::MV_G) * 32 * piq::MV_G;
+  w.inv = ws_align((size_t)up_div(2 * batch, 16) * 16 * padded * sizeof(uint16_t));
+  w.part = w.inv + ws_align(sizeof(float) * 32);
+  w.total = w.part + ws_align(sizeof(float) * 2 * batch * (size_t)rows * shares_of(rows, cols));
   return w;
 }
 
@@ -28,7 +37,7 @@ int size_of(int32_t dtype) { return dtype == PI_F32 ? 4 : 2; }
 
 pi_status check_sizes(int32_t rows, int32_t cols, int32_t batch) {
   if (rows < 1 || cols < 32 || cols % 32 != 0 || batch < 1 || batch > 32) return PI_EINVAL;
-  return rows > (1 << 28) || cols > (1 << 22) ? PI_EUNSUPPORTED : PI_OK;
+  return rows > (1 << 22) || cols > (1 << 22) ? PI_EUNSUPPORTED : PI_OK;
 }
 
 // f(constant of the dtype)
@@ -44,7 +53,7 @@ void with_dtype(int32_t dtype, F f) {
 extern "C" {
 
 size_t pi_matvec_workspace_bytes(int32_t rows, int32_t cols, int32_t batch) {
-  return check_sizes(rows, cols, batch) == PI_OK ? ws_of(cols, batch).total : 0;
+  return check_sizes(rows, cols, batch) == PI_OK ? ws_of(rows, cols, batch).total : 0;
 }
 
 pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* bias, const void* x, int32_t x_dtype,
@@ -56,7 +65,7 @@ pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* 
   for (int32_t t : {x_dtype, y_dtype})
     if (t != PI_F32 && t != PI_F16 && t != PI_BF16) return PI_EINVAL;
   if (!x || !on(x, size_of(x_dtype)) || !y || !on(y, size_of(y_dtype)) || ldx < cols || ldy < rows) return PI_EINVAL;
-  const Ws W = ws_of(cols, batch);
+  const Ws W = ws_of(rows, cols, batch);
   if (!ws || ws_bytes < W.total || !on(ws, kWsAlign)) return PI_EWORKSPACE;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint16_t* xo = static_cast<uint16_t*>(ws);
@@ -67,7 +76,7 @@ pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* 
     const int columns = P * batch;
     // few columns whose operand fits beside another block's in LDS: each block makes it for itself
     const size_t lds = (size_t)2 * columns * cols;
-    const bool few = columns <= 16 && lds <= kOperandLds;
+    const bool few = columns <= 16 && lds <= kOperandLds, tiny = cols < 32 * piq::MV_G;
     const int tiles = (int)up_div(columns, 16);
     if (!few)
       hipLaunchKernelGGL((piq::k_mv_operand<X>), dim3(16 * tiles / P, (unsigned)std::min<int64_t>(16, up_div(cols, 1024))),
@@ -79,20 +88,30 @@ pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* 
         auto go = [&](auto ma) {
           // as many blocks as fit at once (up to four a compute unit), each with an even share of the row tiles
           const int64_t fit = std::min<int64_t>(4, (160 << 10) / (int64_t)(lds + (10 << 10)));
-          hipLaunchKernelGGL((piq::k_matvec_few<X, Y, decltype(ma)::value>),
-                             dim3((unsigned)std::min(up_div(rows, piq::MV_ROWS), 256 * fit)),
-                             dim3(piq::MV_WAVES * piq::WAVE), lds, st, w_of, mat->scale, bias, rows, cols, x, ldx,
-                             batch, y, ldy);
+          auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)std::min(up_div(rows, piq::MV_ROWS), 256 * fit)),
+                               dim3(piq::MV_WAVES * piq::WAVE), lds, st, w_of, mat->scale, bias, rows, cols, x, ldx,
+                               batch, y, ldy);
+          };
+          if (tiny) launch(piq::k_matvec_few<X, Y, decltype(ma)::value, true>);
+          else launch(piq::k_matvec_few<X, Y, decltype(ma)::value, false>);
         };
         if (columns <= 4) go(std::integral_constant<int, 1>());
         else if (columns <= 8) go(std::integral_constant<int, 2>());
         else go(std::integral_constant<int, 4>());
         return;
       }
+      const int shares = shares_of(rows, cols);
+      float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + W.part);
       auto go = [&](auto mt) {
-        hipLaunchKernelGGL((piq::k_matvec<X, Y, decltype(mt)::value>),
-                           dim3((unsigned)up_div(rows, piq::MV_ROWS)), dim3(piq::MV_WAVES * piq::WAVE), 0, st, w_of,
-                           mat->scale, bias, rows, cols, xo, inv, batch, y, ldy);
+        auto launch = [&](auto kernel) {
+          hipLaunchKernelGGL(kernel, dim3((unsigned)up_div(rows, piq::MV_ROWS * piq::MV_WAVES), (unsigned)shares),
+                             dim3(piq::MV_WAVES * piq::WAVE), 0, st, w_of, mat->scale, rows, cols, xo, columns, part);
+        };
+        if (tiny) launch(piq::k_matvec<decltype(mt)::value, true>);
+        else launch(piq::k_matvec<decltype(mt)::value, false>);
+        hipLaunchKernelGGL((piq::k_matvec_join<P, Y>), dim3((unsigned)up_div(rows, 256), (unsigned)batch), dim3(256), 0,
+                           st, part, inv, bias, rows, shares, batch, y, ldy);
       };
       if (tiles == 1) go(std::integral_constant<int, 1>());
       else if (tiles == 2) go(std::integral_constant<int, 2>());

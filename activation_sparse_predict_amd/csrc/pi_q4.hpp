@@ -26,7 +26,7 @@ using namespace pit;
 constexpr int MV_ROWS = 16;              // matrix rows of a tile
 constexpr int MV_G = 8;                  // 32-blocks of a group: 128 bytes of a row's nibbles, one cache line
 constexpr int MV_WAVES = 8;              // waves of a block
-constexpr int MV_AHEAD = 3;              // groups of a wave on their way
+constexpr int MV_AHEAD = 2;              // groups of a wave on their way
 
 // Load one element of x, stored as dtype X (pi_dtype), as float32.
 template <int X> __device__ __forceinline__ float x_at(const void* p, int64_t i) {
@@ -160,8 +160,8 @@ k_mv_operand(const void* __restrict__ x, int64_t ldx, int batch, int cols, int t
   }
 }
 
-// A lane's share of a group of 8 blocks of one row tile: lane (r, kg) holds blocks 8 j + 2 kg and + 1 of row r, and
-// the scales of all eight.
+// A lane's share of 8 blocks of one row tile: lane (r, kg) holds blocks 2 kg and 2 kg + 1 of the eight of row r, and
+// the scales of all of them.
 struct Group {
   u4 q[2], s;
 };
@@ -171,24 +171,39 @@ struct __attribute__((packed, aligned(2))) Scales {
   u4 v;
 };
 
-// `left`: blocks of the row from the group on.  A group that is not whole is read block by block, and what lies
-// behind it has scale 0 (its operand is 0 too).
-__device__ __forceinline__ Group load_group(const uint8_t* q, const uint16_t* s, int kg, int left) {
+// The blocks of group g: 8 g .., but where the row ends inside them the row's last 8, of which the first belong to the
+// group before.  So every load is whole and none hangs on a condition, behind which the compiler would wait for all
+// loads at once.  TINY: rows of fewer than 8 blocks, read block by block.
+__device__ __forceinline__ int group_start(int g, int blocks) { return min(MV_G * g, max(blocks - MV_G, 0)); }
+
+template <bool TINY>
+__device__ __forceinline__ Group load_group(const uint8_t* q, const uint16_t* s, int start, int kg, int blocks) {
   Group g;
-  if (left >= MV_G) {
-    g.q[0] = *reinterpret_cast<const u4*>(q + 32 * kg);
-    g.q[1] = *reinterpret_cast<const u4*>(q + 32 * kg + 16);
-    g.s = reinterpret_cast<const Scales*>(s)->v;
+  if constexpr (!TINY) {
+    q += 16 * start + 32 * kg;
+    g.q[0] = *reinterpret_cast<const u4*>(q);
+    g.q[1] = *reinterpret_cast<const u4*>(q + 16);
+    g.s = reinterpret_cast<const Scales*>(s + start)->v;
   } else {
-    g.q[0] = *reinterpret_cast<const u4*>(q + 16 * min(2 * kg, left - 1));
-    g.q[1] = *reinterpret_cast<const u4*>(q + 16 * min(2 * kg + 1, left - 1));
+    g.q[0] = *reinterpret_cast<const u4*>(q + 16 * min(2 * kg, blocks - 1));
+    g.q[1] = *reinterpret_cast<const u4*>(q + 16 * min(2 * kg + 1, blocks - 1));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = 2 * i < left ? s[2 * i] : 0, b = 2 * i + 1 < left ? s[2 * i + 1] : 0;
-      g.s[i] = a | b << 16;
-    }
+    for (int i = 0; i < 4; ++i) g.s[i] = s[min(2 * i, blocks - 1)] | (uint32_t)s[min(2 * i + 1, blocks - 1)] << 16;
   }
   return g;
+}
+
+// f(j) for the blocks of group g, block j of the eight read: all, without branches, so that they overlap, or those that
+// are the group's own.
+template <class F> __device__ __forceinline__ void each_block(int g, int start, int blocks, F f) {
+  if (start == MV_G * g && blocks >= start + MV_G) {
+#pragma unroll
+    for (int j = 0; j < MV_G; ++j) f(j);
+  } else {
+#pragma unroll
+    for (int j = 0; j < MV_G; ++j)
+      if (start + j >= MV_G * g && start + j < blocks) f(j);
+  }
 }
 
 // Word kg of each of four blocks, from the lanes that hold the blocks whole: block i comes to w[i].
@@ -211,10 +226,10 @@ __device__ __forceinline__ float scale_at(u4 s, int i) {
 // their sums through LDS.  Columns go to operand rows such that D registers
 // 0 .. MA - 1 hold them (col_row).
 //
-// 36864 x 12288, one float32 row: 60 us, 4.2 TB/s; 74 us with 4 waves a block,
-// 61 to 63 us with 2 or 4 groups ahead, 77 us with a branch at each block of a
-// whole group.  4096 x 4096: 6.2 us a call.
-template <int X, int Y, int MA>
+// 36864 x 12288, one float32 row: 59 us, 4.3 TB/s; 74 us with 4 waves a block,
+// 61 and 62 us with 3 and 4 groups ahead, 77 us with a branch at each block of
+// a whole group.  4096 x 4096: 6.4 us a call.
+template <int X, int Y, int MA, bool TINY>
 __global__ void __launch_bounds__(MV_WAVES * WAVE)
 k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, const float* __restrict__ bias,
              int rows, int cols, const void* __restrict__ x, int64_t ldx, int batch, void* __restrict__ y,
@@ -229,15 +244,13 @@ k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, 
   const int tiles = (rows + MV_ROWS - 1) / MV_ROWS;
   // this block's tiles, and this wave's groups of each: w, w + W, ..
   const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
-  Group buf[MV_AHEAD];                                  // groups on their way
-  int ta = w < groups ? t0 : t1, ga = w;           // the next one to load
+  Group buf[MV_AHEAD];                             // groups on their way
+  int ta = t0, ga = min(w, groups - 1);            // the next one to load; behind the last one, that one again
   auto ahead = [&](Group& to) {
-    if (ta >= t1) return;
-    const int row = min(ta * MV_ROWS + r, rows - 1);
-    to = load_group(q + (int64_t)row * (cols / 2) + 128 * ga, scale + (int64_t)row * blocks + MV_G * ga, kg,
-                    blocks - MV_G * ga);
+    const int row = min(min(ta, t1 - 1) * MV_ROWS + r, rows - 1);
+    to = load_group<TINY>(q + (int64_t)row * (cols / 2), scale + (int64_t)row * blocks, group_start(ga, blocks), kg, blocks);
     ga += W;
-    if (ga >= groups) ga = w, ++ta;
+    if (ga >= groups) ga = min(w, groups - 1), ++ta;
   };
 #pragma unroll
   for (int i = 0; i < MV_AHEAD; ++i) ahead(buf[i]);
@@ -267,22 +280,15 @@ k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, 
     uint32_t wd[2][4];
     spread(now.q[0], wd[0]);
     spread(now.q[1], wd[1]);
-    const char* at = xl + 64 * PB * MV_G * g;
-    auto block = [&](int j) {
+    const int start = group_start(g, blocks);
+    const char* at = xl + 64 * PB * start;
+    each_block(g, start, blocks, [&](int j) {
       const u4 xf = *reinterpret_cast<const u4*>(at + 64 * PB * j);
       const f4 d = H16::mma16(xf, q4_unpack(wd[j & 1][j >> 1]), (f4)(0.f));
       const float sf = scale_at(now.s, j);
 #pragma unroll
       for (int m = 0; m < MA; ++m) acc[m] = fmaf(sf, d[m], acc[m]);
-    };
-    if (MV_G * (g + 1) <= blocks) {                // without branches, so that the blocks overlap
-#pragma unroll
-      for (int j = 0; j < MV_G; ++j) block(j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < MV_G; ++j)
-        if (MV_G * g + j < blocks) block(j);
-    }
+    });
   };
   auto join = [&](int t) {                         // the waves' sums of tile t
     auto& rd = red[t % RB];
@@ -324,94 +330,109 @@ k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, 
   }
 }
 
-// Products of many columns: one block takes 16 rows, the waves taking groups of
-// 8 blocks in turn; the operand comes from memory (in its second-level cache).
-template <int X, int Y, int MT>
-__global__ void __launch_bounds__(MV_WAVES * WAVE)
-k_matvec(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, const float* __restrict__ bias, int rows,
-         int cols, const uint16_t* __restrict__ xo, const float* __restrict__ inv, int batch, void* __restrict__ y,
-         int64_t ldy) {
-  constexpr int RT = 1, W = MV_WAVES;
-  constexpr int P = parts<X>();
-  __shared__ float red[W][MT * 16][MV_ROWS + 1];
+// Products of many columns: one block takes 128 rows, 16 a wave, and one share
+// of the groups, whose operand all its waves read from LDS.  Of a group's
+// operand each wave brings MT KB, two groups ahead: loaded while one group is
+// computed, written to LDS while the next one is.  part: [share][column][row].
+//
+// What bounds it are its vector instructions: 13 to unpack a lane's 8 weights
+// and 4 to scale each column tile's product.  9216 x 8192 with 32 bfloat16 rows:
+// 28 us a call, 25 us of them here; three groups ahead 31 us.  36864 x 12288:
+// 95 us (115 us with 16 rows a block, whose operand came from the second-level
+// cache for each).
+template <int MT, bool TINY>
+__global__ void __launch_bounds__(MV_WAVES * WAVE, 2)
+k_matvec(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, int rows, int cols,
+         const uint16_t* __restrict__ xo, int columns, float* __restrict__ part) {
+  __shared__ u4 xs[2][MV_G * MT * WAVE];
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15,
             kg = lane >> 4;
-  const int row0 = blockIdx.x * MV_ROWS * RT, blocks = cols / 32, groups = (blocks + MV_G - 1) / MV_G;
-  const u4* xl = reinterpret_cast<const u4*>(xo) + lane;
-  f4 acc[RT][MT];
-  Group buf[RT];
-  auto ahead = [&](int g) {
-    if (g >= groups) return;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int row = min(row0 + MV_ROWS * i + r, rows - 1);
-      buf[i] = load_group(q + (int64_t)row * (cols / 2) + 128 * g, scale + (int64_t)row * blocks + MV_G * g, kg,
-                          blocks - MV_G * g);
-    }
+  const int row0 = (blockIdx.x * MV_WAVES + w) * MV_ROWS, row = min(row0 + r, rows - 1);
+  const int blocks = cols / 32, groups = (blocks + MV_G - 1) / MV_G;
+  const int g0 = (int)((int64_t)groups * blockIdx.y / gridDim.y), g1 = (int)((int64_t)groups * (blockIdx.y + 1) / gridDim.y);
+  const uint8_t* qr = q + (int64_t)row * (cols / 2);
+  const uint16_t* sr = scale + (int64_t)row * blocks;
+  const u4* xl = reinterpret_cast<const u4*>(xo);
+  Group buf[MV_AHEAD];
+  u4 xr[MT];
+  // behind the share's last group, that one again
+  auto weights = [&](Group& to, int g) {
+    to = load_group<TINY>(qr, sr, group_start(min(g, g1 - 1), blocks), kg, blocks);
   };
-  ahead(w);
+  auto operand = [&](int g) {                      // the operand is there for whole groups
+    const u4* from = xl + (int64_t)MV_G * MT * WAVE * min(g, g1 - 1) + MT * w * WAVE + lane;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < MT; ++i) xr[i] = from[i * WAVE];
+  };
+  auto stage = [&](int g) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[i][t] = (f4)(0.f);
-  for (int g = w; g < groups; g += W) {
-    uint32_t wd[RT][2][4];
-    u4 sc[RT];
+    for (int i = 0; i < MT; ++i) xs[g & 1][(MT * w + i) * WAVE + lane] = xr[i];
+  };
+  operand(g0);
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      spread(buf[i].q[0], wd[i][0]);
-      spread(buf[i].q[1], wd[i][1]);
-      sc[i] = buf[i].s;
-    }
-    ahead(g + W);
-    auto block = [&](int j) {
-      u4 xf[MT];
+  for (int i = 0; i < MV_AHEAD; ++i) weights(buf[i], g0 + i);
+  stage(g0);
+  operand(g0 + 1);
+  f4 acc[MT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) xf[t] = xl[(int64_t)((MV_G * g + j) * MT + t) * 64];
+  for (int t = 0; t < MT; ++t) acc[t] = (f4)(0.f);
+  for (int base = g0; base < g1; base += MV_AHEAD) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const u4 wf = q4_unpack(wd[i][j & 1][j >> 1]);
-        const float sf = scale_at(sc[i], j);
+    for (int i = 0; i < MV_AHEAD; ++i) {
+      const int g = base + i;
+      if (g >= g1) break;
+      // this group's operand is written, and the one before it has been read; loads stay on their way
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const Group now = buf[i];
+      weights(buf[i], g + MV_AHEAD);
+      stage(g + 1);
+      operand(g + 2);
+      uint32_t wd[2][4];
+      spread(now.q[0], wd[0]);
+      spread(now.q[1], wd[1]);
+      const int start = group_start(g, blocks);
+      const u4* at = xs[g & 1] + lane + (start - MV_G * g) * MT * WAVE;
+      each_block(g, start, blocks, [&](int j) {
+        const u4 wf = q4_unpack(wd[j & 1][j >> 1]);
+        const float sf = scale_at(now.s, j);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          const f4 d = H16::mma16(xf[t], wf, (f4)(0.f));
+          const f4 d = H16::mma16(at[(j * MT + t) * WAVE], wf, (f4)(0.f));
 #pragma unroll
-          for (int m = 0; m < 4; ++m) acc[i][t][m] = fmaf(sf, d[m], acc[i][t][m]);
+          for (int m = 0; m < 4; ++m) acc[t][m] = fmaf(sf, d[m], acc[t][m]);
         }
-      }
-    };
-    if (MV_G * (g + 1) <= blocks) {                // without branches, so that the blocks overlap
-#pragma unroll
-      for (int j = 0; j < MV_G; ++j) block(j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < MV_G; ++j)
-        if (MV_G * g + j < blocks) block(j);
+      });
     }
   }
+  if (row0 + r >= rows) return;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    if (i) __syncthreads();
+  for (int t = 0; t < MT; ++t)
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) red[w][16 * t + 4 * m + kg][r] = acc[i][t][m];
-    __syncthreads();
-    for (int e = tid; e < batch * MV_ROWS; e += W * WAVE) {
-      const int b = e / MV_ROWS, n = e % MV_ROWS, row = row0 + MV_ROWS * i + n;
-      if (row >= rows) continue;
-      float v = 0.f, z = 0.f;
-#pragma unroll
-      for (int x = 0; x < W; ++x) {
-        v += red[x][P * b][n];
-        if constexpr (P == 2) z += red[x][P * b + 1][n];
-      }
-      if constexpr (P == 2) v = fmaf(z, 1.f / 2048.f, v);
-      v *= inv[b];
-      if (bias) v += bias[row];
-      y_to<Y>(y, b * ldy + row, v);
+    for (int m = 0; m < 4; ++m) {                  // operand row 4 kg + m is column 4 m + kg
+      const int c = 16 * t + 4 * m + kg;
+      if (c < columns) part[((int64_t)blockIdx.y * columns + c) * rows + row0 + r] = acc[t][m];
     }
+}
+
+// The shares' sums, scaled back: one thread per output.
+template <int P, int Y>
+__global__ void __launch_bounds__(256)
+k_matvec_join(const float* __restrict__ part, const float* __restrict__ inv, const float* __restrict__ bias, int rows,
+              int shares, int batch, void* __restrict__ y, int64_t ldy) {
+  const int row = blockIdx.x * 256 + threadIdx.x, b = blockIdx.y;
+  if (row >= rows) return;
+  const int64_t step = (int64_t)P * batch * rows;
+  const float* at = part + (int64_t)P * b * rows + row;
+  float v = 0.f, z = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < shares; ++i) {
+    v += at[i * step];
+    if constexpr (P == 2) z += at[i * step + rows];
   }
+  if constexpr (P == 2) v = fmaf(z, 1.f / 2048.f, v);
+  v *= inv[b];
+  if (bias) v += bias[row];
+  y_to<Y>(y, b * ldy + row, v);
 }
 
 }  // namespace piq
