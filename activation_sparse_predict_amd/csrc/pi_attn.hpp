@@ -15,6 +15,7 @@
 // of the second (the order of the keys inside a matrix instruction is free).
 #pragma once
 #include "pi.h"
+#include "pi_share.hpp"
 #include "pi_tile.hpp"
 
 #include <type_traits>
@@ -22,6 +23,7 @@
 namespace pia {
 
 using namespace pit;
+using namespace pish;
 
 // A [tokens][heads][dim] tensor with its strides in elements (dim is contiguous).
 struct Rows {
@@ -392,23 +394,11 @@ __device__ __forceinline__ int slot_of(const int32_t* seqs, int b, int slots) {
 // Tokens of batch row b; none where the slot or its length cannot be.
 __device__ __forceinline__ int len_of(const Pages& pg, const int32_t* seqs, int b) {
   const int slot = slot_of(seqs, b, pg.slots);
-  const int len = slot >= 0 ? pg.lens[slot] : 0;
-  return len < 0 || len > (int64_t)pg.max_pages * pg.page ? 0 : len;
+  return usable_len(slot >= 0 ? pg.lens[slot] : 0, pg.max_pages, pg.page);
 }
 
-// A prefix that no table row can hold is none.
-__device__ __forceinline__ int common_tokens(const Pages& pg, const int32_t* prefix) {
-  const int n = prefix ? *prefix : 0;
-  return n > 0 && n <= pg.max_pages ? n * pg.page : 0;
-}
-
-// Shares of the common keys: whole tiles, SH_TILES of them at least, and `most` shares at most.  (4096 common keys, 32
-// rows of 64 heads on 8, 128 wide: 37 us a call; with 2 tiles 49 us, with 8 42 us: more shares, more sums to write and
-// join, or fewer blocks.)
-constexpr int SH_TILES = 4;
-__device__ __forceinline__ int shares_of(int total, int most) {
-  const int tiles = (total + PT_K - 1) / PT_K;
-  return max(1, min(most, tiles / SH_TILES));
+__device__ __forceinline__ int common_of(const Pages& pg, const int32_t* prefix) {
+  return prefix ? common_tokens(*prefix, pg.max_pages, pg.page) : 0;
 }
 
 // ---- the common keys, for all queries of a key head at once.
@@ -437,9 +427,9 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
   const int pair = blockIdx.x % 8 + 8 * (blockIdx.x / (8 * qtiles)), qt = blockIdx.x / 8 % qtiles;
   const int g = pair / shares, share = pair % shares;
   if (g >= kv_heads) return;
-  const int total = common_tokens(pg, prefix);
+  const int total = common_of(pg, prefix);
   if (total == 0) return;
-  const int n = shares_of(total, shares);
+  const int n = common_shares(total, shares);
   if (share >= n) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), hi = lane >> 5;
   int holder = -1;                                 // a batch row whose table names the pages
@@ -464,8 +454,8 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
   if (nchunk < L::NC) {                            // chunks that no load fills
     for (int e = tid; e < 2 * S * R::BYTES / 16; e += NT) reinterpret_cast<u4*>(ring)[e] = u4{0, 0, 0, 0};
   }
-  const int tiles = (total + PT_K - 1) / PT_K;
-  const int first = tiles * share / n, last = tiles * (share + 1) / n;   // 2^25 tiles and 64 shares at most
+  const int tiles = pieces(total, PT_K);
+  const int first = share_begin(tiles, share, n), last = share_begin(tiles, share + 1, n);
   const int r0 = tid / L::NC;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * w;
   const int per = pg.page / 16;
@@ -474,8 +464,8 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
     bool bad = false;
     const int at = 4 * base + tid;
     if (at < 4 * last) {
-      const int x = min(at, total / 16 - 1), id = table[x / per];
-      bad = (unsigned)id >= (unsigned)pg.pages;
+      const int x = min(at, total / 16 - 1), id = usable_page(table[x / per], pg.pages);
+      bad = id < 0;
       ids[tid] = bad ? -1 : (((int64_t)id * kv_heads + g) * pg.page + x % per * 16) * dim;
       if (bad) atomicOr(pg.flags, PI_CACHE_EPAGE);
     }
@@ -597,7 +587,7 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
 // ---- the keys of each row's own.
 constexpr int DC_WAVES = 4;
 constexpr int DC_K = 32;                 // keys of a wave's step
-constexpr int DC_MOST = 128;             // shares of a row at most
+static_assert(DC_WAVES * DC_K == UNIT && PT_K == TILE, "pi_share.hpp");
 constexpr int DC_ROWS = 1024;            // tiles of queries from which on a row has one share
 
 // O^T of the 16x16x32 product: a lane's A operand row l % 16 stands for VW
@@ -614,25 +604,13 @@ struct Share {
   int b, slot, len, i, n;                // n = 0: nothing to do
 };
 
-// 128 keys are a unit of work.  `free` shares are dealt to the rows, of `size` units each (the last of a row may be
-// smaller), so that all rows together take no more than one share each beside them.
-__device__ __forceinline__ uint32_t share_size(uint64_t all, int free) {
-  int s = 0;                                       // 32-bit division: what is lost of `all` is made up for
-  while (all >> s >> 31) ++s;
-  return max(1u, ((uint32_t)(all >> s) + free - 1) / free << s) + (s ? 1u << s : 0u);
-}
-__device__ __forceinline__ int deal(int units, uint32_t size) {
-  return max(1, min(DC_MOST, (int)(((uint32_t)units + size - 1) / size)));
-}
-__device__ __forceinline__ int units_of(int keys) { return (keys + DC_WAVES * DC_K - 1) / (DC_WAVES * DC_K); }
-
 __device__ __forceinline__ Share find_share(const Pages& pg, const int32_t* seqs, int batch, int total, int idx, int free) {
   const int lane = threadIdx.x & (WAVE - 1);
   int slot = -1, len = 0;                          // of row base + lane
   auto units = [&](int b) {
     slot = b < batch ? slot_of(seqs, b, pg.slots) : -1;
     len = slot >= 0 ? pg.lens[slot] : 0;
-    const int n = len < 0 || len > (int64_t)pg.max_pages * pg.page ? 0 : len;
+    const int n = usable_len(len, pg.max_pages, pg.page);
     return units_of(n - (n >= total ? total : 0));
   };
   // of one row at most 2^24 units: 64 rows fit 32 bits
@@ -679,7 +657,7 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
   const int group = heads / kv_heads, rts = (group + 15) / 16, g = blockIdx.y / rts, rt = blockIdx.y % rts;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kg = lane >> 4;
-  const int total = common_tokens(pg, prefix);
+  const int total = common_of(pg, prefix);
   Share me;
   if (free) {
     me = find_share(pg, seqs, batch, total, blockIdx.x, free);
@@ -689,14 +667,11 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
     me = Share{(int)blockIdx.x, slot, slot >= 0 ? pg.lens[slot] : 0, 0, 1};
   }
   const int b = me.b, slot = me.slot;
-  int len = me.len;
-  if (slot < 0 || len < 0 || len > (int64_t)pg.max_pages * pg.page) {
-    if (tid == 0) atomicOr(pg.flags, slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
-    len = 0;
-  }
+  const int len = usable_len(me.len, pg.max_pages, pg.page);
+  if (tid == 0 && (slot < 0 || len != me.len)) atomicOr(pg.flags, slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
   const int from = total > 0 && len >= total ? total : 0;
-  const int steps = (len - from + DC_K - 1) / DC_K;
-  const int first = (int)((int64_t)steps * me.i / me.n), last = (int)((int64_t)steps * (me.i + 1) / me.n);
+  const int steps = pieces(len - from, DC_K);
+  const int first = share_begin(steps, me.i, me.n), last = share_begin(steps, me.i + 1, me.n);
   const int nchunk = dim / 8;
 
   const int head = g * group + 16 * rt + min(r, group - 16 * rt - 1);
@@ -721,9 +696,8 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
     for (int h = 0; h < 2; ++h) {
       const int key = from + st * DC_K + 16 * h;
       seen[h] = max(0, min(16, len - key));
-      const int place = min(key / pg.page, pg.max_pages - 1);
-      int id = row[place];
-      if ((unsigned)id >= (unsigned)pg.pages) {    // a broken table: its keys are not seen
+      int id = usable_page(row[place_of(key, pg.page, pg.max_pages)], pg.pages);
+      if (id < 0) {                                // a broken table: its keys are not seen
         if (seen[h] && lane == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
         seen[h] = 0;
         id = 0;
@@ -826,7 +800,7 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
 #pragma unroll
       for (int f = 0; f < V::W; ++f) so[w][r][(16 * gr + 4 * kg + i) * V::W + f] = o[gr * V::W + f][i];
   __syncthreads();
-  const int queries = min(16, group - 16 * rt), common = from > 0 ? shares_of(total, shares) : 0;
+  const int queries = min(16, group - 16 * rt), common = from > 0 ? common_shares(total, shares) : 0;
   const bool whole = me.n == 1 && common == 0;
   const int64_t mine = (int64_t)blockIdx.x * gridDim.y + blockIdx.y;   // this block's place among the parts
   uint16_t* dst = out + b * out_token + (g * group + 16 * rt) * out_head;
@@ -863,7 +837,7 @@ k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, cons
             const float* __restrict__ part, const float* __restrict__ stat, uint16_t* __restrict__ out,
             int64_t out_token, int64_t out_head, int batch, int heads, int kv_heads, int dim, int shares) {
   typedef float Dims __attribute__((ext_vector_type(W)));
-  __shared__ float weight[4][DC_MOST + 64];
+  __shared__ float weight[4][MOST + 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t row = (int64_t)blockIdx.x * 4 + w;
   if (row >= (int64_t)batch * heads) return;
@@ -883,7 +857,7 @@ k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, cons
   Dims y[AHEAD];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) y[i] = at(min(i, all - 1));
-  constexpr int PER = (DC_MOST + 64) / 64;
+  constexpr int PER = (MOST + 64) / 64;
   float2 st[PER];
   float mm = NEG_INF, ll = 0.f;
 #pragma unroll
