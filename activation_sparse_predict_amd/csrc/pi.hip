@@ -11,7 +11,6 @@
 #include <mutex>
 
 #include "pi_batch.hpp"
-#include "pi_host.hpp"
 #include "pi_kernels.hpp"
 
 namespace {
@@ -655,8 +654,6 @@ pi_status launch_status() {
 }
 
 }  // namespace
-
-pi_status pih::launched() { return launch_status(); }
 
 namespace {
 

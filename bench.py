@@ -185,23 +185,23 @@ def copy_bandwidth(torch, dev, stream, mib=1024, reps=5):
     return 2 * n * 4 / (ms * 1e-3) / 1e9
 
 
+# the HIP sources of the kernels that this program measures
+FFN_SOURCES = ("pi.hip", "pi_batch.hpp", "pi_kernels.hpp")
+
+
 def source_digest(rev=None):
-    """sha256 over the HIP sources (of the working tree, or of git revision `rev`);
+    """sha256 over the sparse FFN's HIP sources (of the working tree, or of git revision `rev`);
     counter summaries taken on other sources do not apply."""
     import subprocess
     h = hashlib.sha256()
     csrc = "activation_sparse_predict_amd/csrc"
-    if rev:
-        names = subprocess.run(["git", "ls-tree", "--name-only", f"{rev}:{csrc}"], cwd=ROOT, check=True,
-                               capture_output=True, text=True).stdout.split()
-        for n in sorted(names):
-            blob = subprocess.run(["git", "show", f"{rev}:{csrc}/{n}"], cwd=ROOT, check=True,
-                                  capture_output=True).stdout
-            h.update(n.encode() + b"\0" + blob)
-        return h.hexdigest()
-    for p in sorted(glob.glob(os.path.join(ROOT, csrc, "*"))):
-        with open(p, "rb") as fh:
-            h.update(os.path.basename(p).encode() + b"\0" + fh.read())
+    for n in FFN_SOURCES:
+        if rev:
+            blob = subprocess.run(["git", "show", f"{rev}:{csrc}/{n}"], cwd=ROOT, check=True, capture_output=True).stdout
+        else:
+            with open(os.path.join(ROOT, csrc, n), "rb") as fh:
+                blob = fh.read()
+        h.update(n.encode() + b"\0" + blob)
     return h.hexdigest()
 
 
