@@ -162,12 +162,12 @@ template <class T, int D> struct Sums {
 
   // Of a tile's scores, those of keys that a row does not see: it sees the first `seen`.
   static __device__ __forceinline__ void mask(f16v* s, int seen) {
-    const int hi = (threadIdx.x & 63) >> 5;
+    const int limit = seen - 4 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (32 * h + 8 * (i / 4) + 4 * hi + i % 4 >= seen) s[h][i] = NEG_INF;
+        if (32 * h + 8 * (i / 4) + i % 4 >= limit) s[h][i] = NEG_INF;
   }
 
   // The weights of a tile's scores, rounded, and their part of l.
@@ -407,13 +407,13 @@ __device__ __forceinline__ int common_of(const Pages& pg, const int32_t* prefix)
 // over one share of the common keys, in tiles of 64 through LDS as in
 // k_attn_prompt, S - 1 of them ahead.  Tiles are found through the pages; 16
 // keys lie in one page.  24 rows of 128 heads on 8, 64 wide, over 32768 common
-// keys: 51 us, 500 TFLOP/s, bound by the exponentials and the latency of a tile's
+// keys: 50 us, 520 TFLOP/s, bound by the exponentials and the latency of a tile's
 // steps with two waves on a SIMD (17 us without the products and exponentials).
 // part, stat: unnormalised sums, and (reference point, l) of each.
 constexpr int SH_IDS = 256;              // places of 16 keys that are looked up at once: 64 tiles
 
 template <class T, int D>
-__global__ void __launch_bounds__(4 * WAVE, D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(4 * WAVE, D <= 64 ? 3 : D <= 128 ? 2 : 1)
 k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t* __restrict__ prefix, int batch,
               int heads, int kv_heads, int dim, int shares, int qtiles, float c, float* __restrict__ part,
               float* __restrict__ stat) {

@@ -46,12 +46,15 @@ pi_status check_list(const int32_t* list, int32_t n) {
   return n > pic::MAX_N ? PI_EUNSUPPORTED : PI_OK;
 }
 
-// enough blocks to fill the chip several times over; each block takes whole pages
-void copy_pages(const pi_cache* c, int most, const pic::Plan& plan, hipStream_t st) {
+// Enough blocks to fill the chip several times over; each block takes whole pages.  to: the map that the tables follow
+// (a compaction's), or NULL.
+void copy_pages(const pi_cache* c, int most, const pic::Plan& plan, const int32_t* to, int32_t* moved, hipStream_t st) {
   const int64_t chunks = (int64_t)c->kv_heads * c->page * c->dim / 8;
-  const int per_layer = std::max(1, std::min(most, (int)up_div(4096, 2 * c->layers)));
-  hipLaunchKernelGGL(pic::k_cache_copy, dim3(per_layer, 2 * c->layers), dim3(256), 0, st,
-                     static_cast<pit::u4*>(c->k), static_cast<pit::u4*>(c->v), chunks * c->pages, (int)chunks, plan);
+  int x = std::max(1, std::min(most, (int)up_div(4096, 2 * c->layers)));
+  if (to) x = std::max(x, 64);                     // the tables' blocks
+  hipLaunchKernelGGL(pic::k_cache_copy, dim3(x, 2 * c->layers + (to ? 1 : 0)), dim3(256), 0, st,
+                     static_cast<pit::u4*>(c->k), static_cast<pit::u4*>(c->v), chunks * c->pages, (int)chunks,
+                     c->layers, plan, meta_of(c), to, moved);
 }
 
 }  // namespace
@@ -121,7 +124,7 @@ pi_status pi_cache_fork(const pi_cache* c, const int32_t* parents, const int32_t
   const pic::Plan plan = plan_of(c, ws);
   (void)hipGetLastError();
   hipLaunchKernelGGL(pic::k_cache_fork, dim3(1), dim3(pic::PL_T), 0, st, meta_of(c), parents, children, n, plan);
-  copy_pages(c, n, plan, st);
+  copy_pages(c, n, plan, nullptr, nullptr, st);
   return launched();
 }
 
@@ -146,9 +149,7 @@ pi_status pi_cache_compact(const pi_cache* c, int32_t* moved, void* ws, size_t w
   const pic::Meta m = meta_of(c);
   (void)hipGetLastError();
   hipLaunchKernelGGL(pic::k_cache_compact, dim3(1), dim3(pic::PL_T), 0, st, m, plan, to);
-  const int64_t entries = std::max<int64_t>((int64_t)c->slots * c->max_pages, c->pages);
-  hipLaunchKernelGGL(pic::k_cache_remap, dim3((unsigned)up_div(entries, 256)), dim3(256), 0, st, m, to, moved);
-  copy_pages(c, std::max(1, c->pages / 2), plan, st);
+  copy_pages(c, std::max(1, c->pages / 2), plan, to, moved, st);
   return launched();
 }
 

@@ -271,15 +271,35 @@ k_cache_fork(Meta m, const int32_t* __restrict__ parents, const int32_t* __restr
   }
 }
 
-// Whole pages from src to dst, in every layer of both pools: blockIdx.y is layer * 2 + pool.
+// After a compaction: the tables, and where each page went.  Entry e of slots max_pages, or page e.
+__device__ __forceinline__ void remap(const Meta& m, const int32_t* to, int32_t* moved, int64_t e) {
+  if (moved && e < m.pages) moved[e] = to[e];
+  if (e >= (int64_t)m.slots * m.max_pages) return;
+  const int slot = (int)(e / m.max_pages), place = (int)(e % m.max_pages);
+  if ((int64_t)place * m.page >= m.lens[slot]) return;
+  const int p = m.table[e];
+  const int now = (unsigned)p < (unsigned)m.pages ? to[p] : -1;
+  if (now < 0) atomicOr(&m.words[1], PI_CACHE_EPAGE);
+  else m.table[e] = now;
+}
+
+// Whole pages from src to dst, in every layer of both pools: blockIdx.y is layer * 2 + pool.  Behind the last layer,
+// blocks that follow a compaction's map (`to`).
 __global__ void __launch_bounds__(256)
-k_cache_copy(u4* __restrict__ k, u4* __restrict__ v, int64_t layer_chunks, int page_chunks, Plan plan) {
+k_cache_copy(u4* __restrict__ k, u4* __restrict__ v, int64_t layer_chunks, int page_chunks, int layers, Plan plan, Meta m,
+             const int32_t* __restrict__ to, int32_t* __restrict__ moved) {
+  if ((int)blockIdx.y == 2 * layers) {
+    const int64_t entries = max((int64_t)m.slots * m.max_pages, (int64_t)m.pages);
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < entries; e += (int64_t)gridDim.x * blockDim.x)
+      remap(m, to, moved, e);
+    return;
+  }
   u4* pool = ((blockIdx.y & 1) ? v : k) + (int64_t)(blockIdx.y >> 1) * layer_chunks;
   const int count = *plan.count;
   for (int i = blockIdx.x; i < count; i += gridDim.x) {
     const u4* from = pool + (int64_t)plan.src[i] * page_chunks;
-    u4* to = pool + (int64_t)plan.dst[i] * page_chunks;
-    for (int e = threadIdx.x; e < page_chunks; e += blockDim.x) to[e] = from[e];
+    u4* into = pool + (int64_t)plan.dst[i] * page_chunks;
+    for (int e = threadIdx.x; e < page_chunks; e += blockDim.x) into[e] = from[e];
   }
 }
 
@@ -377,19 +397,6 @@ __global__ void __launch_bounds__(PL_T) k_cache_compact(Meta m, Plan plan, int32
     m.words[2] = used;
     *plan.count = movers;
   }
-}
-
-// The tables after a compaction: one thread per entry.
-__global__ void __launch_bounds__(256) k_cache_remap(Meta m, const int32_t* __restrict__ to, int32_t* __restrict__ moved) {
-  const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (moved && e < m.pages) moved[e] = to[e];
-  if (e >= (int64_t)m.slots * m.max_pages) return;
-  const int slot = (int)(e / m.max_pages), place = (int)(e % m.max_pages);
-  if ((int64_t)place * m.page >= m.lens[slot]) return;
-  const int p = m.table[e];
-  const int now = (unsigned)p < (unsigned)m.pages ? to[p] : -1;
-  if (now < 0) atomicOr(&m.words[1], PI_CACHE_EPAGE);
-  else m.table[e] = now;
 }
 
 }  // namespace pic
