@@ -28,12 +28,6 @@ constexpr int MV_G = 8;                  // 32-blocks of a group: 128 bytes of a
 constexpr int MV_WAVES = 8;              // waves of a block
 constexpr int MV_AHEAD = 2;              // groups of a wave on their way
 
-// Load one element of x, stored as dtype X (pi_dtype), as float32.
-template <int X> __device__ __forceinline__ float x_at(const void* p, int64_t i) {
-  if constexpr (X == PI_F32) return static_cast<const float*>(p)[i];
-  else if constexpr (X == PI_F16) return (float)static_cast<const _Float16*>(p)[i];
-  else return (float)static_cast<const __bf16*>(p)[i];
-}
 // Four elements from i on, whatever their alignment.
 struct __attribute__((packed, aligned(4))) Four32 {
   float v[4];
@@ -68,10 +62,6 @@ template <int X> constexpr int parts() { return X == PI_F32 ? 2 : 1; }
 
 // Column c of the x operand is row m of its 16: neighbours go to different lane groups of D.
 __host__ __device__ constexpr int col_row(int c) { return 4 * (c % 4) + c / 4; }
-
-// Element e of lane group kg inside a 32-block: the order in which the nibbles of
-// word kg of the block come out of q4_unpack.
-__device__ __forceinline__ int slot_k(int kg, int e) { return 4 * kg + 2 * (e & 1) + (e >> 2) + 16 * ((e >> 1) & 1); }
 
 // The 8 weights of a 4-byte word as binary16 q - 8: 0x6400 | q is 1024 + q, and
 // 0x6400 | 16 q is 1024 + 16 q.
@@ -126,8 +116,9 @@ __device__ __forceinline__ uint32_t x_part(float v, int p) {
   return __builtin_bit_cast(uint16_t, (_Float16)rest);
 }
 
-// Elements 4 a .. 4 a + 3 of a 32-block, a < 8, lie at words `at(a)` and `at(a) + 2` of the block's 16, elements
-// 0 and 2 in the first (the order of slot_k).
+// A block's elements in the operand stand in the order in which q4_unpack gives the weights of word kg: 4 kg + 0, 2,
+// 16, 18, 1, 3, 17, 19.  So of elements 4 a .. 4 a + 3, a < 8, the first and third lie in word word_of(a) of the block's
+// 16 and the other two in word word_of(a) + 2.
 __device__ __forceinline__ int word_of(int a) { return 4 * (a & 3) + (a >> 2); }
 
 // x -> operand [block][column tile][lane][8] and, per row, 1 / scale.  Block (b, i): a share of x row b's blocks.
