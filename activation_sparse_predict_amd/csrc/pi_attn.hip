@@ -174,7 +174,7 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
                        out->token_stride, out->head_stride, seqs, prefix, batch, heads, cache->kv_heads, dim, u.free,
                        u.shares, c, reinterpret_cast<int4*>(base), floats(W.part), floats(W.stat));
     if (prefix || u.free)
-      hipLaunchKernelGGL((pia::k_attn_join<T, D <= 128 ? 2 : 4>), dim3((unsigned)up_div((int64_t)batch * heads, 4)),
+      hipLaunchKernelGGL((pia::k_attn_join<T, D <= 64 ? 16 : D <= 128 ? 32 : 64>), dim3((unsigned)up_div((int64_t)batch * heads, 4)),
                          dim3(256), 0, st, reinterpret_cast<const int4*>(base), floats(W.cpart), floats(W.cstat),
                          floats(W.part), floats(W.stat), static_cast<uint16_t*>(out->p), out->token_stride,
                          out->head_stride, batch, heads, cache->kv_heads, dim, u.shares);

@@ -830,13 +830,13 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
   if (me.i == 0 && blockIdx.y == 0 && tid == 0) plan[b] = int4{(int)blockIdx.x, whole ? 0 : me.n, common, 0};
 }
 
-// Join the shares of a query: one wave each, W dims a lane.
-template <class T, int W>
+// Join the shares of a query: one wave each, N lanes (of 4 dims each) for a share, 64 / N shares at once.
+template <class T, int N>
 __global__ void __launch_bounds__(256)
 k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, const float* __restrict__ cstat,
             const float* __restrict__ part, const float* __restrict__ stat, uint16_t* __restrict__ out,
             int64_t out_token, int64_t out_head, int batch, int heads, int kv_heads, int dim, int shares) {
-  typedef float Dims __attribute__((ext_vector_type(W)));
+  constexpr int AT_ONCE = 64 / N, AHEAD = 8;       // shares a load, loads on their way
   __shared__ float weight[4][MOST + 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t row = (int64_t)blockIdx.x * 4 + w;
@@ -847,16 +847,15 @@ k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, cons
   const int tiles = kv_heads * rts, tile = h / group * rts + h % group / 16;
   const int64_t own0 = ((int64_t)pl.x * tiles + tile) * 16 + h % group % 16, own1 = 16 * (int64_t)tiles;
   const int n = pl.y, all = n + pl.z;
-  const int d = min(W * lane, dim - W);
+  const int d = min(4 * (lane % N), dim - 4), mine = lane / N;
   // the first sums are on their way while the weights are made
   auto at = [&](int i) {
-    const float* p = i < n ? part + (own0 + i * own1) * dim : cpart + (row * shares + i - n) * dim;
-    return *reinterpret_cast<const Dims*>(p + d);
+    i = min(i, all - 1);
+    return *reinterpret_cast<const f4*>((i < n ? part + (own0 + i * own1) * dim : cpart + (row * shares + i - n) * dim) + d);
   };
-  constexpr int AHEAD = 16;
-  Dims y[AHEAD];
+  f4 y[AHEAD];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) y[i] = at(min(i, all - 1));
+  for (int i = 0; i < AHEAD; ++i) y[i] = at(AT_ONCE * i + mine);
   constexpr int PER = (MOST + 64) / 64;
   float2 st[PER];
   float mm = NEG_INF, ll = 0.f;
@@ -882,25 +881,30 @@ k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, cons
   for (int x = 32; x; x >>= 1) ll += __shfl_xor(ll, x);
   // a wave reads its own weights only
   __builtin_amdgcn_wave_barrier();
-  Dims sum = (Dims)(0.f);
-  for (int base_i = 0; base_i < all; base_i += AHEAD) {
-    if (base_i) {
+  f4 sum = (f4)(0.f);
+  for (int i0 = 0; i0 < all; i0 += AT_ONCE * AHEAD) {
+    if (i0) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) y[i] = at(min(base_i + i, all - 1));
+      for (int i = 0; i < AHEAD; ++i) y[i] = at(i0 + AT_ONCE * i + mine);
     }
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      if (base_i + i < all) {
-        const float a = weight[w][base_i + i];
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = i0 + AT_ONCE * i + mine;
+      if (k < all) {
+        const float a = weight[w][k];
 #pragma unroll
-        for (int j = 0; j < W; ++j) sum[j] = fmaf(y[i][j], a, sum[j]);
+        for (int j = 0; j < 4; ++j) sum[j] = fmaf(y[i][j], a, sum[j]);
       }
+    }
   }
+#pragma unroll
+  for (int x = N; x < 64; x *= 2)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], x);
   const float inv = ll == 0.f ? 0.f : 1.f / ll;    // a row that sees no key is zero
-  uint16_t* dst = out + b * out_token + h * out_head + d;
-  if (W * lane >= dim) return;
-  if constexpr (W == 4) *reinterpret_cast<u2*>(dst) = u2{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
-  else *reinterpret_cast<uint32_t*>(dst) = T::pack(sum[0] * inv, sum[1] * inv);
+  if (lane < N && 4 * lane < dim)
+    *reinterpret_cast<u2*>(out + b * out_token + h * out_head + d) =
+        u2{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
 }
 
 }  // namespace pia
