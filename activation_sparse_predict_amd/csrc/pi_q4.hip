@@ -13,10 +13,19 @@ namespace {
 // 12288 float32 values; with the sums of the waves (9 KB) a block keeps to 64 KB
 constexpr size_t kOperandLds = 48 << 10;
 
-// Shares of the groups of 8 blocks in a product of many columns: two blocks for each compute unit, at most 32 shares.
+// Shares of the groups of 8 blocks in a product of many columns, 32 at most: those with which the rounds of 512 blocks
+// (two for each compute unit), at 2.5 us a group, and the shares' sums, at 1 us for each 9216 rows of 32 columns,
+// written and read, take least.  (32 bfloat16 rows, 9216 x 8192: 6, 7, 8, 9, 11 shares 25.9, 25.0, 27.9, 27.1, 29.0 us;
+// 18432 x 8192: 3, 4, 5 shares 43, 48, 44 us; 36864 x 12288: 2, 3, 4 shares 98, 91, 91 us.)
 int shares_of(int32_t rows, int32_t cols) {
   const int64_t groups = up_div(cols, 32 * piq::MV_G), blocks = up_div(rows, piq::MV_ROWS * piq::MV_WAVES);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({up_div(512, blocks), groups, 32}));
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= std::min<int64_t>(groups, 32); ++s) {
+    const int64_t cost = 5 * up_div(blocks * s, 512) * up_div(groups, s) * 9216 + 2 * (int64_t)s * rows;
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
 }
 
 // the operand made of x, whole groups of it, of the largest number of columns a type of x takes; a row's scale; the

@@ -328,9 +328,9 @@ k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, 
 //
 // What bounds it are its vector instructions: 13 to unpack a lane's 8 weights
 // and 4 to scale each column tile's product.  9216 x 8192 with 32 bfloat16 rows:
-// 28 us a call, 25 us of them here; three groups ahead 31 us.  36864 x 12288:
-// 95 us (115 us with 16 rows a block, whose operand came from the second-level
-// cache for each).
+// 25 us a call (in 8 shares 28 us, and with three groups ahead 31 us then).
+// 36864 x 12288: 91 us (115 us with 16 rows a block, whose operand came from the
+// second-level cache for each).
 template <int MT, bool TINY>
 __global__ void __launch_bounds__(MV_WAVES * WAVE, 2)
 k_matvec(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, int rows, int cols,
