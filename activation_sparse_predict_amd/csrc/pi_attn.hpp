@@ -2,12 +2,20 @@
 //
 // For a query row q and the keys j it sees, with c = scale log2(e):
 //   o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c (s_j - m)),  s_j = q . k_j
-// with m the largest s_j so far; when m grows, what was summed is multiplied by
-// 2^(c (m_old - m)).  Scores, m, the sums and o are float32.  The unnormalised
-// p_j are rounded to the inputs' type for the second product (as the type's
-// matrix instruction takes them): at most half a step each, relative to values
-// in (0, 1], and independent between keys, so the output is off by less than
-// its own rounding to that type.  sum_j p_j adds the unrounded values.
+// with c m a reference point near the largest c s_j so far; when it moves, what was
+// summed is multiplied by 2^(c (m_old - m)).  Scores, m, the sums and o are float32.
+// The p_j are rounded to the inputs' type for the second product, as the type's
+// matrix instruction takes them; sum_j p_j adds the unrounded values.  A p_j that is
+// normal in the type is off by at most half a step u of its own, so o by at most
+// u sum_j p_j |v_j| / sum_j p_j, about as much as by its own rounding.
+// binary16 has no normal values below 2^-14: were the largest p_j 1, keys 2^14 times
+// below one that outscores all others would lose bits, below 2^25 times vanish, and
+// where that one's value is small they are the result.  So c m lies LOW under the
+// largest c s_j it was taken from, which makes that p_j 2^LOW, and moves once a p_j
+// passes 2^(LOW + LAG), 2^15 in binary16: bits go only 2^25 times below the largest,
+// and no more than 2^-36 of it a key.  A kernel that moves c m with every rise puts
+// it HIGH under the largest (2^29 times, 2^-40).  bfloat16 has float32's exponents
+// and needs neither.
 //
 // Both kernels compute S^T = K Q^T and O^T = V^T P^T, so that a lane holds all
 // its scores for one query: softmax statistics need one or two cross-lane
@@ -36,7 +44,6 @@ constexpr float NEG_INF = -__builtin_inff();
 
 // ------------------------------------------------------- attention over prompts
 constexpr int PT_K = 64;                 // keys of a tile
-constexpr float RISE = 8.f;              // powers of two that a p_j may grow to before the sums are multiplied
 
 // LDS rows of a tile: a power of two of 16-byte chunks, so that a row starts on
 // a fixed bank, and chunk c of row r lies at position c ^ swz(r).  The 32 rows
@@ -180,13 +187,15 @@ template <class T, int D> struct Sums {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
     top = max32(top);
-    // mc may lag behind the largest score: p stays below 2^RISE, and o is seldom multiplied
-    if (__ballot(top > RISE || mc == NEG_INF)) {
+    // mc may lag behind the largest score by LAG more than LOW, so that o is seldom multiplied.  (binary16, 8192 tokens of
+    // 56 heads of 128, scores of deviation 1 and 3: LAG 2 1001 and 1039 us, 4 991 and 1022, 8 991 and 1005.)
+    if (__ballot(top > T::LOW + T::LAG || mc == NEG_INF)) {
       const bool none = mc == NEG_INF;
-      const float up = none ? (top == NEG_INF ? 0.f : top) : fmaxf(top, 0.f);
+      const float low = top - T::LOW;
+      const float up = none ? (top == NEG_INF ? 0.f : low) : fmaxf(low, 0.f);
       // where there was no score yet o and l are zero, whatever they are multiplied by
       const float alpha = none ? 1.f : exp2_fast(-up);
-      mc = none ? top : mc + up;
+      mc = none ? low : mc + up;
       l *= alpha;
 #pragma unroll
       for (int t = 0; t < L::DT; ++t)
@@ -684,7 +693,7 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
   f4 o[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) o[f] = (f4)(0.f);
-  float mc = NEG_INF, l = 0.f;                     // mc: c times the largest score so far
+  float mc = NEG_INF, l = 0.f;                     // mc: HIGH under c times the largest score so far
   const int32_t* row = pg.table + (int64_t)max(slot, 0) * pg.max_pages;
   const int64_t head_stride = (int64_t)pg.page * dim, page_stride = head_stride * kv_heads;
 
@@ -746,7 +755,7 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
     float mt = NEG_INF;
 #pragma unroll
     for (int i = 0; i < 4; ++i) mt = fmaxf(mt, fmaxf(s[0][i], s[1][i]));
-    const float top = fmaxf(mc, max16(mt) * c);
+    const float top = fmaxf(mc, max16(mt) * c - T::HIGH);
     const float base = top == NEG_INF ? 0.f : top;   // rows whose scores so far are all -inf
     const float alpha = exp2_fast(mc - base);
     mc = top;

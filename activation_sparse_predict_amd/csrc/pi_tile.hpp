@@ -22,7 +22,9 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 
+// LOW, LAG, HIGH: powers of two of the weights in a softmax, see pi_attn.hpp.
 struct H16 {                       // IEEE binary16
+  static constexpr float LOW = 11.f, LAG = 4.f, HIGH = LOW + LAG;
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ f16v mma32(u4 a, u4 b, f16v c) {
@@ -38,6 +40,7 @@ struct H16 {                       // IEEE binary16
 };
 
 struct B16 {                       // bfloat16
+  static constexpr float LOW = 0.f, LAG = 8.f, HIGH = 0.f;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ f16v mma32(u4 a, u4 b, f16v c) {
