@@ -430,7 +430,7 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
   constexpr int NT = 4 * WAVE, S = D <= 128 ? 3 : 2;
   using R = Ring<D, S, NT>;
   __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES];   // K tiles, then V tiles
-  __shared__ int64_t ids[SH_IDS];                  // first element of 16 keys in the layer's pages, or -1
+  __shared__ int64_t ids[SH_IDS];                  // first element of 16 keys in the layer's pages, or -1: not seen
 
   // the query tiles of one share run on one die (block b runs on die b % 8)
   const int pair = blockIdx.x % 8 + 8 * (blockIdx.x / (8 * qtiles)), qt = blockIdx.x / 8 % qtiles;
@@ -473,9 +473,10 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
     bool bad = false;
     const int at = 4 * base + tid;
     if (at < 4 * last) {
-      const int x = min(at, total / 16 - 1), id = usable_page(table[x / per], pg.pages);
-      bad = id < 0;
-      ids[tid] = bad ? -1 : (((int64_t)id * kv_heads + g) * pg.page + x % per * 16) * dim;
+      const bool there = at < total / 16;          // the last tile may be short
+      const int x = there ? at : 0, id = usable_page(table[x / per], pg.pages);
+      bad = id < 0 && there;
+      ids[tid] = bad || !there ? -1 : (((int64_t)id * kv_heads + g) * pg.page + x % per * 16) * dim;
       if (bad) atomicOr(pg.flags, PI_CACHE_EPAGE);
     }
     return __syncthreads_or(bad) != 0;
@@ -485,7 +486,7 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
     const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)v), h = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
     return (int64_t)((uint64_t)h << 32 | a);
   };
-  // a tile into LDS; keys of a broken page are zeros
+  // a tile into LDS; keys that are not seen are zeros: with anything else there, 0 times an infinity would be NaN
   auto fetch = [&](int tile, int base) {
 #pragma unroll
     for (int i = 0; i < R::LD; ++i) {
@@ -523,13 +524,16 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
       for (int i = 0; i < 4; ++i)
         if (place(4 * (t - base) + i) < 0) bits &= ~(1u << i);
     }
-    if (total - t * PT_K < PT_K) bits &= (1u << (total - t * PT_K) / 16) - 1;
+    if (total - t * PT_K < PT_K) {
+      bits &= (1u << (total - t * PT_K) / 16) - 1;
+      any = true;
+    }
     seen |= bits << 4 * (t % S);
     fetch(t, base);
   };
   for (int t = first; t < min(last, first + S - 1); ++t) ahead(t);
-  // what was fetched for the S - 2 tiles behind this one may still be on its way; at the end, and where a broken page's
-  // keys were not loaded, there are fewer
+  // what was fetched for the S - 2 tiles behind this one may still be on its way; at the end, and where keys that are not
+  // seen were not loaded (`any`), there are fewer
   auto turn = [&](int t) {
     if (t + S - 2 < last && !any) arrive<(S - 2) * 2 * R::LD>();
     else arrive<0>();

@@ -121,3 +121,21 @@ def test_decode_of_many_keys_of_small_weight(prefix, first_value):
     cache.k_pool[:, first, :, 0, 0] = 25.05 * math.log(2) * 2
     cache.v_pool[:, first, :, 0] = first_value
     check_decode(cache, q, prefix, 70000 / 64 + 256)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("shared", [1, 3, 5, 22, 23])
+def test_decode_infinite_value_in_the_last_common_keys(shared, dim, dtype):
+    """An infinite value of a key that is seen makes the result infinite, whatever stands behind the common keys."""
+    lens = [16 * shared + 1, 16 * shared + 40]
+    cache = make_cache(23, dtype, 1, dim, 16, lens, shared=shared)
+    cache.v_pool[:, int(cache.table[0, shared - 1]), :, 7, 3] = float("inf")
+    q = normal(4, 2, 4, dim, dtype=TYPES[dtype])
+    out = torch.full_like(q, float("nan"))
+    pi.attn_decode(cache, 1, q, out, prefix=ints([shared]))
+    assert (out[..., 3] == float("inf")).all()
+    ks, vs = held_by(cache, 1)
+    ref, tol = attn_ref.decode(q, ks, vs)
+    keep = [i for i in range(dim) if i != 3]
+    attn_ref.check(out[..., keep], ref[..., keep], tol[..., keep])
