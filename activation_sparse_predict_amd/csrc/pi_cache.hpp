@@ -309,8 +309,13 @@ __device__ __forceinline__ int uses(const int32_t* ref) {
 }
 
 // The listed slots become empty; pages that no slot uses any more go to the stack, the lowest on top.
-// Until they are collected such pages carry a count of -1, so that their order does not depend on timing.
+// First every listed use is taken off its page's count; a page that is held more often than counted shows as a count that
+// was not positive, and then all of them are put back and the call is refused.  Pages left without a use are marked by a
+// count of GONE, which one thread for each sets and counts, so neither the marks nor their number depend on timing, and
+// the pool is searched for the marks in the stack's order.  (One slot of 3001 tokens: 11.6 us, 32 of them 25.1 us; without
+// the check of the counts 10.8 and 23.2 us.)
 __global__ void __launch_bounds__(PL_T) k_cache_release(Meta m, const int32_t* __restrict__ seqs, int n) {
+  constexpr int GONE = INT32_MIN;
   __shared__ int slot[MAX_N];
   for (int i = threadIdx.x; i < n; i += blockDim.x) slot[i] = seqs[i];
   __syncthreads();
@@ -323,39 +328,52 @@ __global__ void __launch_bounds__(PL_T) k_cache_release(Meta m, const int32_t* _
   if (top < 0 || top > m.pages) bad |= PI_CACHE_EPAGE;
   if (refuse(bad, m.words)) return;
   const int w = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1), waves = blockDim.x / WAVE;
-  for (int i = w; i < n; i += waves) {
-    const int32_t* row = m.table + (int64_t)slot[i] * m.max_pages;
-    for (int j = lane; j < pages_of(m.lens[slot[i]], m.page); j += WAVE)
-      if ((unsigned)row[j] >= (unsigned)m.pages) bad |= PI_CACHE_EPAGE;
-  }
+  // f(page) for every place of every listed slot, in no order; several waves share a slot where there are few
+  const int parts = n < waves ? waves / n : 1, part = n < waves ? w / n : 0;
+  auto each = [&](auto f) {
+    for (int i = n < waves ? w % n : w; i < n && part < parts; i += waves) {
+      const int32_t* row = m.table + (int64_t)slot[i] * m.max_pages;
+      const int held = pages_of(m.lens[slot[i]], m.page);
+      for (int j = part * WAVE + lane; j < held; j += parts * WAVE) f(row[j]);
+    }
+  };
+  each([&](int p) {
+    if ((unsigned)p >= (unsigned)m.pages) bad |= PI_CACHE_EPAGE;
+  });
   if (refuse(bad, m.words)) return;
-  for (int i = w; i < n; i += waves) {
-    const int32_t* row = m.table + (int64_t)slot[i] * m.max_pages;
-    for (int j = lane; j < pages_of(m.lens[slot[i]], m.page); j += WAVE) {
-      const int was = atomicSub(&m.ref[row[j]], 1);
-      if (was == 1) {
-        atomicExch(&m.ref[row[j]], -1);
-      } else if (was <= 0) {                       // held more often than it was counted
-        atomicAdd(&m.ref[row[j]], 1);
-        atomicOr(&m.words[1], PI_CACHE_EPAGE);
-      }
+  each([&](int p) {
+    if (atomicSub(&m.ref[p], 1) <= 0) bad |= PI_CACHE_EPAGE;
+  });
+  bool back = refuse(bad, m.words);
+  int gone = 0, total = 0;
+  if (!back) {
+    each([&](int p) { gone += atomicCAS(&m.ref[p], 0, GONE) == 0; });
+    block_scan(gone, total);
+    // more pages than there are places: the stack held one of them already
+    back = refuse(total > m.pages - top ? PI_CACHE_EPAGE : 0, m.words);
+    if (back) {
+      each([&](int p) { atomicCAS(&m.ref[p], GONE, 0); });
+      __syncthreads();
     }
   }
-  __syncthreads();
+  if (back) {
+    each([&](int p) { atomicAdd(&m.ref[p], 1); });
+    return;
+  }
   for (int i = threadIdx.x; i < n; i += blockDim.x) m.lens[slot[i]] = 0;
   int at = top;
   for (int base = 0; base < m.pages; base += blockDim.x) {
     const int p = m.pages - 1 - (base + (int)threadIdx.x);
-    const int mine = p >= 0 && uses(&m.ref[p]) == -1;
-    int total;
-    const int pos = at + block_scan(mine, total);
+    const int mine = p >= 0 && uses(&m.ref[p]) == GONE;
+    int here;
+    const int pos = at + block_scan(mine, here);
     if (mine) {
       m.ref[p] = 0;
       if (pos < m.pages) m.free[pos] = p;
     }
-    at += total;
+    at += here;
   }
-  if (threadIdx.x == 0) m.words[0] = min(at, m.pages);
+  if (threadIdx.x == 0) m.words[0] = top + total;
 }
 
 // The pages in use move to the front of the pool: the i-th page in use at or behind place `used` goes to the
