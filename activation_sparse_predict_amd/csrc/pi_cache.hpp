@@ -55,16 +55,21 @@ __device__ __forceinline__ bool twice(const int* slots, int i) {
   return any;
 }
 
-// The pages that `need` pops take from the stack: free, in range, and as many as there are.
-__device__ __forceinline__ int stack_errors(const Meta& m, int total) {
+// The pages that `total` pops take from the stack: in range, free, each there once, and as many as there are.  Each
+// page's count becomes 1, which tells a page that comes twice; `taken` of these are the thread's, for stack_back.
+__device__ __forceinline__ int stack_errors(const Meta& m, int total, int& taken) {
   const int top = m.words[0];
+  taken = 0;
   if (top < 0 || top > m.pages) return PI_CACHE_EPAGE;
   if (total > top) return PI_CACHE_EFULL;
-  for (int i = threadIdx.x; i < total; i += blockDim.x) {
+  for (int i = threadIdx.x; i < total; i += blockDim.x, ++taken) {
     const int p = m.free[top - 1 - i];
-    if ((unsigned)p >= (unsigned)m.pages || m.ref[p] != 0) return PI_CACHE_EPAGE;
+    if ((unsigned)p >= (unsigned)m.pages || atomicCAS(&m.ref[p], 0, 1) != 0) return PI_CACHE_EPAGE;
   }
   return 0;
+}
+__device__ __forceinline__ void stack_back(const Meta& m, int taken) {
+  for (int i = 0; i < taken; ++i) m.ref[m.free[m.words[0] - 1 - (int)threadIdx.x - i * (int)blockDim.x]] = 0;
 }
 
 // Room for counts[i] more tokens in slot seqs[i]: pages from the stack, in the order of the list.
@@ -90,8 +95,9 @@ k_cache_extend(Meta m, const int32_t* __restrict__ seqs, const int32_t* __restri
     block_scan(need, total);
     carry = min(carry + total, m.pages + 1);       // more than there are is all the same
   }
-  bad |= stack_errors(m, carry);
-  if (refuse(bad, m.words)) return;
+  int taken;
+  bad |= stack_errors(m, carry, taken);
+  if (refuse(bad, m.words)) return stack_back(m, taken);
   const int top = m.words[0];
   int at = 0;
   for (int base = 0; base < n; base += blockDim.x) {
@@ -107,7 +113,6 @@ k_cache_extend(Meta m, const int32_t* __restrict__ seqs, const int32_t* __restri
     for (int j = 0; j < need; ++j) {
       const int p = m.free[top - 1 - before - j];
       m.table[(int64_t)slot[i] * m.max_pages + have + j] = p;
-      m.ref[p] = 1;
     }
     if (i < n) m.lens[slot[i]] = len + counts[i];
     at += total;
@@ -231,8 +236,11 @@ k_cache_fork(Meta m, const int32_t* __restrict__ parents, const int32_t* __restr
     for (int u = 0; u < U; ++u)
       if (page[u] != -2 && ref[u] <= 0) bad |= PI_CACHE_EPAGE;
   }
-  bad |= stack_errors(m, all);
-  if (refuse(bad, m.words)) return;
+  // a free page in a parent's table has been seen by now; from here on its count may be 1
+  __syncthreads();
+  int taken;
+  bad |= stack_errors(m, all, taken);
+  if (refuse(bad, m.words)) return stack_back(m, taken);
   int at = 0;
   for (int base = 0; base < n; base += blockDim.x) {
     const int i = base + threadIdx.x;
@@ -244,7 +252,6 @@ k_cache_fork(Meta m, const int32_t* __restrict__ parents, const int32_t* __restr
       plan.src[before] = m.table[(int64_t)dad[i] * m.max_pages + whole];
       plan.dst[before] = p;
       m.table[(int64_t)kid[i] * m.max_pages + whole] = p;
-      m.ref[p] = 1;
     }
     if (i < n) m.lens[kid[i]] = len_of[i];
     at += total;

@@ -77,3 +77,36 @@ def test_many_slots_that_share_pages():
         p.c.release(ints(gone))
         p.check(pool=False)
     assert len(p.m.free) == 700
+
+
+@pytest.mark.parametrize("first,second", [(0, 1), (0, 5), (3, 4)])
+def test_a_page_that_is_twice_on_the_stack(first, second):
+    """It would go to two places: the call that needs both is refused."""
+    p = Pair(1, 1300, 1, 16, 8, 6, 1200)
+    p.extend_append([0], [30])
+    c, top = p.c, int(p.c.words[0])
+    was = int(c.free[top - 1 - second])
+    c.free[top - 1 - second] = int(c.free[top - 1 - first])
+    for _ in range(5):
+        refused(p, lambda: c.extend(ints([1]), ints([16 * (second + 1)])), pi.PI_CACHE_EPAGE)
+        refused(p, lambda: c.extend(ints([1, 2, 3]), ints([16 * 400, 16, 16 * 700])), pi.PI_CACHE_EPAGE)
+        refused(p, lambda: c.extend(ints([1, 9]), ints([16 * 1100, 1])), pi.PI_CACHE_EPAGE | pi.PI_CACHE_ESLOT)
+        if second < 5:
+            refused(p, lambda: c.fork(ints([0] * 5), ints([1, 2, 3, 4, 5])), pi.PI_CACHE_EPAGE)
+    c.free[top - 1 - second] = was
+    p.m.extend([1, 2], [16 * 1100, 3])
+    c.extend(ints([1, 2]), ints([16 * 1100, 3]))
+    p.m.fork([0] * 3, [3, 4, 5])
+    c.fork(ints([0] * 3), ints([3, 4, 5]))
+    p.check()
+
+
+def test_a_free_page_in_a_parents_table():
+    """The page that a copy would go to is the parent's own last page by its table, and counted as free."""
+    p = Pair(1, 12, 1, 16, 8, 6, 8)
+    p.extend_append([0], [30])
+    page = int(p.c.table[0, 1])
+    top = int(p.c.words[0])
+    p.c.ref[page], p.c.free[top], p.c.words[0] = 0, page, top + 1
+    for _ in range(5):
+        refused(p, lambda: p.c.fork(ints([0]), ints([1])), pi.PI_CACHE_EPAGE)
