@@ -69,7 +69,7 @@ class PiCache(ctypes.Structure):
 
 
 # bits of a cache's error word
-PI_CACHE_ESLOT, PI_CACHE_EPAGE, PI_CACHE_EFULL, PI_CACHE_ELENGTH = 1, 2, 4, 8
+PI_CACHE_ESLOT, PI_CACHE_EPAGE, PI_CACHE_EFULL, PI_CACHE_ELENGTH, PI_CACHE_EPREFIX = 1, 2, 4, 8, 16
 
 
 # kernels of one layer, in the order the trace events bracket them
@@ -502,7 +502,8 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
     """Attention of one query row [heads][dim] per batch row over what its slot holds in a layer.
 
     seqs: the slots (None: row b is slot b).  prefix: an int32 tensor of one element, how many
-    leading pages the slots that are not empty have in common.  ws: as Cache.attn_workspace."""
+    leading pages the slots that are not empty have in common (PI_CACHE_EPREFIX in the error
+    word where they do not).  ws: as Cache.attn_workspace."""
     shape = q.shape
     _need(len(shape) == 3 and shape == out.shape and shape[2] == cache.dim and q.dtype == out.dtype == cache.dtype,
           "attn_decode: q, out")

@@ -169,7 +169,7 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
                          dim3((unsigned)(8 * up_div((int64_t)cache->kv_heads * u.shares, 8) * u.qtiles)), dim3(256), 0,
                          st, pg, rows_of(q), seqs, prefix, batch, heads, cache->kv_heads, dim, u.shares, u.qtiles, c,
                          floats(W.cpart), floats(W.cstat));
-    hipLaunchKernelGGL((pia::k_attn_decode<T, D>), dim3((unsigned)u.blocks, (unsigned)u.tiles),
+    hipLaunchKernelGGL((pia::k_attn_decode<T, D>), dim3((unsigned)u.blocks, (unsigned)u.tiles + (prefix ? 1 : 0)),
                        dim3(pia::DC_WAVES * pia::WAVE), 0, st, pg, rows_of(q), static_cast<uint16_t*>(out->p),
                        out->token_stride, out->head_stride, seqs, prefix, batch, heads, cache->kv_heads, dim, u.free,
                        u.shares, c, reinterpret_cast<int4*>(base), floats(W.part), floats(W.stat));

@@ -247,6 +247,7 @@ typedef struct {
 #define PI_CACHE_EPAGE 2   /* a page number or use count that cannot be (a broken table or stack) */
 #define PI_CACHE_EFULL 4   /* not enough free pages */
 #define PI_CACHE_ELENGTH 8 /* a negative length, or one beyond the slot's table row */
+#define PI_CACHE_EPREFIX 16 /* pages given as common to a batch that its tables do not have in common */
 
 /* A paged key/value cache of `slots` sequences.
  *  k, v:  [layers][pages][kv_heads][page][dim], 16-byte aligned; page a
@@ -318,9 +319,11 @@ pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v
  * NULL (then batch <= slots).  A slot without tokens gives zeros.
  * prefix: NULL, or one int32 on the device: how many leading pages all the
  * batch's slots that are not empty have in common, page for page.  These are
- * read once for the whole batch.  The pages of a slot that is too short to
- * hold them do not count as common, and a number that no table row can hold
- * counts as 0.
+ * read once for the whole batch, by the table of the first slot that holds
+ * them; where another slot's table differs there the results of that row are
+ * those for the first one's pages, and the error word gets PI_CACHE_EPREFIX.
+ * The pages of a slot that is too short to hold them do not count as common,
+ * and a number that no table row can hold counts as 0.
  */
 size_t pi_attn_workspace_bytes(const pi_cache* cache, int32_t batch, int32_t heads);
 pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q, const pi_heads* out, int32_t batch,
