@@ -54,7 +54,8 @@ class Decoder:
         self.cache = pi.Cache.create(layers, pages, kv_heads, page, dim, slots, max_pages, device=device)
         self.one = torch.ones(slots, dtype=torch.int32, device=device)
         self.rows = torch.arange(slots + 1, dtype=torch.int32, device=device)
-        self.prefix = torch.zeros(1, dtype=torch.int32, device=device)
+        self.prefix = torch.zeros(1, dtype=torch.int32, device=device)   # pages that all slots in use have in common
+        self.used = set()                              # slots that were filled
 
     def ints(self, values):
         return torch.tensor(values, dtype=torch.int32, device=self.device)
@@ -89,6 +90,8 @@ class Decoder:
     def prompt(self, x, slot, trace=None):
         """Whole prompt x [tokens, width] into an empty slot; the outputs of its rows."""
         h, g = self.heads, self.kv_heads
+        self.used.add(slot)
+        self.prefix.zero_()
         cu, seqs = self.ints([0, x.shape[0]]), self.ints([slot])
         self.cache.extend(seqs, self.ints([x.shape[0]]))
         for i in range(len(self.ffn)):
@@ -111,9 +114,12 @@ class Decoder:
         return x
 
     def share(self, parent, children, tokens):
-        """Children continue the parent's `tokens` tokens; their common pages are read once from now on."""
+        """Children continue the parent's `tokens` tokens; their common pages are read once from now on, unless slots are in use
+        that hold something else."""
         self.cache.fork(self.ints([parent] * len(children)), self.ints(children))
-        self.prefix.fill_(tokens // self.cache.page)
+        alone = self.used <= {parent, *children}
+        self.prefix.fill_(tokens // self.cache.page if alone else 0)
+        self.used.update(children)
 
 
 def main():
