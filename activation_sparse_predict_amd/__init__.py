@@ -153,6 +153,49 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_torch = None                                          # an import statement in every call would take its time
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _gpu_of(t) -> Optional[int]:
+    """The GPU of a tensor; None for an address, whose caller sees to the current GPU."""
+    dev = t.get_device() if hasattr(t, "get_device") else -1
+    return dev if dev >= 0 else None
+
+
+def _stream_on(dev: Optional[int], stream):
+    """The handle of a stream, or of the current stream of a GPU."""
+    if dev is None:
+        return _stream(stream)
+    if stream is None:
+        return (_torch or _load_torch())._C._cuda_getCurrentRawStream(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise PiError(PI_EINVAL, "stream of another GPU")
+    return _stream(stream)
+
+
+def _on(dev: Optional[int], call, *args) -> int:
+    """A call of the library with GPU `dev` current (None: as it is).  A kernel goes to the current GPU where its stream's
+    handle is 0, which every GPU's default stream has."""
+    if dev is None:
+        return call(*args)
+    gpus = (_torch or _load_torch())._C
+    here = gpus._cuda_getDevice()
+    if here == dev:
+        return call(*args)
+    gpus._cuda_setDevice(dev)
+    try:
+        return call(*args)
+    finally:
+        gpus._cuda_setDevice(here)
+
+
 def _check(status: int, where: str):
     if status != PI_OK:
         raise PiError(status, where)
@@ -233,27 +276,33 @@ def workspace_bytes(layers, batch: int = 1) -> int:
     return int(lib().pi_workspace_bytes(ctypes.cast(arr, ctypes.c_void_p), len(layers), batch))
 
 
-def alloc_workspace(layers, batch: int = 1, device="cuda"):
+def alloc_workspace(layers, batch: int = 1, device=None):
+    """A workspace on `device`: unless it is given, where the first layer lies."""
     import torch
     n = workspace_bytes(layers, batch)
     if n == 0:
         raise PiError(PI_EINVAL, "workspace_bytes")
+    if device is None:
+        gpu = _gpu_of((layers if isinstance(layers, DeviceLayer) else layers[0]).A)
+        device = "cuda" if gpu is None else torch.device("cuda", gpu)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def predict(layer: DeviceLayer, x, idx, count, scores=None, mask=None, ws=None, batch: int = 1,
             stream=None):
+    dev = _gpu_of(x)
     ws = alloc_workspace(layer, batch) if ws is None else ws
-    st = lib().pi_predict(ctypes.byref(layer.struct), _p(x), batch, _p(scores), _p(mask), _p(idx),
-                          _p(count), _p(ws), ws.numel(), _stream(stream))
+    st = _on(dev, lib().pi_predict, ctypes.byref(layer.struct), _p(x), batch, _p(scores), _p(mask), _p(idx),
+             _p(count), _p(ws), ws.numel(), _stream_on(dev, stream))
     _check(st, "pi_predict")
 
 
 def sparse_ffn(layer: DeviceLayer, x, idx, count, y, mask=None, ws=None, batch: int = 1,
                stream=None):
+    dev = _gpu_of(x)
     ws = alloc_workspace(layer, batch) if ws is None else ws
-    st = lib().pi_sparse_ffn(ctypes.byref(layer.struct), _p(x), batch, _p(idx), _p(count),
-                             _p(mask), _p(y), _p(ws), ws.numel(), _stream(stream))
+    st = _on(dev, lib().pi_sparse_ffn, ctypes.byref(layer.struct), _p(x), batch, _p(idx), _p(count),
+             _p(mask), _p(y), _p(ws), ws.numel(), _stream_on(dev, stream))
     _check(st, "pi_sparse_ffn")
 
 
@@ -287,9 +336,10 @@ class Stack:
 
     def __call__(self, x, out, counts=None, trace=None, stream=None, nz_counts=None):
         tr = None if trace is None else ctypes.cast(trace, ctypes.c_void_p)
-        st = lib().pi_ffn_stack(ctypes.cast(self.arr, ctypes.c_void_p), len(self.layers), _p(x),
-                                self.batch, _p(out), _p(counts), _p(nz_counts), tr, _p(self.ws),
-                                self.ws.numel(), _stream(stream))
+        dev = _gpu_of(x)
+        st = _on(dev, lib().pi_ffn_stack, ctypes.cast(self.arr, ctypes.c_void_p), len(self.layers), _p(x),
+                 self.batch, _p(out), _p(counts), _p(nz_counts), tr, _p(self.ws),
+                 self.ws.numel(), _stream_on(dev, stream))
         _check(st, "pi_ffn_stack")
 
 
@@ -304,8 +354,9 @@ def ffn_stack_static(layers, x, out, counts=None, trace=None, batch: int = 1, st
     """pi_ffn_stack_static: the stack on the library's own per-GPU scratch array (no workspace)."""
     arr = _layer_array(list(layers))
     tr = None if trace is None else ctypes.cast(trace, ctypes.c_void_p)
-    st = lib().pi_ffn_stack_static(ctypes.cast(arr, ctypes.c_void_p), len(arr), _p(x), batch, _p(out),
-                                   _p(counts), _p(nz_counts), tr, _stream(stream))
+    dev = _gpu_of(x)
+    st = _on(dev, lib().pi_ffn_stack_static, ctypes.cast(arr, ctypes.c_void_p), len(arr), _p(x), batch, _p(out),
+             _p(counts), _p(nz_counts), tr, _stream_on(dev, stream))
     _check(st, "pi_ffn_stack_static")
 
 
@@ -344,14 +395,6 @@ def _gpu(what: str, first, *tensors) -> int:
     if dev < 0:
         raise PiError(PI_EINVAL, what)
     return dev
-
-
-def _stream_on(dev: int, stream):
-    """The handle of a stream, or of the current stream of a GPU."""
-    if stream is not None:
-        return _stream(stream)
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _ints(t, n: Optional[int], what: str) -> Optional[int]:
@@ -431,8 +474,8 @@ class Cache:
         """Room for counts[i] more tokens in slot seqs[i]."""
         n = seqs.numel()
         dev = _gpu("extend: tensors of one GPU", self.meta, seqs, counts)
-        _check(self._lib.pi_cache_extend(self._ref, _ints(seqs, n, "extend: seqs"), _ints(counts, n, "extend: counts"),
-                                         n, _stream_on(dev, stream)), "pi_cache_extend")
+        _check(_on(dev, self._lib.pi_cache_extend, self._ref, _ints(seqs, n, "extend: seqs"),
+                   _ints(counts, n, "extend: counts"), n, _stream_on(dev, stream)), "pi_cache_extend")
 
     def append(self, layer: int, k, v, cu, seqs, stream=None):
         """Rows cu[i] .. cu[i + 1] - 1 of k and v [tokens][kv_heads][dim] become the last tokens of slot seqs[i]."""
@@ -441,30 +484,30 @@ class Cache:
               and k.dtype == v.dtype == self.dtype, "append: k, v")
         n = seqs.numel()
         dev = _gpu("append: tensors of one GPU", self.meta, k, v, cu, seqs)
-        _check(self._lib.pi_cache_append(self._ref, layer, _heads(k, shape, "append: k"), _heads(v, shape, "append: v"),
-                                         shape[0], _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
-                                         _stream_on(dev, stream)), "pi_cache_append")
+        _check(_on(dev, self._lib.pi_cache_append, self._ref, layer, _heads(k, shape, "append: k"),
+                   _heads(v, shape, "append: v"), shape[0], _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
+                   _stream_on(dev, stream)), "pi_cache_append")
 
     def fork(self, parents, children, stream=None):
         """The empty slot children[i] becomes a copy of slot parents[i]."""
         n = parents.numel()
         dev = _gpu("fork: tensors of one GPU", self.meta, parents, children)
-        _check(self._lib.pi_cache_fork(self._ref, _ints(parents, n, "fork: parents"),
-                                       _ints(children, n, "fork: children"), n, self._ws, self._ws_bytes,
-                                       _stream_on(dev, stream)), "pi_cache_fork")
+        _check(_on(dev, self._lib.pi_cache_fork, self._ref, _ints(parents, n, "fork: parents"),
+                   _ints(children, n, "fork: children"), n, self._ws, self._ws_bytes, _stream_on(dev, stream)),
+               "pi_cache_fork")
 
     def release(self, seqs, stream=None):
         """The listed slots become empty."""
         n = seqs.numel()
         dev = _gpu("release: tensors of one GPU", self.meta, seqs)
-        _check(self._lib.pi_cache_release(self._ref, _ints(seqs, n, "release: seqs"), n, _stream_on(dev, stream)),
-               "pi_cache_release")
+        _check(_on(dev, self._lib.pi_cache_release, self._ref, _ints(seqs, n, "release: seqs"), n,
+                   _stream_on(dev, stream)), "pi_cache_release")
 
     def compact(self, moved=None, stream=None):
         """The pages in use move to the front of the pool; moved [pages]: the new place of each."""
         dev = _gpu("compact: tensors of one GPU", self.meta, moved)
-        _check(self._lib.pi_cache_compact(self._ref, _ints(moved, self.pages, "compact: moved"), self._ws,
-                                          self._ws_bytes, _stream_on(dev, stream)), "pi_cache_compact")
+        _check(_on(dev, self._lib.pi_cache_compact, self._ref, _ints(moved, self.pages, "compact: moved"), self._ws,
+                   self._ws_bytes, _stream_on(dev, stream)), "pi_cache_compact")
 
     def errors(self) -> int:
         """The error word (waits for the device)."""
@@ -493,9 +536,9 @@ def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
     _need(n > 0, "attn_prompt: cu")
     offsets, what = _ints(cu, None, "attn_prompt: cu"), "attn_prompt: strides"
     dev = _gpu("attn_prompt: tensors of one GPU", q, k, v, out, cu)
-    _check((_lib or lib()).pi_attn_prompt(_heads(q, qs, what), _heads(k, ks, what), _heads(v, ks, what),
-                                          _heads(out, qs, what), qs[0], qs[1], ks[1], qs[2], _dtype_of(q), offsets, n,
-                                          scale, _stream_on(dev, stream)), "pi_attn_prompt")
+    _check(_on(dev, (_lib or lib()).pi_attn_prompt, _heads(q, qs, what), _heads(k, ks, what), _heads(v, ks, what),
+               _heads(out, qs, what), qs[0], qs[1], ks[1], qs[2], _dtype_of(q), offsets, n, scale,
+               _stream_on(dev, stream)), "pi_attn_prompt")
 
 
 def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale: float = 0.0, ws=None, stream=None):
@@ -511,9 +554,9 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
     batch, heads, _ = shape
     ws = cache.attn_workspace(batch, heads) if ws is None else ws
     what = "attn_decode: strides"
-    _check(cache._lib.pi_attn_decode(cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch, heads,
-                                     _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"),
-                                     scale, ws.data_ptr(), ws.numel(), _stream_on(dev, stream)), "pi_attn_decode")
+    _check(_on(dev, cache._lib.pi_attn_decode, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch,
+               heads, _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,
+               ws.data_ptr(), ws.numel(), _stream_on(dev, stream)), "pi_attn_decode")
 
 
 class Q4Matrix:
@@ -559,9 +602,8 @@ def matvec(mat: Q4Matrix, x, y, stream=None):
     if batch == 1:                                     # a row's stride says nothing there
         ldx, ldy = xs[1], ys[1]
     dev = _gpu("matvec: tensors of one GPU", mat.nibbles, x, y)
-    _check(mat._lib.pi_matvec(*mat._args, x.data_ptr(), _dtype_of(x), ldx, y.data_ptr(), _dtype_of(y), ldy, batch,
-                              mat._ws, mat._ws_bytes, _stream_on(dev, stream)), "pi_matvec")
-
+    _check(_on(dev, mat._lib.pi_matvec, *mat._args, x.data_ptr(), _dtype_of(x), ldx, y.data_ptr(), _dtype_of(y), ldy,
+               batch, mat._ws, mat._ws_bytes, _stream_on(dev, stream)), "pi_matvec")
 
 
 # ------------------------------------------------------- HIP runtime plumbing
