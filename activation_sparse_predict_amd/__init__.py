@@ -10,7 +10,7 @@ Entry points (same names and meaning as the C functions):
   predict(layer, x, idx, count, scores=None, mask=None, ws=None)
   sparse_ffn(layer, x, idx, count, y, mask=None, ws=None)
   ffn_stack(layers, x, out, counts=None, trace=None, ws=None, nz_counts=None)
-  Cache(k_pool, v_pool, meta, slots, max_pages) with .extend, .append, .fork, .release, .compact
+  Cache(k_pool, v_pool, meta, slots, max_pages) with .extend, .append, .fork, .release, .compact, .reserve
   attn_prompt(q, k, v, out, cu)
   attn_decode(cache, layer, q, out, prefix=None, seqs=None)
   Q4Matrix(nibbles, scales, bias, batch) and matvec(mat, x, y)
@@ -422,8 +422,9 @@ class Cache:
 
     k_pool, v_pool: [layers][pages][kv_heads][page][dim], float16 or bfloat16.  meta: the page
     tables, one int32 tensor; .table, .lens, .ref, .free and .words are views of its parts.
-    Workspaces are allocated on first use and kept, so a call that is captured into a graph
-    has to have run once before with the same sizes; calls on one cache belong on one stream."""
+    The workspace of attn_decode is one buffer that grows when a call needs more, never inside a
+    capture: a call that is captured has to have run once before with the same sizes, or .reserve
+    has been called.  Calls on one cache belong on one stream."""
 
     def __init__(self, k_pool, v_pool, meta, slots: int, max_pages: int):
         import torch
@@ -451,7 +452,7 @@ class Cache:
         self.dtype, self._lib = k_pool.dtype, lib()
         self.ws = torch.empty(n, dtype=torch.uint8, device=k_pool.device)
         self._ws, self._ws_bytes = self.ws.data_ptr(), n
-        self._attn_ws = {}
+        self._attn_need, self._attn_ws, self._attn_bytes, self._attn_before = {}, None, 0, []
 
     @staticmethod
     def meta_words(slots: int, max_pages: int, pages: int) -> int:
@@ -513,17 +514,33 @@ class Cache:
         """The error word (waits for the device)."""
         return int(self.words[1])
 
+    def reserve(self, batch: int, heads: int):
+        """Memory for attn_decode of up to `batch` rows of `heads` heads, so that no call of these has to take any."""
+        self._attn_grow(max(self._attn_needs(b, heads) for b in range(1, batch + 1)) if batch > 0 else 0)
+
     def attn_workspace(self, batch: int, heads: int):
-        """The workspace of attn_decode for these sizes."""
-        ws = self._attn_ws.get((batch, heads))
-        if ws is None:
-            import torch
-            n = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
-            _need(n > 0, "attn_decode: batch, heads")
-            # memory taken while a graph is captured belongs to that graph
-            _need(not torch.cuda.is_current_stream_capturing(), "attn_decode: first call of these sizes inside a capture")
-            ws = self._attn_ws[batch, heads] = torch.empty(n, dtype=torch.uint8, device=self.k_pool.device)
-        return ws
+        """The workspace of attn_decode for these sizes: a buffer of at least as many bytes, the same for all sizes."""
+        n = self._attn_need.get((batch, heads)) or self._attn_needs(batch, heads)
+        if n > self._attn_bytes:
+            self._attn_grow(n)
+        return self._attn_ws
+
+    def _attn_needs(self, batch: int, heads: int) -> int:
+        n = self._attn_need[batch, heads] = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
+        return n
+
+    def _attn_grow(self, n: int):
+        import torch
+        _need(n > 0, "attn_decode: batch, heads")
+        if n <= self._attn_bytes:
+            return
+        # memory taken while a graph is captured belongs to that graph
+        _need(not torch.cuda.is_current_stream_capturing(), "attn_decode: a call inside a capture needs more workspace")
+        # graphs hold the buffers before this one, so these stay; twice the size each time, they are smaller than it together
+        if self._attn_ws is not None:
+            self._attn_before.append(self._attn_ws)
+        self._attn_bytes = max(n, 2 * self._attn_bytes)
+        self._attn_ws = torch.empty(self._attn_bytes, dtype=torch.uint8, device=self.k_pool.device)
 
 
 def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
