@@ -417,6 +417,57 @@ def _heads(t, shape, what: str):
     return ctypes.byref(PiHeads(t.data_ptr() or None, token if shape[0] > 1 else 0, head if shape[1] > 1 else 0))
 
 
+def _stream_of(dev: int, handle: int):
+    import torch
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+def _capturing(dev: int, handle: Optional[int] = None) -> bool:
+    """Whether a graph is being captured on a stream, or on the current one."""
+    import torch
+    if handle is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_stream_of(dev, handle)):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _mark(dev: int):
+    """An event behind the work of a GPU's current stream so far."""
+    import torch
+    if _capturing(dev):                                # what is captured runs after all that came before it
+        return None
+    stream = torch.cuda.current_stream(dev)
+    return stream.record_event()
+
+
+def _wait_for(dev: int, handle: int, event) -> bool:
+    """A stream waits for an event; False inside a capture, which cannot wait for what is outside of it."""
+    if _capturing(dev, handle):
+        return False
+    _stream_of(dev, handle).wait_event(event)
+    return True
+
+
+class _Scratch:
+    """Workspace memory that a handle keeps for its calls.
+
+    Torch gives out memory again when the work that uses it is on its way on the stream it was taken on, so that stream may
+    still be reading what another stream's call would write: such a stream waits, once, for the work there was when the
+    memory was taken.  (A capture begins when the work before it is done; torch.cuda.graph sees to that.)"""
+
+    def __init__(self, n: int, device):
+        import torch
+        self.mem = torch.empty(n, dtype=torch.uint8, device=device)
+        self.dev, self.address, self.bytes = self.mem.get_device(), self.mem.data_ptr(), n
+        self.streams, self.taken = {torch._C._cuda_getCurrentRawStream(self.dev)}, _mark(self.dev)
+
+    def on(self, handle: int) -> int:
+        """Its address, for a call on a stream."""
+        if handle not in self.streams and (self.taken is None or _wait_for(self.dev, handle, self.taken)):
+            self.streams.add(handle)
+        return self.address
+
+
 class Cache:
     """A paged key/value cache (pi_cache in include/pi.h) over tensors of the caller's.
 
@@ -450,9 +501,9 @@ class Cache:
         if n == 0:                                   # say which rule it is
             _check(lib().pi_cache_release(self._ref, None, 1, None), "Cache")
         self.dtype, self._lib = k_pool.dtype, lib()
-        self.ws = torch.empty(n, dtype=torch.uint8, device=k_pool.device)
-        self._ws, self._ws_bytes = self.ws.data_ptr(), n
-        self._attn_need, self._attn_ws, self._attn_bytes, self._attn_before = {}, None, 0, []
+        self._ws = _Scratch(n, k_pool.device)
+        self.ws = self._ws.mem
+        self._attn_need, self._attn_ws, self._attn_before = {}, None, []
 
     @staticmethod
     def meta_words(slots: int, max_pages: int, pages: int) -> int:
@@ -493,9 +544,9 @@ class Cache:
         """The empty slot children[i] becomes a copy of slot parents[i]."""
         n = parents.numel()
         dev = _gpu("fork: tensors of one GPU", self.meta, parents, children)
+        on = _stream_on(dev, stream)
         _check(_on(dev, self._lib.pi_cache_fork, self._ref, _ints(parents, n, "fork: parents"),
-                   _ints(children, n, "fork: children"), n, self._ws, self._ws_bytes, _stream_on(dev, stream)),
-               "pi_cache_fork")
+                   _ints(children, n, "fork: children"), n, self._ws.on(on), self._ws.bytes, on), "pi_cache_fork")
 
     def release(self, seqs, stream=None):
         """The listed slots become empty."""
@@ -507,8 +558,9 @@ class Cache:
     def compact(self, moved=None, stream=None):
         """The pages in use move to the front of the pool; moved [pages]: the new place of each."""
         dev = _gpu("compact: tensors of one GPU", self.meta, moved)
-        _check(_on(dev, self._lib.pi_cache_compact, self._ref, _ints(moved, self.pages, "compact: moved"), self._ws,
-                   self._ws_bytes, _stream_on(dev, stream)), "pi_cache_compact")
+        on = _stream_on(dev, stream)
+        _check(_on(dev, self._lib.pi_cache_compact, self._ref, _ints(moved, self.pages, "compact: moved"), self._ws.on(on),
+                   self._ws.bytes, on), "pi_cache_compact")
 
     def errors(self) -> int:
         """The error word (waits for the device)."""
@@ -516,31 +568,35 @@ class Cache:
 
     def reserve(self, batch: int, heads: int):
         """Memory for attn_decode of up to `batch` rows of `heads` heads, so that no call of these has to take any."""
-        self._attn_grow(max(self._attn_needs(b, heads) for b in range(1, batch + 1)) if batch > 0 else 0)
+        n = max(self._attn_needs(b, heads) for b in range(1, batch + 1)) if batch > 0 else 0
+        if n == 0 or self._attn_ws is None or n > self._attn_ws.bytes:
+            self._attn_grow(n, None)
 
     def attn_workspace(self, batch: int, heads: int):
         """The workspace of attn_decode for these sizes: a buffer of at least as many bytes, the same for all sizes."""
+        return self._attn_scratch(batch, heads, None).mem
+
+    def _attn_scratch(self, batch: int, heads: int, handle: Optional[int]) -> _Scratch:
+        """That workspace, for a call on a stream (None: the current one)."""
         n = self._attn_need.get((batch, heads)) or self._attn_needs(batch, heads)
-        if n > self._attn_bytes:
-            self._attn_grow(n)
+        if self._attn_ws is None or n > self._attn_ws.bytes:
+            self._attn_grow(n, handle)
         return self._attn_ws
 
     def _attn_needs(self, batch: int, heads: int) -> int:
         n = self._attn_need[batch, heads] = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
         return n
 
-    def _attn_grow(self, n: int):
-        import torch
+    def _attn_grow(self, n: int, handle: Optional[int]):
         _need(n > 0, "attn_decode: batch, heads")
-        if n <= self._attn_bytes:
-            return
         # memory taken while a graph is captured belongs to that graph
-        _need(not torch.cuda.is_current_stream_capturing(), "attn_decode: a call inside a capture needs more workspace")
+        _need(not (_capturing(self._ws.dev) or handle is not None and _capturing(self._ws.dev, handle)),
+              "attn_decode: a call inside a capture needs more workspace")
         # graphs hold the buffers before this one, so these stay; twice the size each time, they are smaller than it together
         if self._attn_ws is not None:
             self._attn_before.append(self._attn_ws)
-        self._attn_bytes = max(n, 2 * self._attn_bytes)
-        self._attn_ws = torch.empty(self._attn_bytes, dtype=torch.uint8, device=self.k_pool.device)
+            n = max(n, 2 * self._attn_ws.bytes)
+        self._attn_ws = _Scratch(n, self.k_pool.device)
 
 
 def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
@@ -569,11 +625,16 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
           "attn_decode: q, out")
     dev = _gpu("attn_decode: tensors of one GPU", cache.meta, q, out, prefix, seqs, ws)
     batch, heads, _ = shape
-    ws = cache.attn_workspace(batch, heads) if ws is None else ws
+    on = _stream_on(dev, stream)
+    if ws is None:
+        scratch = cache._attn_scratch(batch, heads, on)
+        memory, size = scratch.on(on), scratch.bytes
+    else:
+        memory, size = ws.data_ptr(), ws.numel()
     what = "attn_decode: strides"
     _check(_on(dev, cache._lib.pi_attn_decode, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch,
                heads, _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,
-               ws.data_ptr(), ws.numel(), _stream_on(dev, stream)), "pi_attn_decode")
+               memory, size, on), "pi_attn_decode")
 
 
 class Q4Matrix:
@@ -595,9 +656,10 @@ class Q4Matrix:
         _gpu("Q4Matrix: tensors of one GPU", nibbles, scales, bias)
         self.nibbles, self.scales, self.bias = nibbles, scales, bias
         self.struct = PiMat(_p(nibbles), _p(scales))
-        self.ws = torch.empty(n, dtype=torch.uint8, device=nibbles.device)
+        self._ws = _Scratch(n, nibbles.device)
+        self.ws = self._ws.mem
         self._args = ctypes.byref(self.struct), self.rows, self.cols, _p(bias)
-        self._ws, self._ws_bytes, self._lib = self.ws.data_ptr(), n, lib()
+        self._lib = lib()
 
     @classmethod
     def upload(cls, mat, bias=None, batch: int = 1, device="cuda") -> "Q4Matrix":
@@ -619,8 +681,9 @@ def matvec(mat: Q4Matrix, x, y, stream=None):
     if batch == 1:                                     # a row's stride says nothing there
         ldx, ldy = xs[1], ys[1]
     dev = _gpu("matvec: tensors of one GPU", mat.nibbles, x, y)
+    on = _stream_on(dev, stream)
     _check(_on(dev, mat._lib.pi_matvec, *mat._args, x.data_ptr(), _dtype_of(x), ldx, y.data_ptr(), _dtype_of(y), ldy,
-               batch, mat._ws, mat._ws_bytes, _stream_on(dev, stream)), "pi_matvec")
+               batch, mat._ws.on(on), mat._ws.bytes, on), "pi_matvec")
 
 
 # ------------------------------------------------------- HIP runtime plumbing

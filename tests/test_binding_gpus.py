@@ -45,6 +45,11 @@ def spy(pi, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: gpus[-1], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_setDevice", gpus.append, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", STREAMS.__getitem__, raising=False)
+    monkeypatch.setattr(pi, "_capturing", lambda *a: False, raising=False)
+    # events of the workspaces: where they are recorded, and which streams wait for them before which call
+    monkeypatch.setattr(pi, "_mark", lambda dev: ("mark", dev), raising=False)
+    s.waits = []
+    monkeypatch.setattr(pi, "_wait_for", lambda *a: s.waits.append((len(s.calls), *a)) or True, raising=False)
     return s
 
 
@@ -99,6 +104,35 @@ def test_a_stream_that_is_given(pi, spy):
         with pytest.raises(pi.PiError) as e:
             call()
         assert e.value.status == pi.PI_EINVAL and not spy.calls, name
+
+
+@pytest.mark.parametrize("name", ["pi_cache_fork", "pi_cache_compact", "pi_attn_decode", "pi_matvec"])
+def test_another_stream_waits_for_memory_that_was_taken_on_the_current_one(pi, spy, name):
+    """The memory may have been given back with work of the current stream still reading it."""
+    class Stream:
+        cuda_stream, device_index = 99, 1
+    half, some = torch.zeros(3, 4, 64, dtype=torch.float16), torch.zeros(2, 64)
+    c = pi.Cache.create(1, 8, 2, 16, 64, 4, 4, device="cpu")
+    mat = pi.Q4Matrix(torch.zeros(64, 32, dtype=torch.uint8), torch.zeros(64, 2, dtype=torch.float16), batch=2)
+    if name == "pi_attn_decode":
+        c.reserve(3, 4)
+
+    def call(stream):
+        if name == "pi_cache_fork":
+            c.fork(ints(0), ints(1), stream)
+        elif name == "pi_cache_compact":
+            c.compact(None, stream)
+        elif name == "pi_attn_decode":
+            pi.attn_decode(c, 0, half, half.clone(), stream=stream)
+        else:
+            pi.matvec(mat, some, some.clone(), stream=stream)
+    call(None)                                         # the stream it was taken on
+    assert spy.waits == [] and len(spy.calls) == 1
+    call(Stream())
+    assert spy.waits == [(1, 1, 99, ("mark", 1))]      # before the second call
+    call(Stream())
+    call(None)
+    assert len(spy.waits) == 1 and [c[2] for c in spy.calls] == [0, 99, 99, 0]
 
 
 def test_the_current_gpu_comes_back_after_an_error(pi, spy, monkeypatch):

@@ -92,3 +92,56 @@ def test_growth_inside_a_capture_is_refused():
     assert e.value.status == pi.PI_EINVAL
     graph.replay()
     torch.cuda.synchronize()
+
+
+def busy_reader(n):
+    """Memory of n bytes that the current stream reads a while from now, given back already; the copy, and what it has to be."""
+    block = torch.arange(n // 4, dtype=torch.int32, device=DEV)
+    want, copy = block.clone(), torch.empty_like(block)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    copy.copy_(block)
+    del block
+    return copy, want
+
+
+def test_first_call_on_another_stream_leaves_the_current_ones_memory_alone():
+    cache, q, out = setup()
+    want, side = torch.zeros_like(q), torch.cuda.Stream()
+    cache2, _, _ = setup()
+    pi.attn_decode(cache2, 1, q, want)
+    for _ in range(2):
+        copy, same = busy_reader(needs(cache, ROWS))
+        pi.attn_decode(cache, 1, q, out, stream=side)  # the first time takes the memory that was given back
+        torch.cuda.synchronize()
+        assert torch.equal(copy, same) and torch.equal(out, want)
+
+
+def test_products_on_another_stream_leave_the_current_ones_memory_alone():
+    rows, cols, batch = 2048, 1024, 32
+    q = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device=DEV)
+    sc = torch.rand(rows, cols // 32, device=DEV).half()
+    x, side = torch.randn(batch, cols, device=DEV), torch.cuda.Stream()
+    want, y = torch.empty(batch, rows, device=DEV), torch.zeros(batch, rows, device=DEV)
+    pi.matvec(pi.Q4Matrix(q, sc, batch=batch), x, want)
+    copy, same = busy_reader(int(pi.lib().pi_matvec_workspace_bytes(rows, cols, batch)) // 4 * 4)
+    mat = pi.Q4Matrix(q, sc, batch=batch)
+    pi.matvec(mat, x, y, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, same) and torch.equal(y, want)
+
+
+def test_calls_captured_on_a_stream_of_their_own():
+    """A graph's stream is another one than the memory was taken on; what is captured runs all the same."""
+    cache, q, out = setup()
+    want = torch.zeros_like(q)
+    pi.attn_decode(cache, 1, q, want)
+    torch.cuda.synchronize()
+    side = pi.HipStream()
+    graph = pi.HipGraph(side, lambda s: pi.attn_decode(cache, 1, q, out, stream=s))
+    for i in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        side.synchronize()
+        assert torch.equal(out, want), i
