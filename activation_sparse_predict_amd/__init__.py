@@ -630,7 +630,8 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
         scratch = cache._attn_scratch(batch, heads, on)
         memory, size = scratch.on(on), scratch.bytes
     else:
-        memory, size = ws.data_ptr(), ws.numel()
+        _need(ws.is_contiguous(), "attn_decode: ws")   # any other's elements lie elsewhere than one after the other
+        memory, size = ws.data_ptr(), ws.numel() * ws.element_size()
     what = "attn_decode: strides"
     _check(_on(dev, cache._lib.pi_attn_decode, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch,
                heads, _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,

@@ -1,0 +1,39 @@
+"""Arguments that the binding refuses, on the host: tensors that say they lie on GPU 0, and a library that only writes down
+what it is called with."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_binding_gpus import Spy, ints, pi  # noqa: E402, F401
+
+
+@pytest.fixture
+def spy(pi, monkeypatch):  # noqa: F811
+    s = Spy(pi.lib(), [0])
+    monkeypatch.setattr(pi, "_lib", s)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(pi, "_mark", lambda dev: None)
+    monkeypatch.setattr(pi, "_capturing", lambda *a: False)
+    return s
+
+
+def refused(pi, spy, call, what=""):  # noqa: F811
+    with pytest.raises(pi.PiError) as e:
+        call()
+    assert e.value.status == pi.PI_EINVAL and what in str(e.value)
+    assert spy.calls == []
+
+
+def test_workspace_of_a_decoding_step(pi, spy):  # noqa: F811
+    """Its bytes have to be there: elements that repeat, or lie apart, are no memory of their number's size."""
+    q = torch.zeros(3, 4, 64, dtype=torch.float16)
+    c = pi.Cache.create(1, 8, 2, 16, 64, 4, 4, device="cpu")
+    n = int(pi.lib().pi_attn_workspace_bytes(c._ref, 3, 4))
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(n), torch.zeros(2 * n, dtype=torch.uint8)[::2],
+               torch.zeros(64, n // 64, dtype=torch.uint8).t()):
+        refused(pi, spy, lambda: pi.attn_decode(c, 0, q, q.clone(), ws=ws))
+    pi.attn_decode(c, 0, q, q.clone(), ws=torch.zeros(n, dtype=torch.uint8))
+    pi.attn_decode(c, 0, q, q.clone(), ws=torch.zeros(n // 4, dtype=torch.float32))
+    assert [name for name, _, _ in spy.calls] == ["pi_attn_decode"] * 2
