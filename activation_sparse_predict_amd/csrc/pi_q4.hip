@@ -49,6 +49,16 @@ pi_status check_sizes(int32_t rows, int32_t cols, int32_t batch) {
   return rows > (1 << 22) || cols > (1 << 22) ? PI_EUNSUPPORTED : PI_OK;
 }
 
+// Whether a row of y lies over a row of x: `n` of each, of xn and yn bytes, every xs and ys bytes.
+bool over(const void* x, int64_t xs, int64_t xn, const void* y, int64_t ys, int64_t yn, int n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  if (b >= a + (n - 1) * xs + xn || a >= b + (n - 1) * ys + yn) return false;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (a + i * xs < b + j * ys + yn && b + j * ys < a + i * xs + xn) return true;
+  return false;
+}
+
 // f(constant of the dtype)
 template <class F>
 void with_dtype(int32_t dtype, F f) {
@@ -76,6 +86,9 @@ pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* 
   if (!x || !on(x, size_of(x_dtype)) || !y || !on(y, size_of(y_dtype)) || ldx < cols || ldy < rows) return PI_EINVAL;
   const Ws W = ws_of(rows, cols, batch);
   if (!ws || ws_bytes < W.total || !on(ws, kWsAlign)) return PI_EWORKSPACE;
+  // blocks read x while others write y
+  const int xb = size_of(x_dtype), yb = size_of(y_dtype);
+  if (over(x, ldx * xb, (int64_t)cols * xb, y, ldy * yb, (int64_t)rows * yb, batch)) return PI_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   uint16_t* xo = static_cast<uint16_t*>(ws);
   float* inv = reinterpret_cast<float*>(static_cast<char*>(ws) + W.inv);

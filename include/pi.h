@@ -229,6 +229,8 @@ pi_status pi_ffn_stack_static(const pi_layer* layers, int32_t n_layers, const fl
  *    with 8 <= dim <= 256 and dim % 8 == 0; scores, softmax statistics and
  *    sums are float32.
  *  - heads % kv_heads == 0; query head h reads key head h / (heads / kv_heads).
+ *  - An output lies over no input, but pi_attn_prompt's and pi_attn_decode's may
+ *    be q itself, with q's strides.
  *  - What only the device knows (lengths, slot and page numbers) is checked
  *    there: nothing outside the tensors is ever read or written for it.  An
  *    accounting call (extend, fork, release) that cannot be carried out whole
@@ -335,8 +337,9 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
  * [rows][cols] (pi_mat, 16-byte aligned nibbles, 2-byte aligned scales),
  * cols % 32 == 0, bias [rows] float32 or NULL.  x [batch][ldx] and
  * y [batch][ldy] are PI_F32, PI_F16 or PI_BF16 each, aligned to their type,
- * ldx >= cols and ldy >= rows (elements).  Products and sums carry float32's
- * precision whatever the types are.
+ * ldx >= cols and ldy >= rows (elements); no row of y lies over a row of x
+ * (PI_EINVAL).  Products and sums carry float32's precision whatever the types
+ * are.
  */
 size_t pi_matvec_workspace_bytes(int32_t rows, int32_t cols, int32_t batch);
 pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* bias, const void* x, int32_t x_dtype,
