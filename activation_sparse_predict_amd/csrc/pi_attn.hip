@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "pi_host.hpp"
 
@@ -26,6 +27,21 @@ bool scale_of(float scale, int dim, float* c) {
 
 pia::Rows rows_of(const pi_heads* h) {
   return pia::Rows{static_cast<const uint16_t*>(h->p), h->token_stride, h->head_stride};
+}
+
+// Whether rows of `dim` elements of an output lie over each other.
+bool folded(const pi_heads* h, int64_t tokens, int64_t heads, int64_t dim) {
+  int64_t s = std::abs(h->token_stride), ns = tokens, l = std::abs(h->head_stride), nl = heads;
+  if (ns > 1 && s < dim) return true;
+  if (nl > 1 && l < dim) return true;
+  if (ns == 1 || nl == 1) return false;
+  if (s > l) std::swap(s, l), std::swap(ns, nl);
+  if (l >= s * (ns - 1) + dim) return false;       // one after the other, as tensors are laid out
+  for (int64_t i = 1; i < heads; ++i) {
+    const int64_t at = i * std::abs(h->head_stride), step = std::abs(h->token_stride), t = at / step;
+    if ((t < tokens && at - t * step < dim) || (t + 1 < tokens && (t + 1) * step - at < dim)) return true;
+  }
+  return false;
 }
 
 // How a decode call is cut up.
@@ -112,6 +128,7 @@ pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v
   // a tile of each sequence may be short
   const int64_t blocks = (up_div(tokens, rows) + std::min(n, tokens)) * (heads / hg);
   if (blocks > INT32_MAX) return PI_EUNSUPPORTED;
+  if (folded(out, tokens, heads, dim)) return PI_EINVAL;
   (void)hipGetLastError();
   with_type(dtype, dim, [&](auto t, auto d) {
     using T = decltype(t);
@@ -144,6 +161,7 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
   if (!scale_of(scale, cache->dim, &c)) return PI_EINVAL;
   const Ws W = ws_of(cache, batch, heads);
   if (!ws || ws_bytes < W.total || !on(ws, kWsAlign)) return PI_EWORKSPACE;
+  if (folded(out, batch, heads, cache->dim)) return PI_EINVAL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Cut u = cut_of(cache, batch, heads);
   const int dim = cache->dim;

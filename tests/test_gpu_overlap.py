@@ -43,3 +43,14 @@ def test_decode_in_place_of_the_queries(prefix):
     ref = attn_ref.decode(q, ks, vs)
     pi.attn_decode(cache, 1, q, q, prefix=None if prefix is None else ints([prefix]))
     attn_ref.check(q, *ref)
+
+
+@pytest.mark.parametrize("tokens,heads,token,head", [(2, 3, 40, 24), (3, 2, 24, 40), (1, 4, 0, 8), (5, 1, 8, 0), (4, 3, 24, 8),
+                                                     (4, 3, 8, 32)])
+def test_outputs_between_each_others_rows(tokens, heads, token, head):
+    """Rows of 8, in any order of strides, that do not meet."""
+    q, k, v = (normal(i, tokens, n, 8, dtype=torch.float16) for i, n in ((0, heads), (1, heads), (2, heads)))
+    size = (tokens - 1) * token + (heads - 1) * head + 8
+    out = torch.zeros(size, dtype=torch.float16, device=DEV).as_strided((tokens, heads, 8), (token, head, 1))
+    pi.attn_prompt(q, k, v, out, ints([0, tokens]))
+    attn_ref.check(out, *attn_ref.prompt(q, k, v, [tokens]))
