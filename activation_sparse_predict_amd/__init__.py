@@ -14,6 +14,9 @@ Entry points (same names and meaning as the C functions):
   attn_prompt(q, k, v, out, cu)
   attn_decode(cache, layer, q, out, prefix=None, seqs=None)
   Q4Matrix(nibbles, scales, bias, batch) and matvec(mat, x, y)
+
+The last four lines' operators have no gradient and refuse tensors that want one.  Tensors and
+handles of a call have to live until its work on the stream is done.
 """
 from __future__ import annotations
 
@@ -387,11 +390,15 @@ def _need(ok: bool, what: str):
 
 
 def _gpu(what: str, first, *tensors) -> int:
-    """The GPU on which all tensors (None aside) lie: a kernel cannot follow an address of the host's."""
+    """The GPU on which all tensors (None aside) lie: a kernel cannot follow an address of the host's.  None of them may want
+    a gradient, which these operators do not have."""
     dev = first.get_device()
     for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise PiError(PI_EINVAL, what)
+        if t is not None:
+            if t.get_device() != dev:
+                raise PiError(PI_EINVAL, what)
+            if t.requires_grad and (_torch or _load_torch()).is_grad_enabled():
+                raise PiError(PI_EINVAL, what.split(":")[0] + ": a tensor wants a gradient (torch.no_grad says that none is wanted)")
     if dev < 0:
         raise PiError(PI_EINVAL, what)
     return dev
@@ -608,7 +615,7 @@ def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
           and q.dtype == k.dtype == v.dtype == out.dtype, "attn_prompt: q, k, v, out")
     _need(n > 0, "attn_prompt: cu")
     offsets, what = _ints(cu, None, "attn_prompt: cu"), "attn_prompt: strides"
-    dev = _gpu("attn_prompt: tensors of one GPU", q, k, v, out, cu)
+    dev = _gpu("attn_prompt: tensors of one GPU", cu, q, k, v, out)
     _check(_on(dev, (_lib or lib()).pi_attn_prompt, _heads(q, qs, what), _heads(k, ks, what), _heads(v, ks, what),
                _heads(out, qs, what), qs[0], qs[1], ks[1], qs[2], _dtype_of(q), offsets, n, scale,
                _stream_on(dev, stream)), "pi_attn_prompt")

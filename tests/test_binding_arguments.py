@@ -37,3 +37,28 @@ def test_workspace_of_a_decoding_step(pi, spy):  # noqa: F811
     pi.attn_decode(c, 0, q, q.clone(), ws=torch.zeros(n, dtype=torch.uint8))
     pi.attn_decode(c, 0, q, q.clone(), ws=torch.zeros(n // 4, dtype=torch.float32))
     assert [name for name, _, _ in spy.calls] == ["pi_attn_decode"] * 2
+
+
+def test_tensors_that_want_a_gradient(pi, spy):  # noqa: F811
+    """The outputs would carry none, without a word."""
+    def t(*shape, dtype=torch.float16):
+        return torch.zeros(*shape, dtype=dtype)
+    c = pi.Cache.create(1, 8, 2, 16, 64, 4, 4, device="cpu")
+    c.reserve(3, 4)
+    mat = pi.Q4Matrix(torch.zeros(64, 32, dtype=torch.uint8), t(64, 2), batch=2)
+    calls = {
+        "attn_prompt": (lambda q, k, v, o: pi.attn_prompt(q, k, v, o, ints(0, 3)), [t(3, 4, 64), t(3, 2, 64), t(3, 2, 64), t(3, 4, 64)]),
+        "attn_decode": (lambda q, o: pi.attn_decode(c, 0, q, o), [t(3, 4, 64), t(3, 4, 64)]),
+        "append": (lambda k, v: c.append(0, k, v, ints(0, 3), ints(0)), [t(3, 2, 64), t(3, 2, 64)]),
+        "matvec": (lambda x, y: pi.matvec(mat, x, y), [t(2, 64), t(2, 64)]),
+    }
+    for name, (call, args) in calls.items():
+        for a in args:
+            a.requires_grad_()
+            refused(pi, spy, lambda: call(*args), "gradient")
+            with torch.no_grad():
+                call(*args)
+            spy.calls.clear()
+            a.requires_grad_(False)
+        call(*args)
+        spy.calls.clear()
