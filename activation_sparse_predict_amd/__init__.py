@@ -94,6 +94,13 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is not built (run __graft_entry__.build())")
         L = ctypes.CDLL(LIB_PATH)
         P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        # entry points that are added leave the version as it is: a library without them is an older one
+        missing = [name for name in EXPORTED if not hasattr(L, name)]
+        got = int(L.pi_abi_version()) if "pi_abi_version" not in missing else None
+        if got != ABI_VERSION or missing:
+            raise RuntimeError(f"{LIB_PATH} has ABI version {got}, this binding expects {ABI_VERSION}"
+                               + (f" and {', '.join(missing)}" if missing else "")
+                               + " (rebuild with __graft_entry__.build())")
         L.pi_abi_version.restype = I32
         L.pi_status_str.argtypes = [ctypes.c_int]
         L.pi_status_str.restype = ctypes.c_char_p
@@ -124,10 +131,6 @@ def lib():
                 ("pi_matvec", ctypes.c_int, [P, I32, I32, P, P, I32, I64, P, I32, I64, I32, P, SZ, P])):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = res, args
-        got = int(L.pi_abi_version())
-        if got != ABI_VERSION:
-            raise RuntimeError(f"{LIB_PATH} has ABI version {got}, this binding expects {ABI_VERSION} "
-                               "(rebuild with __graft_entry__.build())")
         _lib = L
     return _lib
 
