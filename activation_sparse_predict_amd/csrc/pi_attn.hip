@@ -47,7 +47,8 @@ bool folded(const pi_heads* h, int64_t tokens, int64_t heads, int64_t dim) {
 // How a decode call is cut up.
 struct Cut {
   int tiles;      // 16-query tiles of a key head's group, over all key heads
-  int free;       // shares of the rows' keys to deal, beside one for each row; 0: one block a row and tile
+  int free;       // shares of the rows' keys to deal, beside one for each row
+  int least;      // units of a share at least, where a row has several
   int blocks;     // for each such tile
   int qtiles;     // 128-query tiles of a key head over the whole batch, for the common keys
   int shares;     // of the common keys at most
@@ -56,8 +57,12 @@ Cut cut_of(const pi_cache* c, int batch, int heads) {
   Cut u{};
   const int group = heads / c->kv_heads;
   u.tiles = c->kv_heads * (int)up_div(group, 16);
-  // two blocks for each compute unit, beside a row's first
-  u.free = (int64_t)batch * u.tiles >= pia::DC_ROWS ? 0 : (int)up_div(512, u.tiles);
+  // two blocks for each compute unit, beside a row's first.  Where the first ones fill the card, only what is longer than 8
+  // units and than twice the average is dealt.  (32 rows of 32 heads on 32, 128 wide, 500 tokens and one row of 32768:
+  // 1642 us with one share a row, 178 so, 180 with all dealt; 100 tokens each 12.9, 13.5, 16.8 us; 1500 each 146, 150, 151;
+  // 1024 rows of one key head, 300 tokens each, 17.0, 16.9, 32.)
+  u.least = (int64_t)batch * u.tiles >= pia::DC_ROWS ? 8 : 1;
+  u.free = pish::units_of(c->max_pages * c->page) > u.least ? (int)up_div(512, u.tiles) : 0;
   u.blocks = batch + u.free;
   u.qtiles = (int)up_div((int64_t)batch * group, 128);
   u.shares = (int)std::max<int64_t>(1, std::min<int64_t>(64, 512 / ((int64_t)u.qtiles * c->kv_heads)));
@@ -190,7 +195,7 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
     hipLaunchKernelGGL((pia::k_attn_decode<T, D>), dim3((unsigned)u.blocks, (unsigned)u.tiles + (prefix ? 1 : 0)),
                        dim3(pia::DC_WAVES * pia::WAVE), 0, st, pg, rows_of(q), static_cast<uint16_t*>(out->p),
                        out->token_stride, out->head_stride, seqs, prefix, batch, heads, cache->kv_heads, dim, u.free,
-                       u.shares, c, reinterpret_cast<int4*>(base), floats(W.part), floats(W.stat));
+                       u.least, u.shares, c, reinterpret_cast<int4*>(base), floats(W.part), floats(W.stat));
     if (prefix || u.free)
       hipLaunchKernelGGL((pia::k_attn_join<T, D <= 64 ? 16 : D <= 128 ? 32 : 64>), dim3((unsigned)up_div((int64_t)batch * heads, 4)),
                          dim3(256), 0, st, reinterpret_cast<const int4*>(base), floats(W.cpart), floats(W.cstat),

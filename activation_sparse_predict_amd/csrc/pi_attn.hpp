@@ -619,7 +619,7 @@ k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t*
 constexpr int DC_WAVES = 4;
 constexpr int DC_K = 32;                 // keys of a wave's step
 static_assert(DC_WAVES * DC_K == UNIT && PT_K == TILE, "pi_share.hpp");
-constexpr int DC_ROWS = 1024;            // tiles of queries from which on a row has one share
+constexpr int DC_ROWS = 1024;            // tiles of queries that fill the card with one share a row
 
 // O^T of the 16x16x32 product: a lane's A operand row l % 16 stands for VW
 // consecutive output dims (VW operands), so V is loaded with VW elements per
@@ -635,30 +635,54 @@ struct Share {
   int b, slot, len, i, n;                // n = 0: nothing to do
 };
 
-__device__ __forceinline__ Share find_share(const Pages& pg, const int32_t* seqs, int batch, int total, int idx, int free) {
+// Block b < batch takes the first share of row b; the others follow the rows, in their order.  A row of no more than
+// `least` units has one share, which needs no look at the other rows.
+__device__ __forceinline__ Share find_share(const Pages& pg, const int32_t* seqs, int batch, int total, int idx, int free,
+                                            int least) {
   const int lane = threadIdx.x & (WAVE - 1);
-  int slot = -1, len = 0;                          // of row base + lane
+  int slot = -1, len = 0;                          // of the row that `units` was last asked for
   auto units = [&](int b) {
     slot = b < batch ? slot_of(seqs, b, pg.slots) : -1;
     len = slot >= 0 ? pg.lens[slot] : 0;
     const int n = usable_len(len, pg.max_pages, pg.page);
     return units_of(n - (n >= total ? total : 0));
   };
-  // of one row at most 2^24 units: 64 rows fit 32 bits
-  int mine = units(lane);
-  int64_t all = __builtin_amdgcn_readlane(scan64(mine), WAVE - 1);
-  for (int base = WAVE; base < batch; base += WAVE) all += __builtin_amdgcn_readlane(scan64(units(base + lane)), WAVE - 1);
-  const uint32_t size = share_size(all, free);
+  int mine, own = 0, own_slot = -1, own_len = 0;
+  if (idx < batch && batch > WAVE) {
+    own = units(idx), own_slot = slot, own_len = len;
+    if (own <= least) return Share{idx, slot, len, 0, 1};
+  }
+  mine = units(lane);
+  if (idx < batch && batch <= WAVE) {
+    own = __builtin_amdgcn_readlane(mine, idx);
+    own_slot = __builtin_amdgcn_readlane(slot, idx);
+    own_len = __builtin_amdgcn_readlane(len, idx);
+    if (own <= least) return Share{idx, own_slot, own_len, 0, 1};
+  }
+  // of one row at most 2^24 units, and 64 rows a lane: the lanes' sums fit 31 bits, and 64 of their halves do
+  int sum = mine, most = mine;
+#pragma unroll 4
+  for (int base = WAVE; base < batch; base += WAVE) {
+    const int n = units(base + lane);
+    sum += n;
+    most = max(most, n);
+  }
+  const uint64_t all = (uint64_t)__builtin_amdgcn_readlane(scan64(sum & 0xffff), WAVE - 1) +
+                       ((uint64_t)__builtin_amdgcn_readlane(scan64(sum >> 16), WAVE - 1) << 16);
+  const uint32_t size = max(share_size(all, free), (uint32_t)least);
+  if (idx < batch) return Share{idx, own_slot, own_len, 0, deal(own, size)};
+  if (!__ballot(deal(most, size) > 1)) return Share{0, -1, 0, 0, 0};   // nothing to deal
+  idx -= batch;
   for (int base = 0; base < batch; base += WAVE) {
     if (batch > WAVE) mine = units(base + lane);
-    const int n = base + lane < batch ? deal(mine, size) : 0;
+    const int n = base + lane < batch ? deal(mine, size) - 1 : 0;
     const int upto = scan64(n);
     const uint64_t hit = __ballot(upto > idx);
     if (hit) {
       const int l = __ffsll((unsigned long long)hit) - 1;
-      const int count = __builtin_amdgcn_readlane(n, l);
+      const int others = __builtin_amdgcn_readlane(n, l);
       return Share{base + l, __builtin_amdgcn_readlane(slot, l), __builtin_amdgcn_readlane(len, l),
-                   idx - (__builtin_amdgcn_readlane(upto, l) - count), count};
+                   1 + idx - (__builtin_amdgcn_readlane(upto, l) - others), 1 + others};
     }
     idx -= __builtin_amdgcn_readlane(upto, WAVE - 1);
   }
@@ -672,7 +696,6 @@ __device__ __forceinline__ Share find_share(const Pages& pg, const int32_t* seqs
 // `part` and `stat` and the row's shares to `plan`, for k_attn_join.  (Joining
 // in the row's last block instead costs more: its loads have to pass the die's
 // cache.  1500 tokens: 16 us, not 13; with an agent-scope fence 52 us.)
-// `free` is 0 where every row has one share: the block's number is the row's.
 // With a prefix, blocks behind the last query tile compare the rows' tables with
 // the one that k_attn_common reads, beside the others.  (32 rows behind 4096
 // common tokens: 37.5 us, 37.4 without.)
@@ -680,7 +703,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(DC_WAVES * WAVE, D <= 128 ? 2 : 1)
 k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head,
               const int32_t* __restrict__ seqs, const int32_t* __restrict__ prefix, int batch, int heads, int kv_heads,
-              int dim, int free, int shares, float c, int4* __restrict__ plan, float* __restrict__ part,
+              int dim, int free, int least, int shares, float c, int4* __restrict__ plan, float* __restrict__ part,
               float* __restrict__ stat) {
   using V = Vec<D>;
   constexpr int NF = V::W * V::G;                  // operands of the second product
@@ -693,14 +716,8 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
   const int r = lane & 15, kg = lane >> 4;
   const int total = common_of(pg, prefix), tiles = kv_heads * rts;
   if ((int)blockIdx.y == tiles) return check_common(pg, seqs, batch, total, blockIdx.x);
-  Share me;
-  if (free) {
-    me = find_share(pg, seqs, batch, total, blockIdx.x, free);
-    if (me.n == 0) return;
-  } else {
-    const int slot = slot_of(seqs, blockIdx.x, pg.slots);
-    me = Share{(int)blockIdx.x, slot, slot >= 0 ? pg.lens[slot] : 0, 0, 1};
-  }
+  const Share me = find_share(pg, seqs, batch, total, blockIdx.x, free, least);
+  if (me.n == 0) return;
   const int b = me.b, slot = me.slot;
   const int len = usable_len(me.len, pg.max_pages, pg.page);
   if (tid == 0 && (slot < 0 || len != me.len)) atomicOr(pg.flags, slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
@@ -861,8 +878,9 @@ k_attn_decode(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, i
       if (d == 0) *reinterpret_cast<float2*>(stat + 2 * (16 * mine + qr)) = float2{mm, ll};
     }
   }
-  // the row's first share, how many there are (0: the result is written), and those of the common keys
-  if (me.i == 0 && blockIdx.y == 0 && tid == 0) plan[b] = int4{(int)blockIdx.x, whole ? 0 : me.n, common, 0};
+  // the place of the row's second share, how many there are (0: the result is written), and those of the common keys; the
+  // second share's block knows, if there is one
+  if (blockIdx.y == 0 && tid == 0 && me.i == (me.n > 1 ? 1 : 0)) plan[b] = int4{(int)blockIdx.x, whole ? 0 : me.n, common, 0};
 }
 
 // Join the shares of a query: one wave each, N lanes (of 4 dims each) for a share, 64 / N shares at once.
@@ -880,13 +898,14 @@ k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, cons
   const int4 pl = plan[b];
   if (pl.y == 0) return;
   const int tiles = kv_heads * rts, tile = h / group * rts + h % group / 16;
-  const int64_t own0 = ((int64_t)pl.x * tiles + tile) * 16 + h % group % 16, own1 = 16 * (int64_t)tiles;
   const int n = pl.y, all = n + pl.z;
+  // the i-th of the row's own shares: block b's, or of those behind the rows
+  auto own = [&](int i) { return ((int64_t)(i ? pl.x + i - 1 : b) * tiles + tile) * 16 + h % group % 16; };
   const int d = min(4 * (lane % N), dim - 4), mine = lane / N;
   // the first sums are on their way while the weights are made
   auto at = [&](int i) {
     i = min(i, all - 1);
-    return *reinterpret_cast<const f4*>((i < n ? part + (own0 + i * own1) * dim : cpart + (row * shares + i - n) * dim) + d);
+    return *reinterpret_cast<const f4*>((i < n ? part + own(i) * dim : cpart + (row * shares + i - n) * dim) + d);
   };
   f4 y[AHEAD];
 #pragma unroll
@@ -897,7 +916,7 @@ k_attn_join(const int4* __restrict__ plan, const float* __restrict__ cpart, cons
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int i = min(64 * j + lane, all - 1);
-    st[j] = *reinterpret_cast<const float2*>(i < n ? stat + 2 * (own0 + i * own1) : cstat + 2 * (row * shares + i - n));
+    st[j] = *reinterpret_cast<const float2*>(i < n ? stat + 2 * own(i) : cstat + 2 * (row * shares + i - n));
     mm = fmaxf(mm, st[j].x);
   }
 #pragma unroll

@@ -68,3 +68,21 @@ def test_shares_of_many_tiles(dim, page, dtype):
     assert cache.errors() == pi.PI_CACHE_EPAGE
     cache.table[:, place] = was
     check(place)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv_heads,rows,long", [(32, 32, 40, {7: 9000}), (16, 8, 140, {0: 1100, 70: 5000, 139: 6001}),
+                                                      (2, 1, 1100, {5: 1025, 1099: 20000}), (32, 32, 40, {})])
+def test_long_rows_among_many_short_ones(heads, kv_heads, rows, long, dtype):
+    """Where the rows fill the card, the long ones are cut up all the same: those of several shares stand anywhere."""
+    assert rows * kv_heads >= 1024
+    lens = [long.get(i, 1 + i * 37 % 200) for i in range(rows)]
+    cache = make_cache(65, dtype, kv_heads, 64, 64, lens, layers=2)
+    q = normal(4, rows, heads, 64, dtype=TYPES[dtype])
+    check_decode(cache, q)
+    again = torch.empty_like(q)
+    want = torch.empty_like(q)
+    pi.attn_decode(cache, 1, q, want)
+    for _ in range(3):
+        pi.attn_decode(cache, 1, q, again)
+        assert torch.equal(again, want)
