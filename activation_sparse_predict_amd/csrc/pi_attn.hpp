@@ -445,7 +445,7 @@ __device__ __forceinline__ void check_common(const Pages& pg, const int32_t* seq
 constexpr int SH_IDS = 256;              // places of 16 keys that are looked up at once: 64 tiles
 
 template <class T, int D>
-__global__ void __launch_bounds__(4 * WAVE, D <= 64 ? 3 : D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(4 * WAVE, D <= 64 ? 3 : 1)
 k_attn_common(Pages pg, Rows q, const int32_t* __restrict__ seqs, const int32_t* __restrict__ prefix, int batch,
               int heads, int kv_heads, int dim, int shares, int qtiles, float c, float* __restrict__ part,
               float* __restrict__ stat) {

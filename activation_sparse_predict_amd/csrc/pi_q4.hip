@@ -10,13 +10,18 @@ using namespace pih;
 
 namespace {
 
-// 12288 float32 values; with the sums of the waves (9 KB) a block keeps to 64 KB
+// The operand of a product of few columns at most: with the sums of the waves (9 KB) a block keeps to 64 KB, what a launch
+// may have without asking for more.  (In the few columns' kernel and in the others': one float32 row of 4096 x 4096 7.1 and
+// 11.6 us, 4096 x 11008 11.5 and 19.7, 9216 x 8192 23 and 23, 36864 x 12288 61 and 82; but 2 bfloat16 rows of 9216 x 8192
+// 27 and 22, 8 of 4096 x 2048 11.3 and 9.6 us.)
 constexpr size_t kOperandLds = 48 << 10;
 
 // Shares of the groups of 8 blocks in a product of many columns, 32 at most: those with which the rounds of 512 blocks
 // (two for each compute unit), at 2.5 us a group, and the shares' sums, at 1 us for each 9216 rows of 32 columns,
 // written and read, take least.  (32 bfloat16 rows, 9216 x 8192: 6, 7, 8, 9, 11 shares 25.9, 25.0, 27.9, 27.1, 29.0 us;
-// 18432 x 8192: 3, 4, 5 shares 43, 48, 44 us; 36864 x 12288: 2, 3, 4 shares 98, 91, 91 us.)
+// 18432 x 8192: 3, 4, 5 shares 43, 48, 44 us; 36864 x 12288: 2, 3, 4 shares 98, 91, 91 us.)  The two costs were taken with 32
+// columns and serve all numbers of them: with 8 to 64 columns and these and other matrices, down to 4096 x 4096 and
+// 12288 x 49152, what they choose takes at most 7 % longer than the best of 1, 2, 3, 4, 6, 8, 12, 16, 24 and 32 shares.
 int shares_of(int32_t rows, int32_t cols) {
   const int64_t groups = up_div(cols, 32 * piq::MV_G), blocks = up_div(rows, piq::MV_ROWS * piq::MV_WAVES);
   int best = 1;

@@ -9,12 +9,15 @@
 // a power of two that puts the row's largest finite value into [2^14, 2^15):
 // one column for bfloat16 rows (their significands fit), two for float32 rows,
 // the rounded value and 2^11 times what it leaves, which together are x within
-// 2^-23 relative.  Values below 2^-39 of their row's largest lose bits to
-// binary16's range; they are under 2^-24 of any sum they could show in by then.
+// 2^-23 relative.  Below 2^-14 binary16 rounds to multiples of 2^-24: with L the
+// row's largest value, float32 values lose bits from 2^-27 L down and are off by
+// at most 2^-50 L, bfloat16 values from 2^-32 L down and by at most 2^-39 L.
+// Beside the rounding of a float32 sum with L in it, that shows only where L's
+// weight is 0 or far smaller than the others.
 //
-// What bounds the products is the read of the matrix, 18 bytes for 32 weights;
-// unpacking them takes about 13 vector instructions for 288 bytes, a quarter of
-// that time.
+// The least that the products cost is the read of the matrix, 18 bytes for 32
+// weights; unpacking them takes about 13 vector instructions for 288 bytes, a
+// quarter of that time.
 #pragma once
 #include "pi.h"
 #include "pi_tile.hpp"
@@ -326,11 +329,14 @@ k_matvec_few(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, 
 // operand each wave brings MT KB, two groups ahead: loaded while one group is
 // computed, written to LDS while the next one is.  part: [share][column][row].
 //
-// What bounds it are its vector instructions: 13 to unpack a lane's 8 weights
-// and 4 to scale each column tile's product.  9216 x 8192 with 32 bfloat16 rows:
-// 25 us a call (in 8 shares 28 us, and with three groups ahead 31 us then).
-// 36864 x 12288: 91 us (115 us with 16 rows a block, whose operand came from the
-// second-level cache for each).
+// What bounds it is the wait for its loads: with 9216 x 8192 and 32 bfloat16 rows
+// vector instructions are issued in 30 % of the cycles and matrix instructions
+// run in 8 %, while waves wait for 41 % of their time.  Loads come in order, so
+// the wait for the next group's operand, which was asked for after the weights of
+// the one behind it, is a wait for those too: of two groups of weights one is on
+// its way.  25 us a call (in 8 shares 28 us, and with three groups ahead 31 us
+// then).  36864 x 12288: 91 us (115 us with 16 rows a block, whose operand came
+// from the second-level cache for each).
 template <int MT, bool TINY>
 __global__ void __launch_bounds__(MV_WAVES * WAVE, 2)
 k_matvec(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, int rows, int cols,

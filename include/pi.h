@@ -339,7 +339,9 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
  * y [batch][ldy] are PI_F32, PI_F16 or PI_BF16 each, aligned to their type,
  * ldx >= cols and ldy >= rows (elements); no row of y lies over a row of x
  * (PI_EINVAL).  Products and sums carry float32's precision whatever the types
- * are.
+ * are; beside it a value of x may be off by 2^-50 (PI_F32) or 2^-39 (PI_BF16) of
+ * the largest finite one of its row, which shows where that one's weight is 0 or
+ * far smaller than the others.
  */
 size_t pi_matvec_workspace_bytes(int32_t rows, int32_t cols, int32_t batch);
 pi_status pi_matvec(const pi_mat* mat, int32_t rows, int32_t cols, const float* bias, const void* x, int32_t x_dtype,
