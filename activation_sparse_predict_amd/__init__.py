@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -70,6 +71,8 @@ class PiCache(ctypes.Structure):
                 ("page", ctypes.c_int32), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("slots", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
+
+_HEADS = struct.Struct("@Pqq")                         # PiHeads
 
 # bits of a cache's error word
 PI_CACHE_ESLOT, PI_CACHE_EPAGE, PI_CACHE_EFULL, PI_CACHE_ELENGTH, PI_CACHE_EPREFIX = 1, 2, 4, 8, 16
@@ -418,13 +421,14 @@ def _ints(t, n: Optional[int], what: str) -> Optional[int]:
     return t.data_ptr()
 
 
-def _heads(t, shape, what: str):
-    """Reference to the pi_heads of a [tokens][heads][dim] tensor with strides; the last dimension contiguous."""
+def _heads(t, shape, what: str) -> bytes:
+    """The pi_heads of a [tokens][heads][dim] tensor with strides, the last dimension contiguous, as the bytes of the structure
+    (which take a third of a PiHeads object's time)."""
     token, head, one = t.stride()
     if one != 1 and shape[2] != 1:
         raise PiError(PI_EINVAL, what)
     # the stride of a dimension of one element says nothing
-    return ctypes.byref(PiHeads(t.data_ptr() or None, token if shape[0] > 1 else 0, head if shape[1] > 1 else 0))
+    return _HEADS.pack(t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
 
 
 def _stream_of(dev: int, handle: int):

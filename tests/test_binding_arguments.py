@@ -62,3 +62,14 @@ def test_tensors_that_want_a_gradient(pi, spy):  # noqa: F811
             a.requires_grad_(False)
         call(*args)
         spy.calls.clear()
+
+
+def test_tensors_of_heads_are_handed_over_as_their_structure(pi):  # noqa: F811
+    import ctypes
+    t = torch.zeros(5, 3, 64, dtype=torch.float16)
+    for x in (t, t[:, 1:], t.transpose(0, 1), t[:1], t[:, :1], t[:0]):
+        raw = pi._heads(x, x.shape, "")
+        assert len(raw) == ctypes.sizeof(pi.PiHeads)
+        got = pi.PiHeads.from_buffer_copy(raw)
+        want = (x.data_ptr() or None, x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
+        assert (got.p, got.token_stride, got.head_stride) == want
