@@ -659,19 +659,25 @@ __device__ __forceinline__ Share find_share(const Pages& pg, const int32_t* seqs
     own_len = __builtin_amdgcn_readlane(len, idx);
     if (own <= least) return Share{idx, own_slot, own_len, 0, 1};
   }
-  // of one row at most 2^24 units, and 64 rows a lane: the lanes' sums fit 31 bits, and 64 of their halves do
-  int sum = mine, most = mine;
+  // of one row at most 2^24 units: the sum of 64 rows fits 31 bits
+  uint64_t all;
+  int most = mine;
+  if (batch <= WAVE) {
+    all = __builtin_amdgcn_readlane(scan64(mine), WAVE - 1);
+  } else {                                         // 64 rows a lane: so do the lanes' sums, and 64 of their halves
+    int sum = mine;
 #pragma unroll 4
-  for (int base = WAVE; base < batch; base += WAVE) {
-    const int n = units(base + lane);
-    sum += n;
-    most = max(most, n);
+    for (int base = WAVE; base < batch; base += WAVE) {
+      const int n = units(base + lane);
+      sum += n;
+      most = max(most, n);
+    }
+    all = (uint64_t)__builtin_amdgcn_readlane(scan64(sum & 0xffff), WAVE - 1) +
+          ((uint64_t)__builtin_amdgcn_readlane(scan64(sum >> 16), WAVE - 1) << 16);
   }
-  const uint64_t all = (uint64_t)__builtin_amdgcn_readlane(scan64(sum & 0xffff), WAVE - 1) +
-                       ((uint64_t)__builtin_amdgcn_readlane(scan64(sum >> 16), WAVE - 1) << 16);
   const uint32_t size = max(share_size(all, free), (uint32_t)least);
   if (idx < batch) return Share{idx, own_slot, own_len, 0, deal(own, size)};
-  if (!__ballot(deal(most, size) > 1)) return Share{0, -1, 0, 0, 0};   // nothing to deal
+  if (batch > WAVE && !__ballot(deal(most, size) > 1)) return Share{0, -1, 0, 0, 0};   // nothing to deal
   idx -= batch;
   for (int base = 0; base < batch; base += WAVE) {
     if (batch > WAVE) mine = units(base + lane);
