@@ -167,7 +167,7 @@ struct Plan {
 // children[i] becomes a copy of parents[i]: it shares the whole pages and gets a page of its own for a
 // last page that is not full, whose copy the plan asks for.  Parents are read as they were before the call.
 // The pages of all children are dealt to all threads, several a thread at once: what takes time here is one
-// read after another.  (24 children of 3001 tokens: 14.6 us with a wave a child and an addition a page and child, 11.3 us so.)
+// read after another.  (24 children of 3001 tokens: 14.6 us with a wave a child and an addition a page and child, 11.6 us so.)
 __global__ void __launch_bounds__(PL_T)
 k_cache_fork(Meta m, const int32_t* __restrict__ parents, const int32_t* __restrict__ children, int n, Plan plan) {
   __shared__ int kid[MAX_N], dad[MAX_N], len_of[MAX_N], most;
