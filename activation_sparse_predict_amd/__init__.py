@@ -189,6 +189,11 @@ def _stream_on(dev: Optional[int], stream):
     return _stream(stream)
 
 
+def _stream_of(dev: int, handle: int):
+    import torch
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
 def _on(dev: Optional[int], call, *args) -> int:
     """A call of the library with GPU `dev` current (None: as it is).  A kernel goes to the current GPU where its stream's
     handle is 0, which every GPU's default stream has."""
@@ -297,10 +302,20 @@ def alloc_workspace(layers, batch: int = 1, device=None):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _call_workspace(layers, batch: int, dev: Optional[int], stream):
+    """A workspace of one call.  It is given back when the call returns, before its work is done, so it is memory of the call's
+    own stream: the next to get it there comes after that work."""
+    if dev is None or stream is None:
+        return alloc_workspace(layers, batch)
+    import torch
+    with torch.cuda.stream(_stream_of(dev, _stream_on(dev, stream))):
+        return alloc_workspace(layers, batch)
+
+
 def predict(layer: DeviceLayer, x, idx, count, scores=None, mask=None, ws=None, batch: int = 1,
             stream=None):
     dev = _gpu_of(x)
-    ws = alloc_workspace(layer, batch) if ws is None else ws
+    ws = _call_workspace(layer, batch, dev, stream) if ws is None else ws
     st = _on(dev, lib().pi_predict, ctypes.byref(layer.struct), _p(x), batch, _p(scores), _p(mask), _p(idx),
              _p(count), _p(ws), ws.numel(), _stream_on(dev, stream))
     _check(st, "pi_predict")
@@ -309,7 +324,7 @@ def predict(layer: DeviceLayer, x, idx, count, scores=None, mask=None, ws=None, 
 def sparse_ffn(layer: DeviceLayer, x, idx, count, y, mask=None, ws=None, batch: int = 1,
                stream=None):
     dev = _gpu_of(x)
-    ws = alloc_workspace(layer, batch) if ws is None else ws
+    ws = _call_workspace(layer, batch, dev, stream) if ws is None else ws
     st = _on(dev, lib().pi_sparse_ffn, ctypes.byref(layer.struct), _p(x), batch, _p(idx), _p(count),
              _p(mask), _p(y), _p(ws), ws.numel(), _stream_on(dev, stream))
     _check(st, "pi_sparse_ffn")
@@ -353,6 +368,8 @@ class Stack:
 
 
 def ffn_stack(layers, x, out, counts=None, trace=None, ws=None, batch: int = 1, stream=None, nz_counts=None):
+    layers = list(layers)
+    ws = _call_workspace(layers, batch, _gpu_of(x), stream) if ws is None else ws
     Stack(layers, batch, ws)(x, out, counts, trace, stream, nz_counts)
 
 
@@ -429,11 +446,6 @@ def _heads(t, shape, what: str) -> bytes:
         raise PiError(PI_EINVAL, what)
     # the stride of a dimension of one element says nothing
     return _HEADS.pack(t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
-
-
-def _stream_of(dev: int, handle: int):
-    import torch
-    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
 
 
 def _capturing(dev: int, handle: Optional[int] = None) -> bool:

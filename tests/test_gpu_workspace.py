@@ -145,3 +145,24 @@ def test_calls_captured_on_a_stream_of_their_own():
         graph.replay()
         side.synchronize()
         assert torch.equal(out, want), i
+
+
+@pytest.mark.parametrize("batch", [1, 8])
+def test_ffn_calls_without_a_workspace_on_another_stream(batch):
+    """The memory that such a call took and gave back is not handed to the current stream while the call's work runs."""
+    import workload
+    layer = pi.DeviceLayer.upload(workload.make_layer(workload.CONFIGS[1].with_(d=512, ffn=1100, rank=128, n_layers=1), 0))
+    x, side = torch.randn(batch, 512, device=DEV), torch.cuda.Stream()
+    want, y = torch.empty_like(x), torch.zeros_like(x)
+    pi.ffn_stack([layer], x, want, batch=batch)
+    n = pi.workspace_bytes([layer], batch)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        y.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(5_000_000)
+        pi.ffn_stack([layer], x, y, batch=batch, stream=side)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and all((j == 255).all() for j in junk)
