@@ -293,18 +293,19 @@ def workspace_bytes(layers, batch: int = 1) -> int:
 def alloc_workspace(layers, batch: int = 1, device=None):
     """A workspace on `device`: unless it is given, where the first layer lies."""
     import torch
+    layers = [layers] if isinstance(layers, DeviceLayer) else list(layers)
     n = workspace_bytes(layers, batch)
     if n == 0:
         raise PiError(PI_EINVAL, "workspace_bytes")
     if device is None:
-        gpu = _gpu_of((layers if isinstance(layers, DeviceLayer) else layers[0]).A)
+        gpu = _gpu_of(layers[0].A)
         device = "cuda" if gpu is None else torch.device("cuda", gpu)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _call_workspace(layers, batch: int, dev: Optional[int], stream):
-    """A workspace of one call.  It is given back when the call returns, before its work is done, so it is memory of the call's
-    own stream: the next to get it there comes after that work."""
+    """A workspace of one call.  It is given back when the call returns, before its work is done, so it is memory of the
+    call's own stream: the next to get it there comes after that work."""
     if dev is None or stream is None:
         return alloc_workspace(layers, batch)
     import torch
@@ -421,7 +422,8 @@ def _gpu(what: str, first, *tensors) -> int:
             if t.get_device() != dev:
                 raise PiError(PI_EINVAL, what)
             if t.requires_grad and (_torch or _load_torch()).is_grad_enabled():
-                raise PiError(PI_EINVAL, what.split(":")[0] + ": a tensor wants a gradient (torch.no_grad says that none is wanted)")
+                raise PiError(PI_EINVAL, what.split(":")[0]
+                              + ": a tensor wants a gradient (torch.no_grad says that none is wanted)")
     if dev < 0:
         raise PiError(PI_EINVAL, what)
     return dev
@@ -439,8 +441,8 @@ def _ints(t, n: Optional[int], what: str) -> Optional[int]:
 
 
 def _heads(t, shape, what: str) -> bytes:
-    """The pi_heads of a [tokens][heads][dim] tensor with strides, the last dimension contiguous, as the bytes of the structure
-    (which take a third of a PiHeads object's time)."""
+    """The pi_heads of a [tokens][heads][dim] tensor with strides, the last dimension contiguous, as the bytes of the
+    structure (which take a third of a PiHeads object's time)."""
     token, head, one = t.stride()
     if one != 1 and shape[2] != 1:
         raise PiError(PI_EINVAL, what)
@@ -594,8 +596,9 @@ class Cache:
 
     def reserve(self, batch: int, heads: int):
         """Memory for attn_decode of up to `batch` rows of `heads` heads, so that no call of these has to take any."""
-        n = max(self._attn_needs(b, heads) for b in range(1, batch + 1)) if batch > 0 else 0
-        if n == 0 or self._attn_ws is None or n > self._attn_ws.bytes:
+        _need(batch > 0, "reserve: batch")
+        n = max(self._attn_needs(b, heads) for b in range(1, batch + 1))
+        if self._attn_ws is None or n > self._attn_ws.bytes:
             self._attn_grow(n, None)
 
     def attn_workspace(self, batch: int, heads: int):
@@ -610,11 +613,12 @@ class Cache:
         return self._attn_ws
 
     def _attn_needs(self, batch: int, heads: int) -> int:
-        n = self._attn_need[batch, heads] = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
+        n = int(lib().pi_attn_workspace_bytes(self._ref, batch, heads))
+        _need(n > 0, "attn_decode: batch, heads")
+        self._attn_need[batch, heads] = n
         return n
 
     def _attn_grow(self, n: int, handle: Optional[int]):
-        _need(n > 0, "attn_decode: batch, heads")
         # memory taken while a graph is captured belongs to that graph
         _need(not (_capturing(self._ws.dev) or handle is not None and _capturing(self._ws.dev, handle)),
               "attn_decode: a call inside a capture needs more workspace")

@@ -73,3 +73,15 @@ def test_tensors_of_heads_are_handed_over_as_their_structure(pi):  # noqa: F811
         got = pi.PiHeads.from_buffer_copy(raw)
         want = (x.data_ptr() or None, x.stride(0) if x.shape[0] > 1 else 0, x.stride(1) if x.shape[1] > 1 else 0)
         assert (got.p, got.token_stride, got.head_stride) == want
+
+
+def test_sizes_of_a_workspace_that_cannot_be(pi, spy):  # noqa: F811
+    c = pi.Cache.create(1, 8, 2, 16, 64, 4, 4, device="cpu")
+    for _ in range(2):                                 # without a buffer, and with one
+        for batch, heads in ((0, 4), (-1, 4), (2, 0), (2, 5), (5000, 4)):
+            with pytest.raises(pi.PiError):
+                c.reserve(batch, heads)
+            with pytest.raises(pi.PiError):
+                c.attn_workspace(batch, heads)
+        c.reserve(3, 4)
+        assert c.attn_workspace(2, 4) is c.attn_workspace(3, 4)

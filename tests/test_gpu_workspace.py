@@ -166,3 +166,11 @@ def test_ffn_calls_without_a_workspace_on_another_stream(batch):
         junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for _ in range(3)]
         torch.cuda.synchronize()
         assert torch.equal(y, want) and all((j == 255).all() for j in junk)
+
+
+def test_workspace_of_layers_given_one_by_one():
+    import workload
+    cfg = workload.CONFIGS[1].with_(d=512, ffn=1100, rank=128, n_layers=2)
+    layers = [pi.DeviceLayer.upload(workload.make_layer(cfg, i)) for i in range(2)]
+    ws = pi.alloc_workspace((layer for layer in layers), 4)
+    assert ws.numel() == pi.workspace_bytes(layers, 4) and ws.device == layers[0].A.device
