@@ -282,7 +282,8 @@ pi_status pi_cache_extend(const pi_cache* cache, const int32_t* seqs, const int3
 
 /* The keys and values of one layer of tokens that a slot has room for: rows
  * cu[i] .. cu[i + 1] - 1 of k and v become the LAST tokens of slot seqs[i].
- * cu: [n + 1] ascending; rows outside cu[0] .. cu[n] - 1 are ignored. */
+ * cu: [n + 1] ascending; rows outside cu[0] .. cu[n] - 1 are ignored.  No slot
+ * comes twice; a page that slots share is written for all of them. */
 pi_status pi_cache_append(const pi_cache* cache, int32_t layer, const pi_heads* k, const pi_heads* v, int32_t tokens,
                           const int32_t* cu, const int32_t* seqs, int32_t n, void* stream);
 
