@@ -14,8 +14,10 @@ Entry points (same names and meaning as the C functions):
   attn_prompt(q, k, v, out, cu)
   attn_decode(cache, layer, q, out, prefix=None, seqs=None)
   Q4Matrix(nibbles, scales, bias, batch) and matvec(mat, x, y)
+  Rope(rotary, base, layout, scaling, ...) with rope_heads(rope, pos, q, q_out, k, k_out) and Cache.append_rope
+  attn_chunk(cache, layer, q, out, cu, seqs=None, cap=0, slopes=None, window=0)
 
-The last four lines' operators have no gradient and refuse tensors that want one.  Tensors and
+The operators from Cache on have no gradient and refuse tensors that want one.  Tensors and
 handles of a call have to live until its work on the stream is done.
 """
 from __future__ import annotations
@@ -72,7 +74,20 @@ class PiCache(ctypes.Structure):
                 ("slots", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
+class PiRope(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_void_p), ("rotary", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+class PiRopeScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("trained", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("rule", ctypes.c_int32)]
+
+
 _HEADS = struct.Struct("@Pqq")                         # PiHeads
+
+_LAYOUT = {"half": 0, "pairs": 1}
+_RULE = {None: 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 # bits of a cache's error word
 PI_CACHE_ESLOT, PI_CACHE_EPAGE, PI_CACHE_EFULL, PI_CACHE_ELENGTH, PI_CACHE_EPREFIX = 1, 2, 4, 8, 16
@@ -130,6 +145,12 @@ def lib():
                 ("pi_attn_prompt", ctypes.c_int, [P, P, P, P, I32, I32, I32, I32, I32, P, I32, F, P]),
                 ("pi_attn_workspace_bytes", SZ, [P, I32, I32]),
                 ("pi_attn_decode", ctypes.c_int, [P, I32, P, P, I32, I32, P, P, F, P, SZ, P]),
+                ("pi_rope_freqs", ctypes.c_int, [P, I32, P, P]),
+                ("pi_rope_steps", ctypes.c_int, [P, I32, P]),
+                ("pi_rope_heads", ctypes.c_int, [P, P, P, P, I32, P, P, P, I32, P, F, I32, I32, I32, P]),
+                ("pi_cache_append_rope", ctypes.c_int, [P, I32, P, P, P, I32, P, P, P, P, F, I32, P, P, I32, P]),
+                ("pi_attn_chunk_workspace_bytes", SZ, [P, I32, I32, I32]),
+                ("pi_attn_chunk", ctypes.c_int, [P, I32, P, P, I32, I32, P, P, I32, F, F, P, I32, P, SZ, P]),
                 ("pi_matvec_workspace_bytes", SZ, [I32, I32, I32]),
                 ("pi_matvec", ctypes.c_int, [P, I32, I32, P, P, I32, I64, P, I32, I64, I32, P, SZ, P])):
             fn = getattr(L, name)
@@ -440,6 +461,15 @@ def _ints(t, n: Optional[int], what: str) -> Optional[int]:
     return t.data_ptr()
 
 
+def _floats(t, n: int, what: str) -> Optional[int]:
+    """Address of a contiguous float32 tensor of n elements, or None for None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != (n,) or not t.is_contiguous() or (_KINDS or _torch_names()).get(t.dtype) != PI_F32:
+        raise PiError(PI_EINVAL, what)
+    return t.data_ptr()
+
+
 def _heads(t, shape, what: str) -> bytes:
     """The pi_heads of a [tokens][heads][dim] tensor with strides, the last dimension contiguous, as the bytes of the
     structure (which take a third of a PiHeads object's time)."""
@@ -501,9 +531,9 @@ class Cache:
 
     k_pool, v_pool: [layers][pages][kv_heads][page][dim], float16 or bfloat16.  meta: the page
     tables, one int32 tensor; .table, .lens, .ref, .free and .words are views of its parts.
-    The workspace of attn_decode is one buffer that grows when a call needs more, never inside a
-    capture: a call that is captured has to have run once before with the same sizes, or .reserve
-    has been called.  Calls on one cache belong on one stream."""
+    The workspace of attn_decode and attn_chunk is one buffer that grows when a call needs more, never
+    inside a capture: a call that is captured has to have run once before with the same sizes, or
+    .reserve or .reserve_chunk has been called.  Calls on one cache belong on one stream."""
 
     def __init__(self, k_pool, v_pool, meta, slots: int, max_pages: int):
         import torch
@@ -568,6 +598,27 @@ class Cache:
                    _heads(v, shape, "append: v"), shape[0], _ints(cu, n + 1, "append: cu"), _ints(seqs, n, "append: seqs"), n,
                    _stream_on(dev, stream)), "pi_cache_append")
 
+    def append_rope(self, layer: int, rope, q, q_out, k, v, cu, seqs, q_norm=None, k_norm=None, eps: float = 1e-6, stream=None):
+        """append of keys that are normed and turned as rope_heads does, at the positions their tokens have in their slots;
+        q [tokens][heads][dim], likewise, goes to q_out (both may be None).  rope None: norms alone."""
+        shape = k.shape
+        _need(len(shape) == 3 and shape == v.shape and shape[1] == self.kv_heads and shape[2] == self.dim
+              and k.dtype == v.dtype == self.dtype, "append_rope: k, v")
+        heads, n, what = 0, seqs.numel(), "append_rope: strides"
+        if q is not None or q_out is not None:
+            _need(q is not None and q_out is not None, "append_rope: q, q_out")
+            qs = q.shape
+            _need(len(qs) == 3 and qs == q_out.shape and qs[0] == shape[0] and qs[1] > 0 and qs[2] == self.dim
+                  and q.dtype == q_out.dtype == self.dtype, "append_rope: q, q_out")
+            heads = qs[1]
+        dev = _gpu("append_rope: tensors of one GPU", self.meta, k, v, cu, seqs, q, q_out, q_norm, k_norm,
+                   None if rope is None else rope.steps)
+        _check(_on(dev, self._lib.pi_cache_append_rope, self._ref, layer, None if rope is None else rope._ref,
+                   _heads(q, qs, what) if heads else None, _heads(q_out, qs, what) if heads else None, heads,
+                   _floats(q_norm, self.dim, "append_rope: q_norm"), _heads(k, shape, what), _heads(v, shape, what),
+                   _floats(k_norm, self.dim, "append_rope: k_norm"), eps, shape[0], _ints(cu, n + 1, "append_rope: cu"),
+                   _ints(seqs, n, "append_rope: seqs"), n, _stream_on(dev, stream)), "pi_cache_append_rope")
+
     def fork(self, parents, children, stream=None):
         """The empty slot children[i] becomes a copy of slot parents[i]."""
         n = parents.numel()
@@ -600,6 +651,31 @@ class Cache:
         n = max(self._attn_needs(b, heads) for b in range(1, batch + 1))
         if self._attn_ws is None or n > self._attn_ws.bytes:
             self._attn_grow(n, None)
+
+    def reserve_chunk(self, tokens: int, heads: int, n: int):
+        """Memory for attn_chunk of up to `tokens` rows of `heads` heads in up to n chunks."""
+        _need(tokens > 0, "reserve_chunk: tokens")
+        need = self._chunk_needs(tokens, heads, n)         # fewer rows or chunks need no more
+        if self._attn_ws is None or need > self._attn_ws.bytes:
+            self._attn_grow(need, None)
+
+    def chunk_workspace(self, tokens: int, heads: int, n: int):
+        """The workspace of attn_chunk for these sizes: the same buffer as attn_decode's."""
+        return self._chunk_scratch(tokens, heads, n, None).mem
+
+    def _chunk_scratch(self, tokens: int, heads: int, n: int, handle: Optional[int]) -> _Scratch:
+        need = self._attn_need.get((tokens, heads, n)) or self._chunk_needs(tokens, heads, n)
+        if self._attn_ws is None or need > self._attn_ws.bytes:
+            self._attn_grow(need, handle)
+        return self._attn_ws
+
+    def _chunk_needs(self, tokens: int, heads: int, n: int) -> int:
+        need = int(lib().pi_attn_chunk_workspace_bytes(self._ref, tokens, heads, n))
+        _need(need > 0, "attn_chunk: tokens, heads, n")
+        if len(self._attn_need) >= 4096:                   # of calls with ever other numbers of tokens
+            self._attn_need.clear()
+        self._attn_need[tokens, heads, n] = need
+        return need
 
     def attn_workspace(self, batch: int, heads: int):
         """The workspace of attn_decode for these sizes: a buffer of at least as many bytes, the same for all sizes."""
@@ -666,6 +742,92 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
     _check(_on(dev, cache._lib.pi_attn_decode, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch,
                heads, _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,
                memory, size, on), "pi_attn_decode")
+
+
+class Rope:
+    """Rotary positions (pi_rope in include/pi.h): the frequencies of a model on one GPU.
+
+    The first `rotary` dimensions of a head turn, in pairs (i, i + rotary / 2) with layout "half" or (2 i, 2 i + 1) with
+    "pairs".  Frequencies follow from `base` by the rule `scaling` (None, "linear", "base", "bands" or "ramp"; pi_rope_rule)
+    with factor, trained, low and high, or are given: freqs, rotary / 2 numbers in radians a token.  magnitude multiplies the
+    turned dimensions (None: the rule's)."""
+
+    def __init__(self, rotary: int, base: float = 10000.0, layout: str = "half", scaling: Optional[str] = None,
+                 factor: float = 1.0, trained: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: Optional[float] = None,
+                 freqs=None, device="cuda"):
+        import math
+
+        import torch
+        _need(layout in _LAYOUT, "Rope: layout")
+        _need(scaling in _RULE, "Rope: scaling")
+        rotary = int(rotary)
+        _need(2 <= rotary <= 256 and rotary % 2 == 0, "Rope: rotary")
+        host, own = (ctypes.c_double * (rotary // 2))(), ctypes.c_float(1.0)
+        if freqs is None:
+            rule = PiRopeScaling(base, factor, trained, low, high, _RULE[scaling])
+            _check(lib().pi_rope_freqs(ctypes.byref(rule), rotary, host, ctypes.byref(own)), "pi_rope_freqs")
+        else:
+            values = [float(f) for f in freqs]
+            _need(len(values) == rotary // 2 and scaling is None, "Rope: freqs")
+            host[:] = values
+        magnitude = own.value if magnitude is None else float(magnitude)
+        _need(math.isfinite(magnitude) and magnitude > 0, "Rope: magnitude")
+        steps = (ctypes.c_int64 * (rotary // 2))()
+        _check(lib().pi_rope_steps(host, rotary // 2, steps), "pi_rope_steps")
+        self.rotary, self.layout, self.magnitude, self.freqs = rotary, layout, magnitude, list(host)
+        self.steps = torch.tensor(list(steps), dtype=torch.int64).to(device)
+        self.struct = PiRope(_p(self.steps), rotary, _LAYOUT[layout], magnitude)
+        self._ref = ctypes.byref(self.struct)
+
+
+def rope_heads(rope: Optional[Rope], pos, q, q_out, k=None, k_out=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+               stream=None):
+    """Queries q [tokens][heads][dim] and, unless they are None, keys k [tokens][kv_heads][dim] to q_out and k_out: normed over
+    each head's dimensions where q_norm or k_norm [dim] (float32) is given, then turned at positions pos [tokens] (int32).
+
+    rope None: norms alone, pos may be None.  q_out and k_out may be q and k themselves."""
+    shape, what = q.shape, "rope_heads: strides"
+    _need(len(shape) == 3 and shape == q_out.shape and q.dtype == q_out.dtype, "rope_heads: q, q_out")
+    heads = 0
+    if k is not None or k_out is not None:
+        _need(k is not None and k_out is not None, "rope_heads: k, k_out")
+        ks = k.shape
+        _need(len(ks) == 3 and ks == k_out.shape and ks[0] == shape[0] and ks[1] > 0 and ks[2] == shape[2]
+              and k.dtype == k_out.dtype == q.dtype, "rope_heads: k, k_out")
+        heads = ks[1]
+    _need(rope is None or pos is not None, "rope_heads: pos")
+    dev = _gpu("rope_heads: tensors of one GPU", q, q_out, k, k_out, pos, q_norm, k_norm, None if rope is None else rope.steps)
+    _check(_on(dev, (_lib or lib()).pi_rope_heads, None if rope is None else rope._ref, _ints(pos, shape[0], "rope_heads: pos"),
+               _heads(q, shape, what), _heads(q_out, shape, what), shape[1], _floats(q_norm, shape[2], "rope_heads: q_norm"),
+               _heads(k, ks, what) if heads else None, _heads(k_out, ks, what) if heads else None, heads,
+               _floats(k_norm, shape[2], "rope_heads: k_norm"), eps, shape[0], shape[2], _dtype_of(q),
+               _stream_on(dev, stream)), "pi_rope_heads")
+
+
+def attn_chunk(cache: Cache, layer: int, q, out, cu, seqs=None, scale: float = 0.0, cap: float = 0.0, slopes=None,
+               window: int = 0, ws=None, stream=None):
+    """Attention of new tokens over the cache: rows cu[i] .. cu[i + 1] - 1 of q and out [tokens][heads][dim] are the last tokens
+    of slot seqs[i] (None: slot i) and see, each, what the slot holds up to itself.
+
+    window: no more than this many tokens back, itself among them (0: all).  cap: scores become cap tanh(score / cap).
+    slopes [heads] (float32): slopes[h] (j - p) is added to the score of key j and row p.  ws: as Cache.chunk_workspace."""
+    shape, n = q.shape, cu.numel() - 1
+    _need(len(shape) == 3 and shape == out.shape and shape[2] == cache.dim and q.dtype == out.dtype == cache.dtype,
+          "attn_chunk: q, out")
+    _need(n > 0, "attn_chunk: cu")
+    dev = _gpu("attn_chunk: tensors of one GPU", cache.meta, q, out, cu, seqs, slopes, ws)
+    tokens, heads, _ = shape
+    on = _stream_on(dev, stream)
+    if ws is None:
+        scratch = cache._chunk_scratch(tokens, heads, n, on)
+        memory, size = scratch.on(on), scratch.bytes
+    else:
+        _need(ws.is_contiguous(), "attn_chunk: ws")    # any other's elements lie elsewhere than one after the other
+        memory, size = ws.data_ptr(), ws.numel() * ws.element_size()
+    what = "attn_chunk: strides"
+    _check(_on(dev, cache._lib.pi_attn_chunk, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), tokens, heads,
+               _ints(cu, n + 1, "attn_chunk: cu"), _ints(seqs, n, "attn_chunk: seqs"), n, scale, cap,
+               _floats(slopes, heads, "attn_chunk: slopes"), window, memory, size, on), "pi_attn_chunk")
 
 
 class Q4Matrix:
@@ -822,4 +984,5 @@ class HipGraph:
 EXPORTED = ("pi_workspace_bytes", "pi_predict", "pi_sparse_ffn", "pi_ffn_stack", "pi_ffn_stack_static",
             "pi_cache_meta_words", "pi_cache_workspace_bytes", "pi_cache_extend", "pi_cache_append", "pi_cache_fork",
             "pi_cache_release", "pi_cache_compact", "pi_attn_prompt", "pi_attn_workspace_bytes", "pi_attn_decode",
-            "pi_matvec_workspace_bytes", "pi_matvec", "pi_status_str", "pi_abi_version", "pi_last_hip_error")
+            "pi_rope_freqs", "pi_rope_steps", "pi_rope_heads", "pi_cache_append_rope", "pi_attn_chunk_workspace_bytes",
+            "pi_attn_chunk", "pi_matvec_workspace_bytes", "pi_matvec", "pi_status_str", "pi_abi_version", "pi_last_hip_error")

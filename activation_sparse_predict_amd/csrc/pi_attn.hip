@@ -2,47 +2,12 @@
 #include "pi_attn.hpp"
 
 #include <algorithm>
-#include <cmath>
-#include <cstdlib>
 
-#include "pi_host.hpp"
+#include "pi_attn_host.hpp"
 
 using namespace pih;
 
 namespace {
-
-pi_status check_shape(int32_t heads, int32_t kv_heads, int32_t dim, int32_t dtype) {
-  if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || dim < 8 || dim % 8 != 0) return PI_EINVAL;
-  if (dtype != PI_F16 && dtype != PI_BF16) return dtype == PI_F32 ? PI_EUNSUPPORTED : PI_EINVAL;
-  if (dim > 256 || heads > 4096) return PI_EUNSUPPORTED;
-  return PI_OK;
-}
-
-// 2^x instead of e^x: c = scale log2(e); false if the scale is not finite and positive
-bool scale_of(float scale, int dim, float* c) {
-  const double s = scale == 0.f ? 1.0 / std::sqrt((double)dim) : (double)scale;
-  *c = (float)(s * 1.4426950408889634);
-  return std::isfinite(*c) && *c > 0.f;
-}
-
-pia::Rows rows_of(const pi_heads* h) {
-  return pia::Rows{static_cast<const uint16_t*>(h->p), h->token_stride, h->head_stride};
-}
-
-// Whether rows of `dim` elements of an output lie over each other.
-bool folded(const pi_heads* h, int64_t tokens, int64_t heads, int64_t dim) {
-  int64_t s = std::abs(h->token_stride), ns = tokens, l = std::abs(h->head_stride), nl = heads;
-  if (ns > 1 && s < dim) return true;
-  if (nl > 1 && l < dim) return true;
-  if (ns == 1 || nl == 1) return false;
-  if (s > l) std::swap(s, l), std::swap(ns, nl);
-  if (l >= s * (ns - 1) + dim) return false;       // one after the other, as tensors are laid out
-  for (int64_t i = 1; i < heads; ++i) {
-    const int64_t at = i * std::abs(h->head_stride), step = std::abs(h->token_stride), t = at / step;
-    if ((t < tokens && at - t * step < dim) || (t + 1 < tokens && (t + 1) * step - at < dim)) return true;
-  }
-  return false;
-}
 
 // How a decode call is cut up.
 struct Cut {
@@ -93,19 +58,6 @@ pi_status check_batch(const pi_cache* c, int32_t batch, int32_t heads) {
   if (batch < 1) return PI_EINVAL;
   if ((s = check_shape(heads, c->kv_heads, c->dim, c->dtype)) != PI_OK) return s;
   return batch > 4096 ? PI_EUNSUPPORTED : PI_OK;
-}
-
-// f(a value of the element type, a constant of the padded dim)
-template <class F>
-void with_type(int dtype, int dim, F f) {
-  auto by_dim = [&](auto t) {
-    if (dim <= 64) f(t, std::integral_constant<int, 64>());
-    else if (dim <= 96) f(t, std::integral_constant<int, 96>());
-    else if (dim <= 128) f(t, std::integral_constant<int, 128>());
-    else f(t, std::integral_constant<int, 256>());
-  };
-  if (dtype == PI_F16) by_dim(pit::H16());
-  else by_dim(pit::B16());
 }
 
 }  // namespace
@@ -175,17 +127,7 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
   const int dim = cache->dim;
   char* base = static_cast<char*>(ws);
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  const int64_t at = (int64_t)layer * cache->pages * cache->kv_heads * cache->page * dim;
-  int32_t* lens = cache->meta + (int64_t)cache->slots * cache->max_pages;
-  const pia::Pages pg{static_cast<const uint16_t*>(cache->k) + at,
-                      static_cast<const uint16_t*>(cache->v) + at,
-                      cache->meta,
-                      lens,
-                      lens + cache->slots + 2 * (int64_t)cache->pages + 1,
-                      cache->pages,
-                      cache->page,
-                      cache->max_pages,
-                      cache->slots};
+  const pia::Pages pg = pages_of(cache, layer);
   (void)hipGetLastError();
   with_type(cache->dtype, dim, [&](auto t, auto d) {
     using T = decltype(t);

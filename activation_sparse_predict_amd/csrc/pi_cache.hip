@@ -6,16 +6,9 @@
 #include "pi_host.hpp"
 
 using namespace pih;
+using pic::meta_of;
 
 namespace {
-
-pic::Meta meta_of(const pi_cache* c) {
-  int32_t* table = c->meta;
-  int32_t* lens = table + (int64_t)c->slots * c->max_pages;
-  int32_t* ref = lens + c->slots;
-  return pic::Meta{table, lens, ref, ref + c->pages, ref + 2 * (int64_t)c->pages, c->slots, c->max_pages, c->pages,
-                   c->page};
-}
 
 // plan: count, sources, targets; then the map of a compaction
 struct Ws {

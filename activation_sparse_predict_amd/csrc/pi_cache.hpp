@@ -6,6 +6,7 @@
 // leaves the tables as they were.
 #pragma once
 #include "pi.h"
+#include "pi_meta.hpp"
 #include "pi_tile.hpp"
 
 namespace pic {
@@ -14,12 +15,6 @@ using namespace pit;
 
 constexpr int PL_T = 1024;               // threads of an accounting block
 constexpr int MAX_N = 4096;              // slots one call may name
-
-// The parts of pi_cache.meta.
-struct Meta {
-  int32_t *table, *lens, *ref, *free, *words;
-  int slots, max_pages, pages, page;
-};
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int page) { return (int)((tokens + page - 1) / page); }
 

@@ -4,6 +4,8 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
+#include <utility>
 
 namespace pih {
 
@@ -20,5 +22,20 @@ pi_status launched();
 pi_status check_cache(const pi_cache* c);
 // Alignment of a [tokens][heads][dim] tensor; see pi_heads in pi.h.
 pi_status check_heads(const pi_heads* h, int32_t tokens);
+
+// Whether rows of `dim` elements of an output lie over each other.
+inline bool folded(const pi_heads* h, int64_t tokens, int64_t heads, int64_t dim) {
+  int64_t s = std::abs(h->token_stride), ns = tokens, l = std::abs(h->head_stride), nl = heads;
+  if (ns > 1 && s < dim) return true;
+  if (nl > 1 && l < dim) return true;
+  if (ns == 1 || nl == 1) return false;
+  if (s > l) std::swap(s, l), std::swap(ns, nl);
+  if (l >= s * (ns - 1) + dim) return false;       // one after the other, as tensors are laid out
+  for (int64_t i = 1; i < heads; ++i) {
+    const int64_t at = i * std::abs(h->head_stride), step = std::abs(h->token_stride), t = at / step;
+    if ((t < tokens && at - t * step < dim) || (t + 1 < tokens && (t + 1) * step - at < dim)) return true;
+  }
+  return false;
+}
 
 }  // namespace pih

@@ -1,0 +1,253 @@
+// Device code of rotary positions and norms of heads for gfx950.
+//
+// The angle of pair i at position p is p f_i.  f_i comes as a part of a turn in units
+// of 2^-64, so the product modulo 2^64 is the angle modulo a turn without any rounding,
+// for every position.  Its upper 32 bits give the nearest quarter turn and, as a float32,
+// the rest of at most an eighth of a turn, of which sine and cosine are their series:
+// |a| <= pi / 4, what is left out is below 2^-29 (sine, after a^9) and 2^-25 (cosine,
+// after a^8).
+#pragma once
+#include "pi.h"
+#include "pi_meta.hpp"
+#include "pi_tile.hpp"
+
+namespace pir {
+
+using namespace pit;
+
+// Which dimensions a lane holds as A[0..7] and B[0..7] of a head:
+//  NONE, PAIRS  chunks of 8 dims 2 l and 2 l + 1; pairs lie inside a chunk
+//  HALF         rotary % 16 == 0: chunk l and the one rotary / 2 dims on; the lanes
+//               behind these take what does not turn, two chunks each
+//  ODD          other rotary: dims 8 l .. of the first half and of the second, which
+//               start on no chunk; values are read and written one by one
+enum { NONE = 0, HALF = 1, PAIRS = 2, ODD = 3 };
+
+struct Turn {
+  const uint64_t* steps;
+  int rotary;
+  float magnitude;
+};
+
+// Some heads of a tensor [tokens][heads][dim] and what they become.
+struct Part {
+  const uint16_t* src;
+  int64_t src_token, src_head;
+  uint16_t* dst;
+  int64_t dst_token, dst_head;
+  const float* weight;                   // of their norm, or NULL
+  int heads;
+};
+
+// cos and sin of 2 pi u 2^-32, times m
+__device__ __forceinline__ void sincos_turns(uint32_t u, float m, float* c, float* s) {
+  const uint32_t q = (u + 0x20000000u) >> 30;                  // the nearest quarter, modulo 4
+  const int32_t rest = (int32_t)(u - (q << 30));               // of it, within an eighth of a turn
+  const float a = (float)rest * (6.28318530717958648f / 4294967296.f), b = a * a;
+  float sn = fmaf(b, 2.7557319223985893e-6f, -1.9841269841269841e-4f);
+  sn = fmaf(b, sn, 8.3333333333333333e-3f);
+  sn = fmaf(b, sn, -1.6666666666666667e-1f);
+  sn = fmaf(b * a, sn, a);
+  float cs = fmaf(b, 2.4801587301587302e-5f, -1.3888888888888889e-3f);
+  cs = fmaf(b, cs, 4.1666666666666667e-2f);
+  cs = fmaf(b, cs, -0.5f);
+  cs = fmaf(b, cs, 1.f);
+  const float x = q & 1 ? sn : cs, y = q & 1 ? cs : sn;
+  *c = (q == 1 || q == 2 ? -x : x) * m;
+  *s = (q & 2 ? -y : y) * m;
+}
+
+// The first sequence i whose end cu[i + 1] lies behind token t, by a wave: 64 places at once.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  int lo = 0, len = n;
+  while (true) {
+    const int step = (len + WAVE - 1) / WAVE;
+    const uint64_t hit = __ballot(cu[lo + min((lane + 1) * step, len)] > t);
+    if (!hit) return -1;                           // behind the last sequence
+    const int before = (__ffsll((unsigned long long)hit) - 1) * step;
+    lo += before;
+    len = min(step, len - before);
+    if (step == 1) return lo;
+  }
+}
+
+// Dims of a lane: of A from a on (na of them), of B from b on; whether they turn.
+struct Dims {
+  int a, b, na, nb;
+  bool turns;
+};
+template <int MODE> __device__ __forceinline__ Dims dims_of(int l, int dim, int rotary) {
+  auto upto = [&](int at) { return max(0, min(8, dim - at)); };
+  if constexpr (MODE == HALF) {
+    const int r = rotary / 16;
+    if (l < r) return Dims{8 * l, rotary / 2 + 8 * l, 8, 8, true};
+    const int at = rotary + 16 * (l - r);
+    return Dims{at, at + 8, upto(at), upto(at + 8), false};
+  } else if constexpr (MODE == ODD) {
+    const int half = rotary / 2, r = (half + 7) / 8;
+    if (l < r) return Dims{8 * l, half + 8 * l, min(8, half - 8 * l), min(8, half - 8 * l), true};
+    const int at = rotary + 16 * (l - r);
+    return Dims{at, at + 8, upto(at), upto(at + 8), false};
+  } else {
+    return Dims{16 * l, 16 * l + 8, upto(16 * l), upto(16 * l + 8), MODE == PAIRS && 16 * l < rotary};
+  }
+}
+
+// A wave takes one token and `its` times 64 / P of its heads, P = 2^shift lanes a head
+// (those of q, then of k, then of v, which is copied).  The angles are made once for all of them.
+template <class T, int MODE, bool PAGED>
+__global__ void __launch_bounds__(256)
+k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::Meta m,
+       const int32_t* __restrict__ cu, const int32_t* __restrict__ seqs, int n, int tokens, int dim, float eps, int shift,
+       int its, int waves) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t job = (int64_t)blockIdx.x * 4 + w;
+  const int t = (int)(job / waves), part = (int)(job % waves);
+  if (t >= tokens) return;
+  int at = 0;                                      // the token's position
+  bool paged = true;
+  int64_t page_at = 0, head_at = 0;                // of the cache's page and heads, in elements
+  if constexpr (PAGED) {
+    if (t < cu[0]) return;
+    const int i = find_seq(cu, n, t);
+    if (i < 0 || cu[i] > t) return;
+    const int slot = seqs[i];
+    int bad = 0;
+    if ((unsigned)slot >= (unsigned)m.slots) {
+      bad = PI_CACHE_ESLOT;
+    } else {
+      const int64_t p = (int64_t)m.lens[slot] - cu[i + 1] + t;
+      if (p < 0 || p >= (int64_t)m.max_pages * m.page) {
+        bad = PI_CACHE_ELENGTH;
+      } else {
+        at = (int)p;
+        const int id = m.table[(int64_t)slot * m.max_pages + at / m.page];
+        if ((unsigned)id >= (unsigned)m.pages) bad = PI_CACHE_EPAGE, paged = false;
+        else page_at = ((int64_t)id * k.heads * m.page + at % m.page) * dim, head_at = (int64_t)m.page * dim;
+      }
+    }
+    if (bad && lane == 0) atomicOr(&m.words[1], bad);
+    if (bad & ~PI_CACHE_EPAGE) return;
+  } else if (MODE != NONE) {
+    at = pos[t];
+  }
+  const int l = lane & ((1 << shift) - 1), per = 64 >> shift;
+  const Dims d = dims_of<MODE>(l, dim, turn.rotary);
+  float cs[8], sn[8];
+  if constexpr (MODE != NONE) {
+    const int first = d.turns ? 8 * l : 0, pairs = turn.rotary / 2;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t step = turn.steps[min(first + e, pairs - 1)];
+      sincos_turns((uint32_t)(((uint64_t)(int64_t)at * step) >> 32), turn.magnitude, &cs[e], &sn[e]);
+    }
+  }
+  const int all = q.heads + k.heads + (PAGED ? k.heads : 0);
+  const float over = 1.f / (float)dim;
+
+  struct Row {
+    u4 a, b;
+    int kind, head;                                // 0 q, 1 k, 2 v, 3 none
+  };
+  auto source = [&](int kind, int head) {
+    const Part& x = kind == 0 ? q : kind == 1 ? k : v;
+    return x.src + t * x.src_token + head * x.src_head;
+  };
+  auto load = [&](int it) {
+    Row r;
+    int h = (part * its + it) * per + (lane >> shift);
+    r.kind = h >= all ? 3 : h < q.heads ? 0 : (h -= q.heads) < k.heads ? 1 : (h -= k.heads, 2);
+    if (it >= its) r.kind = 3;
+    if (PAGED && !paged && r.kind > 0) r.kind = 3;
+    r.head = h;
+    r.a = r.b = u4{0, 0, 0, 0};
+    if (r.kind == 3) return r;
+    const uint16_t* src = source(r.kind, h);
+    if constexpr (MODE == ODD) {
+      uint16_t x[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = e < d.na ? src[d.a + e] : 0;
+        x[8 + e] = e < d.nb ? src[d.b + e] : 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        r.a[e] = x[2 * e] | (uint32_t)x[2 * e + 1] << 16;
+        r.b[e] = x[8 + 2 * e] | (uint32_t)x[8 + 2 * e + 1] << 16;
+      }
+    } else {
+      if (d.na > 0) r.a = *reinterpret_cast<const u4*>(src + d.a);
+      if (d.nb > 0) r.b = *reinterpret_cast<const u4*>(src + d.b);
+    }
+    return r;
+  };
+  Row next = load(0);
+  for (int it = 0; it < its; ++it) {
+    const Row r = next;
+    next = load(it + 1);                           // other heads than those written now
+    u4 ya = r.a, yb = r.b;
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = T::low(r.a[e]), x[2 * e + 1] = T::high(r.a[e]);
+      x[8 + 2 * e] = T::low(r.b[e]), x[8 + 2 * e + 1] = T::high(r.b[e]);
+    }
+    const float* weight = r.kind == 0 ? q.weight : r.kind == 1 ? k.weight : nullptr;
+    if (q.weight || k.weight) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int o = 1; o < 1 << shift; o *= 2) ss += __shfl_xor(ss, o);
+      if (weight) {
+        const float inv = rsqrtf(fmaf(ss, over, eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] *= inv * weight[min(d.a + e, dim - 1)];
+          x[8 + e] *= inv * weight[min(d.b + e, dim - 1)];
+        }
+      }
+    }
+    if constexpr (MODE == HALF || MODE == ODD) {
+      if (d.turns) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a = x[e], b = x[8 + e];
+          x[e] = fmaf(a, cs[e], -(b * sn[e]));
+          x[8 + e] = fmaf(b, cs[e], a * sn[e]);
+        }
+      }
+    } else if constexpr (MODE == PAIRS) {
+      const int mine = turn.rotary / 2 - 8 * l;    // of the lane's pairs, those that turn
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1];
+        x[2 * e] = e < mine ? fmaf(a, cs[e], -(b * sn[e])) : a;
+        x[2 * e + 1] = e < mine ? fmaf(b, cs[e], a * sn[e]) : b;
+      }
+    }
+    if (r.kind < 2 && (d.turns || weight)) {       // all else is moved bit by bit
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ya[e] = T::pack(x[2 * e], x[2 * e + 1]);
+        yb[e] = T::pack(x[8 + 2 * e], x[8 + 2 * e + 1]);
+      }
+    }
+    if (r.kind == 3) continue;
+    uint16_t* dst;
+    if (PAGED && r.kind > 0) dst = (r.kind == 1 ? k.dst : v.dst) + page_at + r.head * head_at;
+    else dst = (r.kind == 0 ? q.dst + t * q.dst_token + r.head * q.dst_head : k.dst + t * k.dst_token + r.head * k.dst_head);
+    if constexpr (MODE == ODD) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e < d.na) dst[d.a + e] = (uint16_t)(ya[e / 2] >> 16 * (e % 2));
+        if (e < d.nb) dst[d.b + e] = (uint16_t)(yb[e / 2] >> 16 * (e % 2));
+      }
+    } else {
+      if (d.na > 0) *reinterpret_cast<u4*>(dst + d.a) = ya;
+      if (d.nb > 0) *reinterpret_cast<u4*>(dst + d.b) = yb;
+    }
+  }
+}
+
+}  // namespace pir

@@ -25,6 +25,7 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 // LOW, LAG, HIGH: powers of two of the weights in a softmax, see pi_attn.hpp.
 struct H16 {                       // IEEE binary16
   static constexpr float LOW = 11.f, LAG = 4.f, HIGH = LOW + LAG;
+  static constexpr uint16_t INF = 0x7c00;
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ f16v mma32(u4 a, u4 b, f16v c) {
@@ -37,10 +38,13 @@ struct H16 {                       // IEEE binary16
     v2 r = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, r);
   }
+  static __device__ __forceinline__ float low(uint32_t w) { return (float)__builtin_bit_cast(v2, w)[0]; }
+  static __device__ __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(v2, w)[1]; }
 };
 
 struct B16 {                       // bfloat16
   static constexpr float LOW = 0.f, LAG = 8.f, HIGH = 0.f;
+  static constexpr uint16_t INF = 0x7f80;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v2 __attribute__((ext_vector_type(2)));
   static __device__ __forceinline__ f16v mma32(u4 a, u4 b, f16v c) {
@@ -53,6 +57,8 @@ struct B16 {                       // bfloat16
     v2 r = {(__bf16)a, (__bf16)b};
     return __builtin_bit_cast(uint32_t, r);
   }
+  static __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 };
 
 // Combine a value with those of the lanes that hold the same column of a D

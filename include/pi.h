@@ -333,6 +333,106 @@ pi_status pi_attn_decode(const pi_cache* cache, int32_t layer, const pi_heads* q
                          int32_t heads, const int32_t* seqs, const int32_t* prefix, float scale, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions and norms of heads, on their own and on the way into the
+ * cache, and attention of chunks of new tokens over it: what a serving step
+ * whose prompts come in pieces needs between its products.
+ */
+
+/* Which two of the first `rotary` dimensions of a head turn together as pair i:
+ * i and i + rotary / 2, or 2 i and 2 i + 1. */
+typedef enum { PI_ROPE_HALF = 0, PI_ROPE_PAIRS = 1 } pi_rope_layout;
+
+/* Rotary positions: at position p pair i, (x, y), becomes
+ *   m (x cos a - y sin a, x sin a + y cos a),  a = p f_i,  m = magnitude.
+ * Dimensions from `rotary` on stay as they are.
+ *  steps: DEVICE, [rotary / 2], 16-byte aligned: f_i as a part of a turn in units
+ *         of 2^-64 (pi_rope_steps).  p steps_i modulo 2^64 is the angle without a
+ *         rounding, so far positions are as exact as near ones.
+ *  rotary: even, 2 .. dim.  layout: pi_rope_layout.  magnitude: finite, positive;
+ *         0 = 1. */
+typedef struct {
+  const uint64_t* steps;
+  int32_t rotary, layout;
+  float magnitude;
+} pi_rope;
+
+/* How the frequencies f_i, i < rotary / 2, follow from the base:
+ *  PLAIN   base^(-2 i / rotary)
+ *  LINEAR  the same over `factor` (positions interpolated)
+ *  BASE    with base factor^(rotary / (rotary - 2)) in place of base; rotary > 2
+ *  BANDS   with f plain and t = trained f / (2 pi) its turns over the trained
+ *          length: f / factor where t <= low, f where t >= high, between them
+ *          f (1 - s) / factor + f s with s = (t - low) / (high - low)
+ *  RAMP    the same with s falling with the pair's number i: from 1 at
+ *          floor(n(high)), at least 0, to 0 at ceil(n(low)), at most rotary - 1,
+ *          n(t) = rotary ln(trained / (2 pi t)) / (2 ln base); where these two are
+ *          equal the second counts as 0.001 more.  magnitude 0.1 ln(factor) + 1. */
+typedef enum {
+  PI_ROPE_PLAIN = 0, PI_ROPE_LINEAR = 1, PI_ROPE_BASE = 2, PI_ROPE_BANDS = 3, PI_ROPE_RAMP = 4
+} pi_rope_rule;
+
+/* base > 1; factor >= 1 (but for PLAIN); trained > 0 and 0 < low < high (BANDS, RAMP). */
+typedef struct {
+  double base, factor, trained, low, high;
+  int32_t rule;
+} pi_rope_scaling;
+
+/* The frequencies of a rule in radians a token, and its magnitude (1 but for RAMP;
+ * may be NULL).  freqs: HOST, [rotary / 2]. */
+pi_status pi_rope_freqs(const pi_rope_scaling* scaling, int32_t rotary, double* freqs, float* magnitude);
+/* steps[i] of n frequencies (finite, of any sign): both in HOST memory.  Off by at
+ * most 2^-52 of the frequency and 2^-64 of a turn. */
+pi_status pi_rope_steps(const double* freqs, int32_t n, uint64_t* steps);
+
+/*
+ * pi_rope_heads -- queries and keys of packed tokens, normed and turned:
+ *   y = x w / sqrt(mean(x^2) + eps)   over a head's dim dimensions, if it has a
+ *                                     norm w ([dim] float32, 16-byte aligned),
+ * then y at position pos[t] ([tokens], any int32) as `rope` says.  rope NULL:
+ * nothing turns, pos is not read.  q_norm, k_norm NULL: no norm; eps finite and
+ * positive where there is one.  k, k_out NULL with kv_heads 0: queries alone.
+ * Everything is float32 with one rounding at the end; each output is x's own
+ * tensor with its strides, or lies over no input and no other output.
+ */
+pi_status pi_rope_heads(const pi_rope* rope, const int32_t* pos, const pi_heads* q, const pi_heads* q_out, int32_t heads,
+                        const float* q_norm, const pi_heads* k, const pi_heads* k_out, int32_t kv_heads,
+                        const float* k_norm, float eps, int32_t tokens, int32_t dim, int32_t dtype, void* stream);
+
+/*
+ * pi_cache_append_rope -- pi_cache_append of normed and turned keys: row t of k,
+ * as pi_rope_heads makes it at the position that the token has in its slot, and
+ * of v go to the slot's pages; row t of q, likewise, goes to q_out (q, q_out NULL
+ * with heads 0: keys alone).  Rows of a slot or length that cannot be are not
+ * written, nor is what a broken page would hold.
+ */
+pi_status pi_cache_append_rope(const pi_cache* cache, int32_t layer, const pi_rope* rope, const pi_heads* q,
+                               const pi_heads* q_out, int32_t heads, const float* q_norm, const pi_heads* k,
+                               const pi_heads* v, const float* k_norm, float eps, int32_t tokens, const int32_t* cu,
+                               const int32_t* seqs, int32_t n, void* stream);
+
+/*
+ * pi_attn_chunk -- attention of new tokens over the cache: rows cu[i] .. cu[i + 1] - 1
+ * of q and out, c of them, are the LAST c of the L tokens that slot seqs[i] (slot i
+ * where seqs is NULL; then n <= slots) holds in the layer, and the row at place
+ * p = L - c + t sees the keys j <= p, with a window > 0 only those with j > p - window:
+ *   x_j = scale q . k_j                     (scale as in pi_attn_prompt)
+ *   x_j = cap tanh(x_j / cap)               if cap > 0 (at most 1024, else PI_EUNSUPPORTED)
+ *   x_j = x_j + slopes[h] (j - p)           if slopes ([heads] float32, on the device)
+ *   out = sum_j p_j v_j,  p = softmax(x)
+ * A chunk may be one token, a whole prompt or anything between, and a batch any mix
+ * of them; a slot may come more than once.  Keys a row does not see leave no trace
+ * in it.  A row that sees no key (a slot that cannot be, PI_CACHE_ESLOT, a slot that
+ * holds fewer than c tokens, PI_CACHE_ELENGTH) is zero; keys of a broken page
+ * (PI_CACHE_EPAGE) are not seen.  Rows that no sequence holds are not written.
+ * cu as in pi_attn_prompt; n <= 4096.  A capped score is off by at most 2^-21 cap
+ * beside its rounding.
+ */
+size_t pi_attn_chunk_workspace_bytes(const pi_cache* cache, int32_t tokens, int32_t heads, int32_t n);
+pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q, const pi_heads* out, int32_t tokens,
+                        int32_t heads, const int32_t* cu, const int32_t* seqs, int32_t n, float scale, float cap,
+                        const float* slopes, int32_t window, void* ws, size_t ws_bytes, void* stream);
+
 /*
  * pi_matvec -- y_b = W x_b + bias for 1 <= batch <= 32 rows, W a Q4_0 matrix
  * [rows][cols] (pi_mat, 16-byte aligned nibbles, 2-byte aligned scales),
