@@ -87,9 +87,13 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   int32_t* count = reinterpret_cast<int32_t*>(base);
   auto* joints = reinterpret_cast<pia::Joint*>(base + W.joints);
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  const int per = cache->page / 16;
-  const pia::Chunks ch{cu, seqs, n, tokens, heads, cache->kv_heads, cache->dim, u.free, 1, u.slots, u.rows,
-                       ((uint64_t(1) << 36) + per - 1) / per};
+  // the page of a place of 16 keys by a multiplication: ceil(2^(31 + shift) / per) is off by less than 1, and with
+  // 2^shift <= per < 2^(shift + 1) that changes no quotient of a place below 2^30
+  const uint32_t per = cache->page / 16;
+  uint32_t shift = 0;
+  while (per >> (shift + 1)) ++shift;
+  const uint32_t mul = (uint32_t)(((uint64_t(1) << (31 + shift)) + per - 1) / per);
+  const pia::Chunks ch{cu, seqs, n, tokens, heads, cache->kv_heads, cache->dim, u.free, 1, u.slots, u.rows, mul, shift};
   const pia::Pages pg = pages_of(cache, layer);
   uint16_t* dst = static_cast<uint16_t*>(out->p);
   (void)hipGetLastError();

@@ -29,7 +29,7 @@ struct Chunks {
   int n, tokens, heads, kv_heads, dim;
   int free, least;                       // shares to deal beside one a tile; key tiles of a share at least
   int slots, rows;                       // places for sums in the workspace, rows of each
-  uint64_t per;                          // 2^36 / (places of 16 keys in a page), rounded up
+  uint32_t mul, shift;                   // a place's page: mulhi(2 place, mul) >> shift
 };
 
 // A tile of rows whose keys are shared out, for k_chunk_join.
@@ -128,7 +128,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 // A table's entry by a scalar load: the tables do not change while the kernel runs.
-__device__ __forceinline__ int entry(const int32_t* table, int64_t at) {
+__device__ __forceinline__ int entry(const int32_t* table, int at) {
   typedef const __attribute__((address_space(4))) int32_t* fixed;
   return reinterpret_cast<fixed>(reinterpret_cast<uintptr_t>(table))[at];
 }
@@ -270,51 +270,81 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
 
   const int r0 = tid / L::NC;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * w;
-  const int64_t table = (int64_t)max(pc.s.slot, 0) * pg.max_pages;
+  const int32_t* table = pg.table + (int64_t)max(pc.s.slot, 0) * pg.max_pages;
   const int64_t head_at = (int64_t)pg.page * ch.dim, page_at = head_at * ch.kv_heads;
-  auto page_of = [&](int x) { return (int)((uint64_t)(uint32_t)x * ch.per >> 36); };
-  auto outside = [&](int j, int i) { return PT_K * j + 16 * i >= to || PT_K * j + 16 * i + 16 <= from; };
-  // page numbers of a tile's four places of 16 keys
+  const uint16_t *kg = pg.k + g * head_at, *vg = pg.v + g * head_at;
+  auto page_of = [&](uint32_t x) { return (int)(__umulhi(2 * x, ch.mul) >> ch.shift); };
+  // first element of a place of 16 keys, from its page's number
+  auto place_at = [&](int x, int id) { return id * page_at + (int64_t)((x - page_of(x) * (pg.page / 16)) * 16 * ch.dim); };
+  // what a lane loads of a place: the chunk that its place in LDS asks for
+  uint32_t off[R::NV];
+  bool mine_too[R::NV];
+#pragma unroll
+  for (int i = 0; i < R::NV; ++i) {
+    const int r = i * R::RN + r0, c = (tid % L::NC) ^ L::swz(r);
+    off[i] = 2 * (uint32_t)(r % 16 * ch.dim + 8 * c);
+    mine_too[i] = c < nchunk;
+  }
+  // page numbers of a tile's four places; below a share's last tile all of them lie in the table's row
   struct Ids {
     int id[4];
   };
   auto look_up = [&](int j) {
     Ids x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x.id[i] = j >= first && !outside(j, i) ? entry(pg.table, table + page_of(4 * j + i)) : -1;
+    for (int i = 0; i < 4; ++i) x.id[i] = entry(table, page_of(4 * j + i));
     return x;
   };
-  // a tile into LDS; keys that no row sees are zeros: with anything else there, 0 times an infinity would be NaN.  Which
-  // places there are.
+  // a tile that is whole: every place is there, and some row sees every key
   auto fetch = [&](int j, const Ids& x) {
-    uint32_t bits = 0;
     int64_t at[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int id = usable_page(x.id[i], pg.pages), p = 4 * j + i;
-      if (id >= 0) bits |= 1u << i;
-      else if (!outside(j, i) && tid == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
-      at[i] = id * page_at + g * head_at + (int64_t)(16 * p - page_of(p) * pg.page) * ch.dim;
-    }
-    const int over = to - PT_K * j, under = from - PT_K * j;
+    for (int i = 0; i < 4; ++i) at[i] = place_at(4 * j + i, x.id[i]);
+    const uint32_t dst = lds0 + j % S * R::BYTES;
+    const char *ka[R::LD], *va[R::LD];
 #pragma unroll
     for (int i = 0; i < R::LD; ++i) {
-      const int r = i * R::RN + r0, c = (tid % L::NC) ^ L::swz(r);
-      const int p = (i * R::RN + 64 * w / L::NC) / 16;   // the wave's rows lie in one place
-      const uint32_t dst = lds0 + j % S * R::BYTES + i * 16 * NT;
-      if ((bits >> p & 1) && r < over && r >= under) {
-        const uint32_t off = 2 * (uint32_t)(r % 16 * ch.dim + 8 * c);
-        int64_t a = at[0];
+      // the wave's rows lie in one place, which for rows of 8 chunks hangs on the wave
+      const int64_t a = uniform(R::RN >= 32 ? (w >= 2 ? at[2 * i + 1] : at[2 * i]) : at[i * R::RN / 16]);
+      ka[i] = reinterpret_cast<const char*>(kg + a), va[i] = reinterpret_cast<const char*>(vg + a);
+    }
 #pragma unroll
-        for (int y = 1; y < 4; ++y) a = p == y ? at[y] : a;
+    for (int v = 0; v < R::NV; ++v)
+      if (mine_too[v])
+#pragma unroll
+        for (int i = v; i < R::LD; i += R::NV) {
+          to_lds(ka[i], off[v], dst + i * 16 * NT);
+          to_lds(va[i], off[v], dst + S * R::BYTES + i * 16 * NT);
+        }
+  };
+  // Any tile; keys that no row sees are zeros: with anything else there, 0 times an infinity would be NaN.  Which places
+  // there are.
+  auto fetch_part = [&](int j) {
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (int i = 0; i < R::LD; ++i) {
+      const int r = i * R::RN + r0, key = PT_K * j + r, c = (tid % L::NC) ^ L::swz(r);
+      const int x = __builtin_amdgcn_readfirstlane(key / 16);
+      const bool inside = 16 * x < to && 16 * x + 16 > from;
+      const int id = inside ? usable_page(entry(table, page_of(x)), pg.pages) : -1;
+      const uint32_t dst = lds0 + j % S * R::BYTES + i * 16 * NT;
+      if (id >= 0 && key < to && key >= from) {
+        const int64_t a = uniform(place_at(x, id));
         if (c < nchunk) {
-          to_lds(pg.k + uniform(a), off, dst);
-          to_lds(pg.v + uniform(a), off, dst + S * R::BYTES);
+          to_lds(kg + a, 2 * (uint32_t)(r % 16 * ch.dim + 8 * c), dst);
+          to_lds(vg + a, 2 * (uint32_t)(r % 16 * ch.dim + 8 * c), dst + S * R::BYTES);
         }
       } else {
         char* own = ring + j % S * R::BYTES + i * 16 * NT + 16 * tid;
         *reinterpret_cast<u4*>(own) = *reinterpret_cast<u4*>(own + S * R::BYTES) = u4{0, 0, 0, 0};
       }
+    }
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int x = 4 * j + i;
+      if (16 * x >= to || 16 * x + 16 <= from) continue;
+      if (usable_page(entry(table, page_of(x)), pg.pages) >= 0) bits |= 1u << i;
+      else if (tid == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
     }
     return bits;
   };
@@ -324,15 +354,18 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   uint32_t bits = 0;
   Ids ids{};
   if (first <= last) {
-    bits = fetch(last, look_up(last));
-    ids = look_up(last - 1);
+    bits = fetch_part(last);
+    if (first < last) ids = look_up(last - 1);
   }
   for (int j = last; j >= first; --j) {
     arrive<0>();
     const uint32_t there = bits;
     if (j > first) {
-      bits = fetch(j - 1, ids);
-      ids = look_up(j - 2);
+      const uint32_t top = max(max((uint32_t)ids.id[0], (uint32_t)ids.id[1]), max((uint32_t)ids.id[2], (uint32_t)ids.id[3]));
+      bits = 15;
+      if (top < (uint32_t)pg.pages && PT_K * (j - 1) >= from) fetch(j - 1, ids);
+      else bits = fetch_part(j - 1);
+      ids = look_up(max(j - 2, first));
     }
     const int k0 = PT_K * j;
     const int below = place + 1 - k0, above = sc.window > 0 ? below - sc.window : 0;
