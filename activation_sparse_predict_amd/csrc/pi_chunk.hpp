@@ -268,82 +268,71 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   }
   const float slope = (MOD & CH_SLOPES) && sc.slopes ? sc.slopes[head] * 1.44269504f : 0.f;
 
-  const int r0 = tid / L::NC;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * w;
   const int32_t* table = pg.table + (int64_t)max(pc.s.slot, 0) * pg.max_pages;
-  const int64_t head_at = (int64_t)pg.page * ch.dim, page_at = head_at * ch.kv_heads;
-  const uint16_t *kg = pg.k + g * head_at, *vg = pg.v + g * head_at;
+  const uint32_t head_bytes = 2 * pg.page * ch.dim, page_bytes = head_bytes * ch.kv_heads;     // at most 2^31
+  const char *kg = reinterpret_cast<const char*>(pg.k) + (int64_t)g * head_bytes;
+  const char *vg = reinterpret_cast<const char*>(pg.v) + (int64_t)g * head_bytes;
   auto page_of = [&](uint32_t x) { return (int)(__umulhi(2 * x, ch.mul) >> ch.shift); };
-  // first element of a place of 16 keys, from its page's number
-  auto place_at = [&](int x, int id) { return id * page_at + (int64_t)((x - page_of(x) * (pg.page / 16)) * 16 * ch.dim); };
-  // what a lane loads of a place: the chunk that its place in LDS asks for
-  uint32_t off[R::NV];
-  bool mine_too[R::NV];
+  // byte of a place of 16 keys, from its page's number
+  auto place_at = [&](int x, int id) {
+    return uniform((int64_t)((uint64_t)(uint32_t)id * page_bytes + (uint32_t)(x - page_of(x) * (pg.page / 16)) * (uint32_t)(32 * ch.dim)));
+  };
+  // A wave loads one place of a tile, LW times 1024 bytes.  What a lane takes of it is the chunk that its place in LDS asks for.
+  constexpr int LW = L::NC / 4, RL = 64 / L::NC;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * LW * w;
+  uint32_t off[LW];
 #pragma unroll
-  for (int i = 0; i < R::NV; ++i) {
-    const int r = i * R::RN + r0, c = (tid % L::NC) ^ L::swz(r);
-    off[i] = 2 * (uint32_t)(r % 16 * ch.dim + 8 * c);
-    mine_too[i] = c < nchunk;
+  for (int i = 0; i < LW; ++i) {
+    const int r = i * RL + lane / L::NC, c = (lane % L::NC) ^ L::swz(r);
+    off[i] = c < nchunk ? 2 * (uint32_t)(r * ch.dim + 8 * c) : ~0u;
   }
-  // page numbers of a tile's four places; below a share's last tile all of them lie in the table's row
-  struct Ids {
-    int id[4];
-  };
-  auto look_up = [&](int j) {
-    Ids x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.id[i] = entry(table, page_of(4 * j + i));
-    return x;
-  };
+  auto look_up = [&](int j) { return entry(table, page_of(4 * j + w)); };
   // a tile that is whole: every place is there, and some row sees every key
-  auto fetch = [&](int j, const Ids& x) {
-    int64_t at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = place_at(4 * j + i, x.id[i]);
+  auto fetch = [&](int j, int id) {
+    const int64_t at = place_at(4 * j + w, id);
+    const char *ka = kg + at, *va = vg + at;
     const uint32_t dst = lds0 + j % S * R::BYTES;
-    const char *ka[R::LD], *va[R::LD];
+    if (nchunk == L::NC) {
 #pragma unroll
-    for (int i = 0; i < R::LD; ++i) {
-      // the wave's rows lie in one place, which for rows of 8 chunks hangs on the wave
-      const int64_t a = uniform(R::RN >= 32 ? (w >= 2 ? at[2 * i + 1] : at[2 * i]) : at[i * R::RN / 16]);
-      ka[i] = reinterpret_cast<const char*>(kg + a), va[i] = reinterpret_cast<const char*>(vg + a);
-    }
+      for (int i = 0; i < LW; ++i) to_lds(ka, off[i], dst + 1024 * i);
 #pragma unroll
-    for (int v = 0; v < R::NV; ++v)
-      if (mine_too[v])
+      for (int i = 0; i < LW; ++i) to_lds(va, off[i], dst + S * R::BYTES + 1024 * i);
+    } else {
 #pragma unroll
-        for (int i = v; i < R::LD; i += R::NV) {
-          to_lds(ka[i], off[v], dst + i * 16 * NT);
-          to_lds(va[i], off[v], dst + S * R::BYTES + i * 16 * NT);
+      for (int i = 0; i < LW; ++i)
+        if (off[i] != ~0u) {
+          to_lds(ka, off[i], dst + 1024 * i);
+          to_lds(va, off[i], dst + S * R::BYTES + 1024 * i);
         }
+    }
   };
   // Any tile; keys that no row sees are zeros: with anything else there, 0 times an infinity would be NaN.  Which places
   // there are.
   auto fetch_part = [&](int j) {
-    uint32_t bits = 0;
-#pragma unroll 1
-    for (int i = 0; i < R::LD; ++i) {
-      const int r = i * R::RN + r0, key = PT_K * j + r, c = (tid % L::NC) ^ L::swz(r);
-      const int x = __builtin_amdgcn_readfirstlane(key / 16);
-      const bool inside = 16 * x < to && 16 * x + 16 > from;
-      const int id = inside ? usable_page(entry(table, page_of(x)), pg.pages) : -1;
-      const uint32_t dst = lds0 + j % S * R::BYTES + i * 16 * NT;
+    const int x = 4 * j + w;
+    const bool inside = 16 * x < to && 16 * x + 16 > from;
+    const int id = inside ? usable_page(entry(table, page_of(x)), pg.pages) : -1;
+    const int64_t at = place_at(x, max(id, 0));
+    const uint32_t dst = lds0 + j % S * R::BYTES;
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+      const int key = 16 * x + i * RL + lane / L::NC;
       if (id >= 0 && key < to && key >= from) {
-        const int64_t a = uniform(place_at(x, id));
-        if (c < nchunk) {
-          to_lds(kg + a, 2 * (uint32_t)(r % 16 * ch.dim + 8 * c), dst);
-          to_lds(vg + a, 2 * (uint32_t)(r % 16 * ch.dim + 8 * c), dst + S * R::BYTES);
+        if (off[i] != ~0u) {
+          to_lds(kg + at, off[i], dst + 1024 * i);
+          to_lds(vg + at, off[i], dst + S * R::BYTES + 1024 * i);
         }
       } else {
-        char* own = ring + j % S * R::BYTES + i * 16 * NT + 16 * tid;
+        char* own = ring + j % S * R::BYTES + 1024 * (LW * w + i) + 16 * lane;
         *reinterpret_cast<u4*>(own) = *reinterpret_cast<u4*>(own + S * R::BYTES) = u4{0, 0, 0, 0};
       }
     }
+    uint32_t bits = 0;
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
-      const int x = 4 * j + i;
-      if (16 * x >= to || 16 * x + 16 <= from) continue;
-      if (usable_page(entry(table, page_of(x)), pg.pages) >= 0) bits |= 1u << i;
+      const int y = 4 * j + i;
+      if (16 * y >= to || 16 * y + 16 <= from) continue;
+      if (usable_page(entry(table, page_of(y)), pg.pages) >= 0) bits |= 1u << i;
       else if (tid == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
     }
     return bits;
@@ -351,41 +340,53 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   const Reads<D> rd(lane);
   Sums<T, D> sum;
   sum.clear();
+  f16v s[2];
+  uint32_t pw[16];
   uint32_t bits = 0;
-  Ids ids{};
-  if (first <= last) {
-    bits = fetch_part(last);
-    if (first < last) ids = look_up(last - 1);
+  if (first <= last) bits = fetch_part(last);
+  // tiles below the last one that every row of the block sees whole; none where a page is broken
+  int upper = min(last - 1, (before + t0 + 1) / PT_K - 1), lower = max(first, (from + PT_K - 1) / PT_K);
+  if (sc.window > 0) lower = max(lower, (before + t1 - sc.window) / PT_K + 1);
+  if (upper >= lower) {
+    bool broken = false;
+    for (int e = page_of(4 * lower) + tid, end = page_of(4 * last); e <= end; e += NT) broken |= usable_page(table[e], pg.pages) < 0;
+    if (__syncthreads_or(broken)) upper = lower - 1;
   }
-  for (int j = last; j >= first; --j) {
-    arrive<0>();
-    const uint32_t there = bits;
-    if (j > first) {
-      const uint32_t top = max(max((uint32_t)ids.id[0], (uint32_t)ids.id[1]), max((uint32_t)ids.id[2], (uint32_t)ids.id[3]));
-      bits = 15;
-      if (top < (uint32_t)pg.pages && PT_K * (j - 1) >= from) fetch(j - 1, ids);
-      else bits = fetch_part(j - 1);
-      ids = look_up(max(j - 2, first));
-    }
+  // one tile of any kind, which lies in LDS; `there`: its places
+  auto take = [&](int j, uint32_t there) {
     const int k0 = PT_K * j;
+    char *sk = ring + j % S * R::BYTES, *sv = sk + S * R::BYTES;
     const int below = place + 1 - k0, above = sc.window > 0 ? below - sc.window : 0;
-    if (t0 != t1 && (k0 + PT_K - 1 > before + t0 || (sc.window > 0 && k0 <= before + t1 - sc.window))) {
-      char* sv = ring + (S + j % S) * R::BYTES;
-      if (wild<T, D>(sv)) {
-        add_wild(sum, sv, above, below);
-        tame<T, D>(sv);
-      }
+    if (t0 != t1 && (k0 + PT_K - 1 > before + t0 || (sc.window > 0 && k0 <= before + t1 - sc.window)) && wild<T, D>(sv)) {
+      add_wild(sum, sv, above, below);
+      tame<T, D>(sv);
     }
-    if (!live || k0 > most || (sc.window > 0 && k0 + PT_K - 1 <= least - sc.window)) continue;
-    const char *sk = ring + j % S * R::BYTES, *sv = ring + (S + j % S) * R::BYTES;
-    const bool full = there == 15 && k0 + PT_K - 1 <= least && (sc.window <= 0 || k0 > most - sc.window);
-    f16v s[2];
-    uint32_t pw[16];
+    if (!live || k0 > most || (sc.window > 0 && k0 + PT_K - 1 <= least - sc.window)) return;
     sum.scores(sk, qf, rd, s);
     if constexpr (MOD != 0) change<MOD>(s, sc, slope, k0 - place);
-    if (!full) hide(s, above, below, there);
+    if (there != 15 || k0 + PT_K - 1 > least || (sc.window > 0 && k0 <= most - sc.window)) hide(s, above, below, there);
     sum.weigh(s, MOD ? 1.f : sc.c, pw);
     sum.add(sv, pw, rd);
+  };
+  for (int j = last; j >= first;) {
+    arrive<0>();
+    const uint32_t there = bits;
+    if (j > first) bits = fetch_part(j - 1);
+    take(j, there);
+    if (--j != upper || upper < lower) continue;
+    int id = look_up(max(j - 1, lower));
+    for (; j > lower; --j) {
+      arrive<0>();
+      fetch(j - 1, id);
+      id = look_up(max(j - 2, lower));
+      if (live) {
+        sum.scores(ring + j % S * R::BYTES, qf, rd, s);
+        if constexpr (MOD != 0) change<MOD>(s, sc, slope, PT_K * j - place);
+        sum.weigh(s, MOD ? 1.f : sc.c, pw);
+        sum.add(ring + (S + j % S) * R::BYTES, pw, rd);
+      }
+    }
+    bits = 15;
   }
   if (n == 1) {
     if (live) sum.store(out + (pc.s.first + t) * out_token + head * out_head, row < end, nchunk);
