@@ -4,28 +4,39 @@
 #include <algorithm>
 
 #include "pi_attn_host.hpp"
+#include "pi_chunk_host.hpp"
 
 using namespace pih;
 
 namespace {
 
-constexpr int BLOCKS = 512;              // blocks that shares are dealt to: two for each compute unit
-
 // How a call is cut up.
 struct Cut {
+  int few;        // 16-row tiles of a block of k_chunk_few, or 0: k_attn_chunk
+  int tile;       // rows of a block
   int64_t tiles;  // of rows, at most
   int free;       // shares beside one a tile
   int slots;      // for sums: tiles with several shares have fewer than twice as many of these as were dealt
   int rows;       // of a slot
 };
-Cut cut_of(const pi_cache* c, int tokens, int heads, int n) {
-  Cut u{};
+Cut cut_of(const pi_cache* c, int tokens, int heads, int few) {
   const int64_t group = heads / c->kv_heads;
-  u.tiles = up_div(tokens * group, pia::CH_ROWS) + std::min(n, tokens);
-  u.free = (int)up_div(BLOCKS, c->kv_heads);
+  Cut u{};
+  u.few = few;
+  u.tile = few ? 16 * few : pia::CH_ROWS;
+  // blocks that run at once: two, three or (wide heads) one for each compute unit
+  const int blocks = c->dim > 128 ? 256 : few == 1 || c->dim <= 64 ? 768 : 512;
+  u.free = (int)up_div(blocks, c->kv_heads);
   u.slots = 2 * u.free;
-  u.rows = (int)std::min<int64_t>(pia::CH_ROWS, up_div(tokens * group, 32) * 32);
+  u.rows = (int)std::min<int64_t>(u.tile, up_div(tokens * group, 16) * 16);
   return u;
+}
+
+// Which kernel takes a call: that for few rows where the chunks' rows of a key head are up to 48 on the average (32 for wide
+// heads).  A chunk that has more of them, or fewer, is in good hands all the same: only its time hangs on this.
+int few_of(const pi_cache* c, int tokens, int heads, int n) {
+  const int64_t rows = up_div(tokens, std::max(1, std::min(n, tokens))) * (heads / c->kv_heads);
+  return rows > (c->dim > 128 ? 32 : 48) ? 0 : (int)up_div(rows, 16);
 }
 
 struct Ws {
@@ -40,16 +51,21 @@ Ws ws_of(const pi_cache* c, const Cut& u) {
   w.total = w.stat + ws_align(sizeof(float) * 2 * rows);
   return w;
 }
+// Of all ways a call with so many rows may go, so that room for more rows is room for fewer.
+size_t ws_bytes_of(const pi_cache* c, int tokens, int heads) {
+  size_t most = 0;
+  for (int few = 0; few <= 3; ++few) most = std::max(most, ws_of(c, cut_of(c, tokens, heads, few)).total);
+  return most;
+}
 
 pi_status check_sizes(const pi_cache* c, int32_t tokens, int32_t heads, int32_t n) {
   pi_status s;
   if ((s = check_cache(c)) != PI_OK) return s;
   if (tokens < 0 || n < 1) return PI_EINVAL;
   if ((s = check_shape(heads, c->kv_heads, c->dim, c->dtype)) != PI_OK) return s;
-  // rows and blocks are 32-bit numbers
-  if (n > 4096 || (int64_t)tokens * heads > INT32_MAX - 127) return PI_EUNSUPPORTED;
-  const Cut u = cut_of(c, tokens, heads, n);
-  return (u.tiles + u.free) * c->kv_heads > INT32_MAX ? PI_EUNSUPPORTED : PI_OK;
+  // rows and blocks are 32-bit numbers: a tile for every 16 rows, for each chunk and for each of 768 shares at most
+  if (n > 4096 || (int64_t)tokens * heads > INT32_MAX / 2) return PI_EUNSUPPORTED;
+  return PI_OK;
 }
 
 }  // namespace
@@ -57,7 +73,7 @@ pi_status check_sizes(const pi_cache* c, int32_t tokens, int32_t heads, int32_t 
 extern "C" {
 
 size_t pi_attn_chunk_workspace_bytes(const pi_cache* c, int32_t tokens, int32_t heads, int32_t n) {
-  return check_sizes(c, tokens, heads, n) == PI_OK ? ws_of(c, cut_of(c, tokens, heads, n)).total : 0;
+  return check_sizes(c, tokens, heads, n) == PI_OK ? ws_bytes_of(c, tokens, heads) : 0;
 }
 
 pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q, const pi_heads* out, int32_t tokens,
@@ -78,14 +94,13 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   }
   sc.slopes = slopes, sc.window = window;
   if (tokens == 0) return PI_OK;
-  const Cut u = cut_of(cache, tokens, heads, n);
-  const Ws W = ws_of(cache, u);
-  if (!ws || ws_bytes < W.total || !on(ws, kWsAlign)) return PI_EWORKSPACE;
+  if (!ws || ws_bytes < ws_bytes_of(cache, tokens, heads) || !on(ws, kWsAlign)) return PI_EWORKSPACE;
   if (folded(out, tokens, heads, cache->dim)) return PI_EINVAL;
-  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Cut u = cut_of(cache, tokens, heads, few_of(cache, tokens, heads, n));
+  const Ws W = ws_of(cache, u);
+  const int64_t most = std::min(n, tokens);        // a tile of each chunk may be short
+  const int64_t tiles = up_div((int64_t)tokens * (heads / cache->kv_heads), u.tile) + most;
   char* base = static_cast<char*>(ws);
-  int32_t* count = reinterpret_cast<int32_t*>(base);
-  auto* joints = reinterpret_cast<pia::Joint*>(base + W.joints);
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
   // the page of a place of 16 keys by a multiplication: ceil(2^(31 + shift) / per) is off by less than 1, and with
   // 2^shift <= per < 2^(shift + 1) that changes no quotient of a place below 2^30
@@ -93,26 +108,36 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   uint32_t shift = 0;
   while (per >> (shift + 1)) ++shift;
   const uint32_t mul = (uint32_t)(((uint64_t(1) << (31 + shift)) + per - 1) / per);
-  const pia::Chunks ch{cu, seqs, n, tokens, heads, cache->kv_heads, cache->dim, u.free, 1, u.slots, u.rows, mul, shift};
-  const pia::Pages pg = pages_of(cache, layer);
-  uint16_t* dst = static_cast<uint16_t*>(out->p);
+  pia::ChunkCall call{};
+  call.pg = pages_of(cache, layer);
+  call.q = rows_of(q);
+  call.out = static_cast<uint16_t*>(out->p), call.out_token = out->token_stride, call.out_head = out->head_stride;
+  call.ch = pia::Chunks{cu, seqs, n, tokens, heads, cache->kv_heads, cache->dim, u.tile, u.free, u.slots, u.rows, mul, shift};
+  call.sc = sc;
+  call.count = reinterpret_cast<int32_t*>(base), call.joints = reinterpret_cast<pia::Joint*>(base + W.joints);
+  call.part = floats(W.part), call.stat = floats(W.stat);
+  call.mod = (cap > 0.f ? pia::CH_CAP : 0) | (slopes ? pia::CH_SLOPES : 0);
+  call.few = u.few;
+  call.blocks = (unsigned)((tiles + u.free) * cache->kv_heads);
+  call.stream = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  with_type(cache->dtype, cache->dim, [&](auto t, auto d) {
-    using T = decltype(t);
-    constexpr int D = decltype(d)::value;
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((u.tiles + u.free) * cache->kv_heads)), dim3(256), 0, st, pg, rows_of(q),
-                         dst, out->token_stride, out->head_stride, ch, sc, joints, count, floats(W.part), floats(W.stat));
-    };
-    if (cap > 0.f && slopes) go(pia::k_attn_chunk<T, D, pia::CH_CAP | pia::CH_SLOPES>);
-    else if (cap > 0.f) go(pia::k_attn_chunk<T, D, pia::CH_CAP>);
-    else if (slopes) go(pia::k_attn_chunk<T, D, pia::CH_SLOPES>);
-    else go(pia::k_attn_chunk<T, D, 0>);
-    hipLaunchKernelGGL(pia::k_chunk_join<T>,
-                       dim3((unsigned)(std::min<int64_t>(u.free, u.tiles) * cache->kv_heads), (unsigned)(u.rows / 4)),
-                       dim3(256), 0, st, joints, count, floats(W.part), floats(W.stat), dst, out->token_stride,
-                       out->head_stride, ch);
-  });
+  if (u.few) {
+    pia::launch_few(cache->dtype, call);
+  } else {
+    with_type(cache->dtype, cache->dim, [&](auto t, auto d) {
+      using T = decltype(t);
+      constexpr int D = decltype(d)::value;
+      pia::with_mod(call.mod, [&](auto m) { pia::launch(pia::k_attn_chunk<T, D, decltype(m)::value>, call); });
+    });
+  }
+  auto join = [&](auto t) {
+    hipLaunchKernelGGL(pia::k_chunk_join<decltype(t)>,
+                       dim3((unsigned)(std::min<int64_t>(u.free, tiles) * cache->kv_heads), (unsigned)up_div(u.rows, 4)),
+                       dim3(256), 0, call.stream, call.joints, call.count, call.part, call.stat, call.out, call.out_token,
+                       call.out_head, call.ch);
+  };
+  if (cache->dtype == PI_F16) join(pit::H16());
+  else join(pit::B16());
   return launched();
 }
 

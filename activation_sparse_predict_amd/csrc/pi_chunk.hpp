@@ -11,7 +11,7 @@
 
 namespace pia {
 
-constexpr int CH_ROWS = 128;             // rows of a block
+constexpr int CH_ROWS = 128;             // rows of a block of k_attn_chunk
 constexpr int CH_MOST = 64;              // shares of a tile's keys at most
 
 enum { CH_CAP = 1, CH_SLOPES = 2 };
@@ -27,7 +27,8 @@ struct ChunkScore {
 struct Chunks {
   const int32_t *cu, *seqs;
   int n, tokens, heads, kv_heads, dim;
-  int free, least;                       // shares to deal beside one a tile; key tiles of a share at least
+  int tile;                              // rows of a block
+  int free;                              // shares to deal beside one a tile
   int slots, rows;                       // places for sums in the workspace, rows of each
   uint32_t mul, shift;                   // a place's page: mulhi(2 place, mul) >> shift
 };
@@ -53,7 +54,7 @@ __device__ __forceinline__ Seq seq_of(const Pages& pg, const Chunks& ch, int win
   s.raw = s.slot >= 0 ? pg.lens[s.slot] : 0;
   s.len = usable_len(s.raw, pg.max_pages, pg.page);
   const int group = ch.heads / ch.kv_heads;
-  s.tiles = (int)(((int64_t)s.count * group + CH_ROWS - 1) / CH_ROWS);
+  s.tiles = (int)(((int64_t)s.count * group + ch.tile - 1) / ch.tile);
   s.keys = pieces(s.len, PT_K);
   // a tile's rows lie at 127 / group + 2 places at most
   if (window > 0) s.keys = (int)min((uint32_t)s.keys, ((uint32_t)min(window, s.len) + 127 / group + 1) / PT_K + 2);
@@ -75,26 +76,40 @@ __device__ __forceinline__ float add64(float v) {        // over the wave, the s
   return v;
 }
 
-// Every tile of rows has one share; `free` more go to those with most keys.  Sums are float32: what they may be off by is
-// made up for in the size of a share, so that the blocks there are suffice.  `count`: count the tiles that are shared out too.
+__device__ __forceinline__ int shares_of(const Seq& s, uint32_t size) {
+  return max(1, min(CH_MOST, (int)(((uint32_t)s.keys + size - 1) / size)));
+}
+
+// Every tile of rows has one share, and up to `free` more are dealt.  Where there are fewer tiles than that, a share is made
+// as small as it can be with no more than `free` of them in all, so that all blocks run at once: a few steps towards that
+// size, for up to 64 sequences.  Sums are float32: what they may be off by is made up for in the size of a share, so that
+// the blocks there are suffice.  `count`: count the tiles that are shared out too.
 __device__ __forceinline__ Piece find_piece(const Pages& pg, const Chunks& ch, int window, int idx, bool count) {
   const int lane = threadIdx.x & (WAVE - 1);
   Seq s = seq_of(pg, ch, window, lane);
-  float work = (float)s.tiles * (float)s.keys;
+  float work = (float)s.tiles * (float)s.keys, tiles = (float)s.tiles;
   for (int base = WAVE; base < ch.n; base += WAVE) {
     const Seq x = seq_of(pg, ch, window, base + lane);
     work += (float)x.tiles * (float)x.keys;
+    tiles += (float)x.tiles;
   }
-  const float all = add64(work);
-  const uint32_t size = __builtin_amdgcn_readfirstlane(
-      max((uint32_t)ch.least, (uint32_t)min(all / (float)ch.free * 1.0001f, 2e9f) + 1));
+  const float all = add64(work), free = (float)ch.free;
+  float want = all / free * 1.0001f;
+  if (ch.n <= WAVE && add64(tiles) < free) {
+    for (int i = 0; i < 4; ++i) {
+      const float got = add64((float)s.tiles * (float)shares_of(s, (uint32_t)min(want, 2e9f) + 1));
+      if (got <= free) break;
+      want = max(want * (got / free), want + 1.f);
+    }
+  }
+  const uint32_t size = __builtin_amdgcn_readfirstlane((uint32_t)min(want, 2e9f) + 1);
   Piece p{};
   p.size = size;
   int slot = 0, joint = 0;
   bool found = false;
   for (int base = 0; base < ch.n; base += WAVE) {
     if (base) s = seq_of(pg, ch, window, base + lane);
-    const int n = max(1, min(CH_MOST, (int)(((uint32_t)s.keys + size - 1) / size)));
+    const int n = shares_of(s, size);
     const int blocks = s.tiles * n, upto = scan64(blocks);
     const int js = n > 1 ? s.tiles : 0, jupto = scan64(js), supto = scan64(n > 1 ? blocks : 0);
     const uint64_t hit = __ballot(upto > idx);
@@ -153,6 +168,26 @@ __device__ __forceinline__ void change(f16v* s, const ChunkScore& sc, float slop
     }
 }
 
+// The same for the scores of a step of 32 keys of few_rows.
+template <int MOD>
+__device__ __forceinline__ void change16(f4* s, const ChunkScore& sc, float slope, int back) {
+  const float at = slope * (float)(back + 4 * (int)((threadIdx.x & 63) >> 4));
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x;
+      if constexpr (MOD & CH_CAP) {
+        const float e = exp2_fast(s[h][i] * sc.pre);
+        x = fmaf(-2.f * sc.cap, __builtin_amdgcn_rcpf(e + 1.f), sc.cap);
+      } else {
+        x = s[h][i] * sc.c;
+      }
+      if constexpr (MOD & CH_SLOPES) x += fmaf(slope, (float)(16 * h + i), at);
+      s[h][i] = x;
+    }
+}
+
 // Scores of keys that a row does not see: it sees those from `lo` on and before `hi` in the places of 16 that `bits` names.
 __device__ __forceinline__ void hide(f16v* s, int lo, int hi, uint32_t bits) {
   const int half = 4 * ((threadIdx.x & 63) >> 5);
@@ -178,26 +213,11 @@ template <class T, int D> __device__ __forceinline__ bool wild(const char* tile)
   return __ballot(top[0] >= T::INF || top[1] >= T::INF) != 0;
 }
 
-// 0 times an infinity or NaN of a value that a row does not see is NaN.  So where a tile that is not seen by all of a block's
-// rows holds such values, they are added as they are, by the rows that see them (a weight times an infinity is that
-// infinity, times NaN is NaN), and count as zeros after that: `add_wild` by every wave, then `tame` by all threads.
-template <class T, int D>
-__device__ __forceinline__ void add_wild(Sums<T, D>& sum, const char* sv, int lo, int hi) {
-  using L = Tile<D>;
-  const int half = (threadIdx.x & 63) >> 5;
-#pragma unroll 1
-  for (int key = 0; key < PT_K; ++key) {
-    const bool seen = key < hi && key >= lo;
-#pragma unroll
-    for (int c = 0; c < 4 * L::DT; ++c) {          // dims 8 c + 4 half ..
-      const u2 x = *reinterpret_cast<const u2*>(sv + 16 * L::chunk(key, c) + 8 * half);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (seen && (x[e] & 0x7fffu) >= T::INF) sum.o[c / 4][4 * (c % 4) + 2 * e] += T::low(x[e]);
-        if (seen && (x[e] >> 16 & 0x7fffu) >= T::INF) sum.o[c / 4][4 * (c % 4) + 2 * e + 1] += T::high(x[e]);
-      }
-    }
-  }
+// 0 times an infinity or NaN of a value that a row does not see is NaN.  So where a tile that not all of a block's rows see
+// whole holds such values, they count as zeros (`tame`) and are added at the end to the results of the rows that see them
+// (`add_wild`): a weight times an infinity is that infinity, times NaN is NaN.
+template <class T> __device__ __forceinline__ uint32_t finite(uint32_t x) {      // a mask of the halves that are
+  return ((x & 0x7fffu) >= T::INF ? 0u : 0xffffu) | ((x >> 16 & 0x7fffu) >= T::INF ? 0u : 0xffff0000u);
 }
 template <class T, int D> __device__ __forceinline__ void tame(char* sv) {
   __syncthreads();
@@ -205,11 +225,329 @@ template <class T, int D> __device__ __forceinline__ void tame(char* sv) {
   for (int i = threadIdx.x; i < PT_K * Tile<D>::NC; i += blockDim.x) {
     u4 x = *reinterpret_cast<const u4*>(sv + 16 * i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[e] &= ((x[e] & 0x7fffu) >= T::INF ? 0u : 0xffffu) | ((x[e] >> 16 & 0x7fffu) >= T::INF ? 0u : 0xffff0000u);
+    for (int e = 0; e < 4; ++e) x[e] &= finite<T>(x[e]);
     *reinterpret_cast<u4*>(sv + 16 * i) = x;
   }
   __syncthreads();
+}
+
+// What a block has to do, beside the tensors.
+struct Task {
+  int g, first, last;                    // key head; key tiles of the share
+  int from, to;                          // keys that any row sees
+  int before, t0, t1;                    // place of the chunk's first token; first and last token of the rows
+  int row0, rows, token;                 // first row, rows (0: nothing to do); the chunk's first token in q
+  int64_t table;                         // the slot's row of the table
+  int slot, shares;                      // place for the sums; shares of the tile's keys (1: the result is written)
+};
+
+// That of this block, with what the join and the error word have to know.  Key heads of a piece run side by side, those of
+// one head on one die where they can (block b runs on die b % 8).
+__device__ __forceinline__ Task find_task(const Pages& pg, const Chunks& ch, int window, Joint* joints, int32_t* count) {
+  const int idx = blockIdx.x / ch.kv_heads;
+  const Piece pc = find_piece(pg, ch, window, idx, blockIdx.x == 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *count = pc.joints;
+  Task k{};
+  if (pc.s.count == 0) return k;
+  const int group = ch.heads / ch.kv_heads;
+  k.g = blockIdx.x % ch.kv_heads;
+  k.before = pc.s.len - pc.s.count;
+  k.row0 = ch.tile * pc.tile;
+  const int rows = min(ch.tile, pc.s.count * group - k.row0);
+  k.t0 = k.row0 / group, k.t1 = (k.row0 + rows - 1) / group;
+  k.to = max(0, k.before + k.t1 + 1), k.from = window > 0 ? max(0, k.before + k.t0 + 1 - window) : 0;
+  const int tiles = k.to > k.from ? (k.to - 1) / PT_K - k.from / PT_K + 1 : 0;
+  // shares of this tile: no more than its keys need
+  k.shares = max(1, min(pc.shares, (int)(((uint32_t)tiles + pc.size - 1) / pc.size)));
+  if (k.g == 0 && pc.share == 0 && threadIdx.x == 0) {
+    if (pc.s.slot < 0 || pc.s.len != pc.s.raw || k.before < 0)
+      atomicOr(pg.flags, pc.s.slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
+    if (pc.shares > 1 && pc.joint < ch.slots / 2)
+      joints[pc.joint] = Joint{pc.slot, k.shares, pc.s.first, k.row0, rows, pc.s.tiles};
+  }
+  k.slot = pc.slot + pc.share * pc.s.tiles;
+  if (pc.share >= k.shares || (k.shares > 1 && k.slot >= ch.slots)) return k;
+  k.first = k.from / PT_K + share_begin(tiles, pc.share, k.shares);
+  k.last = k.from / PT_K + share_begin(tiles, pc.share + 1, k.shares) - 1;
+  k.token = pc.s.first;
+  k.table = (int64_t)max(pc.s.slot, 0) * pg.max_pages;
+  k.rows = rows;
+  return k;
+}
+
+__device__ __forceinline__ int page_of(const Chunks& ch, uint32_t place) {
+  return (int)(__umulhi(2 * place, ch.mul) >> ch.shift);
+}
+
+// Whether some of the rows do not see all keys of a tile.
+__device__ __forceinline__ bool at_edge(const Task& k, int window, int tile) {
+  return PT_K * tile + PT_K - 1 > k.before + k.t0 || (window > 0 && PT_K * tile <= k.before + k.t1 - window);
+}
+
+// What `tame` took from the rows' sums, for all threads of a block after the sums were written.
+template <class T>
+__device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, int window, const Task& k, uint16_t* out,
+                                         int64_t out_token, int64_t out_head, float* part) {
+  __syncthreads();
+  const int group = ch.heads / ch.kv_heads, dim = ch.dim;
+  const int64_t sums = ((int64_t)k.slot * ch.kv_heads + k.g) * ch.rows;
+#pragma unroll 1
+  for (int e = threadIdx.x; e < k.rows * dim; e += blockDim.x) {
+    const int row = k.row0 + e / dim, d = e % dim, place = k.before + row / group;
+    const int lo = window > 0 ? max(k.from, place + 1 - window) : k.from;
+    float more = 0.f;
+#pragma unroll 1
+    for (int j = k.first; j <= k.last; ++j) {
+      if (!at_edge(k, window, j)) continue;
+#pragma unroll 1
+      for (int key = max(PT_K * j, lo); key < min(PT_K * j + PT_K, place + 1); ++key) {
+        const int id = usable_page(pg.table[k.table + page_of(ch, key / 16)], pg.pages);
+        if (id < 0) continue;
+        const uint32_t v = pg.v[(((int64_t)id * ch.kv_heads + k.g) * pg.page + key % pg.page) * dim + d];
+        if ((v & 0x7fffu) >= T::INF) more += T::low(v);
+      }
+    }
+    if (more == 0.f) continue;
+    if (k.shares > 1) {
+      part[(sums + row - k.row0) * dim + d] += more;
+    } else {
+      uint16_t* y = out + (k.token + row / group) * out_token + (k.g * group + row % group) * out_head + d;
+      *y = (uint16_t)T::pack(T::low(*y) + more, 0.f);
+    }
+  }
+}
+
+// ---- chunks of few rows: 16 MT of them for a block, with the products and the layout of k_attn_decode.  The four waves take
+// steps of 32 keys in turn, whose keys and values go straight to registers: what a compute unit has on its way from memory
+// bounds these, and its registers hold more than its LDS.
+template <class T, int D, int MOD, int MT>
+__global__ void __launch_bounds__(4 * WAVE, D > 128 ? 1 : D <= 64 || MT == 1 ? 3 : 2)
+k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
+            Joint* __restrict__ joints, int32_t* __restrict__ count, float* __restrict__ part, float* __restrict__ stat) {
+  using V = Vec<D>;
+  constexpr int NF = V::W * V::G, ROW = 16 * NF + 4, NC = Tile<D>::NC;
+  constexpr bool HELD = MT <= 2;                   // queries stay in registers; else they are read from LDS at each step
+  constexpr int JOIN = 4 * 16 * (ROW + 2) * 4, QUERIES = HELD ? 0 : MT * 16 * NC * 16;
+  __shared__ __attribute__((aligned(16))) char lds[JOIN + QUERIES];
+  const Task k = find_task(pg, ch, sc.window, joints, count);
+  if (k.rows == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, kg = lane >> 4, group = ch.heads / ch.kv_heads, nchunk = ch.dim / 8, dim = ch.dim;
+
+  int place[MT];
+  float slope[MT];
+  u4 qf[HELD ? MT : 1][V::KS];
+  char* held = lds + JOIN;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = k.row0 + min(16 * m + r, k.rows - 1), t = row / group, head = k.g * group + row % group;
+    place[m] = k.before + t;
+    slope[m] = (MOD & CH_SLOPES) && sc.slopes ? sc.slopes[head] * 1.44269504f : 0.f;
+    const uint16_t* src = q.at(k.token + t, head);
+#pragma unroll
+    for (int s = 0; s < V::KS; ++s) {
+      const int c = 4 * s + kg;
+      const u4 x = c < nchunk ? *reinterpret_cast<const u4*>(src + 8 * c) : u4{0, 0, 0, 0};
+      if constexpr (HELD) qf[m][s] = x;
+      else if (w == 0) *reinterpret_cast<u4*>(held + 16 * ((16 * m + r) * NC + (c ^ (r % NC)))) = x;
+    }
+  }
+  if constexpr (!HELD) __syncthreads();
+  f4 o[MT][NF];
+  float mc[MT], l[MT];                             // mc: HIGH under c times the largest score so far
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    mc[m] = NEG_INF, l[m] = 0.f;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) o[m][f] = (f4)(0.f);
+  }
+  const int32_t* table = pg.table + k.table;
+  const int64_t head_at = (int64_t)pg.page * dim, page_at = head_at * ch.kv_heads;
+  bool odd = false;                                // whether there were values that are not finite
+
+  for (int st = 2 * k.first + w; st < 2 * (k.last + 1); st += 4) {
+    const int k0 = 32 * st;
+    const uint16_t *kp[2], *vp[2];
+    int from[2], to[2];                            // of the half's keys, those that some row sees
+    bool gone = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = k0 + 16 * h, x = key / 16;
+      from[h] = max(0, k.from - key), to[h] = min(16, k.to - key);
+      int id = 0;
+      if (to[h] > from[h]) {
+        const int number = entry(table, page_of(ch, x));
+        id = usable_page(number, pg.pages);
+        if (id < 0) {                              // a broken table: its keys are not seen
+          if (lane == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
+          to[h] = 0, id = 0, gone = true;
+        }
+      }
+      const int64_t at = id * page_at + k.g * head_at + (int64_t)((x - page_of(ch, x) * (pg.page / 16)) * 16 * dim);
+      kp[h] = pg.k + at;
+      vp[h] = pg.v + at;
+    }
+    // all of the step's loads are on their way before the first product; keys that do not exist lie in a page all the same
+    u4 kf[2][V::KS];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int ks = 0; ks < V::KS; ++ks) {
+        const int c = 4 * ks + kg;
+        kf[h][ks] = *reinterpret_cast<const u4*>(kp[h] + r * dim + 8 * min(c, nchunk - 1));
+        if (c >= nchunk) kf[h][ks] = u4{0, 0, 0, 0};
+      }
+    uint32_t x[V::G][8][V::W / 2];                 // V: keys 4 kg + 0..3 of both halves
+#pragma unroll
+    for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d0 = (16 * gr + r) * V::W;
+        const uint16_t* src = vp[i / 4] + (4 * kg + i % 4) * dim + (d0 < dim ? d0 : 0);
+        if constexpr (V::W == 8) {
+          const u4 y = *reinterpret_cast<const u4*>(src);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[gr][i][e] = y[e];
+        } else {
+          const u2 y = *reinterpret_cast<const u2*>(src);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[gr][i][e] = y[e];
+        }
+      }
+    // whether some row does not see one of the keys
+    const bool some = gone || k0 + 31 > k.before + k.t0 || k0 < k.from || (sc.window > 0 && k0 <= k.before + k.t1 - sc.window);
+    u4 pf[MT];
+    float alpha[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f4 s[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s[h] = (f4)(0.f);
+#pragma unroll
+        for (int ks = 0; ks < V::KS; ++ks) {
+          u4 b;
+          if constexpr (HELD) b = qf[m][ks];
+          else b = *reinterpret_cast<const u4*>(held + 16 * ((16 * m + r) * NC + ((4 * ks + kg) ^ (r % NC))));
+          s[h] = T::mma16(kf[h][ks], b, s[h]);
+        }
+      }
+      if constexpr (MOD != 0) change16<MOD>(s, sc, slope[m], k0 - place[m]);
+      if (some) {
+        const int hi = place[m] + 1 - k0, lo = sc.window > 0 ? hi - sc.window : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = 4 * kg + i;            // in its half
+            if (16 * h + key >= hi || 16 * h + key < lo || key >= to[h]) s[h][i] = NEG_INF;
+          }
+      }
+      const float c = MOD ? 1.f : sc.c;
+      float mt = NEG_INF;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mt = fmaxf(mt, fmaxf(s[0][i], s[1][i]));
+      const float top = fmaxf(mc[m], max16(mt) * c - T::HIGH);
+      const float base = top == NEG_INF ? 0.f : top;   // rows whose scores so far are all -inf
+      alpha[m] = exp2_fast(mc[m] - base);
+      mc[m] = top;
+      float p[8], ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = exp2_fast(fmaf(s[i / 4][i % 4], c, -base));
+        ls += p[i];
+      }
+      l[m] = fmaf(l[m], alpha[m], ls);
+      pf[m] = u4{T::pack(p[0], p[1]), T::pack(p[2], p[3]), T::pack(p[4], p[5]), T::pack(p[6], p[7])};
+    }
+    if (some) {
+      // what no row sees counts as zeros, whatever is stored there
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (4 * kg + i % 4 >= to[i / 4] || 4 * kg + i % 4 < from[i / 4])
+#pragma unroll
+          for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+            for (int e = 0; e < V::W / 2; ++e) x[gr][i][e] = 0;
+    }
+    if (k.t0 != k.t1 && at_edge(k, sc.window, st / 2)) {
+#pragma unroll
+      for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < V::W / 2; ++e) {
+            const uint32_t keep = finite<T>(x[gr][i][e]);
+            odd |= keep != ~0u;
+            x[gr][i][e] &= keep;
+          }
+    }
+#pragma unroll
+    for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+      for (int e = 0; e < V::W / 2; ++e) {
+        auto& y = x[gr];
+        const u4 a = {lows(y[0][e], y[1][e]), lows(y[2][e], y[3][e]), lows(y[4][e], y[5][e]), lows(y[6][e], y[7][e])};
+        const u4 z = {highs(y[0][e], y[1][e]), highs(y[2][e], y[3][e]), highs(y[4][e], y[5][e]),
+                      highs(y[6][e], y[7][e])};
+        const int f = gr * V::W + 2 * e;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[m][f][i] *= alpha[m];
+            o[m][f + 1][i] *= alpha[m];
+          }
+          o[m][f] = T::mma16(a, pf[m], o[m][f]);
+          o[m][f + 1] = T::mma16(z, pf[m], o[m][f + 1]);
+        }
+      }
+  }
+
+  // join the waves, 16 rows at a time: o[m][f][i] belongs to dim (16 gr + 4 kg + i) W + f % W of row 16 m + r
+  float* so = reinterpret_cast<float*>(lds);       // [4][16][ROW], then (reference point, l) [4][16][2]
+  float* sm = so + 4 * 16 * ROW;
+  const int64_t sums = ((int64_t)k.slot * ch.kv_heads + k.g) * ch.rows;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (16 * m >= k.rows) break;
+    __syncthreads();
+    const float ll = sum16(l[m]);
+    if (lane < 16) *reinterpret_cast<float2*>(sm + (16 * w + r) * 2) = float2{mc[m], ll};
+#pragma unroll
+    for (int gr = 0; gr < V::G; ++gr)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int f = 0; f < V::W; ++f) so[(16 * w + r) * ROW + (16 * gr + 4 * kg + i) * V::W + f] = o[m][gr * V::W + f][i];
+    __syncthreads();
+    const int left = min(16, k.rows - 16 * m);
+    for (int e = 2 * tid; e < left * dim; e += 2 * 4 * WAVE) {
+      const int x = e / dim, d = e % dim;
+      float mm = NEG_INF;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mm = fmaxf(mm, sm[(16 * i + x) * 2]);
+      const float base = mm == NEG_INF ? 0.f : mm;
+      float tl = 0.f, oo = 0.f, od = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = exp2_fast(sm[(16 * i + x) * 2] - base);
+        tl = fmaf(sm[(16 * i + x) * 2 + 1], a, tl);
+        oo = fmaf(so[(16 * i + x) * ROW + d], a, oo);
+        od = fmaf(so[(16 * i + x) * ROW + d + 1], a, od);
+      }
+      if (k.shares == 1) {
+        const float inv = tl == 0.f ? 0.f : 1.f / tl;   // a row that sees no key is zero
+        const int row = k.row0 + 16 * m + x;
+        *reinterpret_cast<uint32_t*>(out + (k.token + row / group) * out_token + (k.g * group + row % group) * out_head + d) =
+            T::pack(oo * inv, od * inv);
+      } else {
+        *reinterpret_cast<float2*>(part + (sums + 16 * m + x) * dim + d) = float2{oo, od};
+        if (d == 0) *reinterpret_cast<float2*>(stat + 2 * (sums + 16 * m + x)) = float2{mm, tl};
+      }
+    }
+  }
+  if (k.t0 != k.t1 && __syncthreads_or(odd)) add_wild<T>(pg, ch, sc.window, k, out, out_token, out_head, part);
 }
 
 // One block of 4 waves: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in
@@ -221,36 +559,18 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   using L = Tile<D>;
   constexpr int NT = 4 * WAVE, S = 2;
   using R = Ring<D, S, NT>;
-  constexpr int SUMS = 4 * 32 * 68 * 4;            // sums on their way out
+  constexpr int SUMS = D <= 64 ? 4 * 32 * 68 * 4 : 0;   // sums on their way out, which take more than small tiles do
   __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES > SUMS ? 2 * S * R::BYTES : SUMS];   // K tiles, then V tiles
 
-  // key heads of a piece run side by side, those of one head on one die where they can (block b runs on die b % 8)
-  const int g = blockIdx.x % ch.kv_heads, idx = blockIdx.x / ch.kv_heads;
-  const Piece pc = find_piece(pg, ch, sc.window, idx, blockIdx.x == 0);
+  const Task task = find_task(pg, ch, sc.window, joints, count);
+  if (task.rows == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), hi = lane >> 5;
-  if (blockIdx.x == 0 && tid == 0) *count = pc.joints;
-  if (pc.s.count == 0) return;
   const int group = ch.heads / ch.kv_heads, nchunk = ch.dim / 8;
-  const int before = pc.s.len - pc.s.count;        // place of the chunk's first token
-  const int rows = min(CH_ROWS, pc.s.count * group - CH_ROWS * pc.tile);
-  const int row_first = CH_ROWS * pc.tile;
-  const int t0 = row_first / group, t1 = (row_first + rows - 1) / group;     // its tokens
-  const int to = max(0, before + t1 + 1), from = sc.window > 0 ? max(0, before + t0 + 1 - sc.window) : 0;
-  const int tiles = to > from ? (to - 1) / PT_K - from / PT_K + 1 : 0;
-  // shares of this tile: no more than its keys need
-  const int n = max(1, min(pc.shares, (int)(((uint32_t)tiles + pc.size - 1) / pc.size)));
-  if (blockIdx.x % ch.kv_heads == 0 && pc.share == 0 && tid == 0) {
-    if (pc.s.slot < 0 || pc.s.len != pc.s.raw || before < 0)
-      atomicOr(pg.flags, pc.s.slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
-    if (pc.shares > 1 && pc.joint < ch.slots / 2)
-      joints[pc.joint] = Joint{pc.slot, n, pc.s.first, row_first, rows, pc.s.tiles};
-  }
-  if (pc.share >= n) return;
-  const int first = from / PT_K + share_begin(tiles, pc.share, n), last = from / PT_K + share_begin(tiles, pc.share + 1, n) - 1;
+  const int first = task.first, last = task.last, from = task.from, to = task.to, before = task.before, t0 = task.t0, t1 = task.t1;
 
-  const int row0 = row_first + 32 * w, row = row0 + (lane & 31), end = row_first + rows;
+  const int row0 = task.row0 + 32 * w, row = row0 + (lane & 31), end = task.row0 + task.rows;
   const bool live = row0 < end;
-  const int mine = min(row, end - 1), t = mine / group, head = g * group + mine % group;
+  const int mine = min(row, end - 1), t = mine / group, head = task.g * group + mine % group;
   const int place = before + t;                    // the row sees keys up to here
   const int least = before + row0 / group, most = before + (min(row0 + 32, end) - 1) / group;   // of the wave's rows
   if (nchunk < L::NC) {
@@ -259,7 +579,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   }
   u4 qf[L::KS];
   {
-    const uint16_t* src = q.at(pc.s.first + t, head);
+    const uint16_t* src = q.at(task.token + t, head);
 #pragma unroll
     for (int s = 0; s < L::KS; ++s) {
       const int at = 2 * s + hi;
@@ -268,14 +588,13 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   }
   const float slope = (MOD & CH_SLOPES) && sc.slopes ? sc.slopes[head] * 1.44269504f : 0.f;
 
-  const int32_t* table = pg.table + (int64_t)max(pc.s.slot, 0) * pg.max_pages;
+  const int32_t* table = pg.table + task.table;
   const uint32_t head_bytes = 2 * pg.page * ch.dim, page_bytes = head_bytes * ch.kv_heads;     // at most 2^31
-  const char *kg = reinterpret_cast<const char*>(pg.k) + (int64_t)g * head_bytes;
-  const char *vg = reinterpret_cast<const char*>(pg.v) + (int64_t)g * head_bytes;
-  auto page_of = [&](uint32_t x) { return (int)(__umulhi(2 * x, ch.mul) >> ch.shift); };
+  const char *kg = reinterpret_cast<const char*>(pg.k) + (int64_t)task.g * head_bytes;
+  const char *vg = reinterpret_cast<const char*>(pg.v) + (int64_t)task.g * head_bytes;
   // byte of a place of 16 keys, from its page's number
   auto place_at = [&](int x, int id) {
-    return uniform((int64_t)((uint64_t)(uint32_t)id * page_bytes + (uint32_t)(x - page_of(x) * (pg.page / 16)) * (uint32_t)(32 * ch.dim)));
+    return uniform((int64_t)((uint64_t)(uint32_t)id * page_bytes + (uint32_t)(x - page_of(ch, x) * (pg.page / 16)) * (uint32_t)(32 * ch.dim)));
   };
   // A wave loads one place of a tile, LW times 1024 bytes.  What a lane takes of it is the chunk that its place in LDS asks for.
   constexpr int LW = L::NC / 4, RL = 64 / L::NC;
@@ -286,7 +605,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     const int r = i * RL + lane / L::NC, c = (lane % L::NC) ^ L::swz(r);
     off[i] = c < nchunk ? 2 * (uint32_t)(r * ch.dim + 8 * c) : ~0u;
   }
-  auto look_up = [&](int j) { return entry(table, page_of(4 * j + w)); };
+  auto look_up = [&](int j) { return entry(table, page_of(ch, 4 * j + w)); };
   // a tile that is whole: every place is there, and some row sees every key
   auto fetch = [&](int j, int id) {
     const int64_t at = place_at(4 * j + w, id);
@@ -311,7 +630,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   auto fetch_part = [&](int j) {
     const int x = 4 * j + w;
     const bool inside = 16 * x < to && 16 * x + 16 > from;
-    const int id = inside ? usable_page(entry(table, page_of(x)), pg.pages) : -1;
+    const int id = inside ? usable_page(entry(table, page_of(ch, x)), pg.pages) : -1;
     const int64_t at = place_at(x, max(id, 0));
     const uint32_t dst = lds0 + j % S * R::BYTES;
 #pragma unroll
@@ -332,7 +651,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     for (int i = 0; i < 4; ++i) {
       const int y = 4 * j + i;
       if (16 * y >= to || 16 * y + 16 <= from) continue;
-      if (usable_page(entry(table, page_of(y)), pg.pages) >= 0) bits |= 1u << i;
+      if (usable_page(entry(table, page_of(ch, y)), pg.pages) >= 0) bits |= 1u << i;
       else if (tid == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
     }
     return bits;
@@ -342,6 +661,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   sum.clear();
   f16v s[2];
   uint32_t pw[16];
+  bool odd = false;                                // whether there were values that are not finite
   uint32_t bits = 0;
   if (first <= last) bits = fetch_part(last);
   // tiles below the last one that every row of the block sees whole; none where a page is broken
@@ -349,7 +669,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   if (sc.window > 0) lower = max(lower, (before + t1 - sc.window) / PT_K + 1);
   if (upper >= lower) {
     bool broken = false;
-    for (int e = page_of(4 * lower) + tid, end = page_of(4 * last); e <= end; e += NT) broken |= usable_page(table[e], pg.pages) < 0;
+    for (int e = page_of(ch, 4 * lower) + tid, end = page_of(ch, 4 * last); e <= end; e += NT) broken |= usable_page(table[e], pg.pages) < 0;
     if (__syncthreads_or(broken)) upper = lower - 1;
   }
   // one tile of any kind, which lies in LDS; `there`: its places
@@ -357,9 +677,9 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     const int k0 = PT_K * j;
     char *sk = ring + j % S * R::BYTES, *sv = sk + S * R::BYTES;
     const int below = place + 1 - k0, above = sc.window > 0 ? below - sc.window : 0;
-    if (t0 != t1 && (k0 + PT_K - 1 > before + t0 || (sc.window > 0 && k0 <= before + t1 - sc.window)) && wild<T, D>(sv)) {
-      add_wild(sum, sv, above, below);
+    if (t0 != t1 && at_edge(task, sc.window, j) && wild<T, D>(sv)) {
       tame<T, D>(sv);
+      odd = true;
     }
     if (!live || k0 > most || (sc.window > 0 && k0 + PT_K - 1 <= least - sc.window)) return;
     sum.scores(sk, qf, rd, s);
@@ -388,37 +708,36 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     }
     bits = 15;
   }
-  if (n == 1) {
-    if (live) sum.store(out + (pc.s.first + t) * out_token + head * out_head, row < end, nchunk);
-    return;
-  }
-  // 64 dims at a time through LDS, so that rows are written whole
   arrive<0>();
-  const int slot = (pc.slot + pc.share * pc.s.tiles) ;
-  if (!live || slot >= ch.slots) return;
-  float* own = reinterpret_cast<float*>(ring) + w * 32 * 68;
-  const int64_t sums = ((int64_t)slot * ch.kv_heads + g) * ch.rows + 32 * w;
-  const int left = end - row0;
+  if (task.shares == 1) {
+    if (live) sum.store(out + (task.token + t) * out_token + head * out_head, row < end, nchunk);
+  } else if (live) {
+    // 64 dims at a time through LDS, so that rows are written whole
+    float* own = reinterpret_cast<float*>(ring) + w * 32 * 68;
+    const int64_t sums = ((int64_t)task.slot * ch.kv_heads + task.g) * ch.rows + 32 * w;
+    const int left = end - row0;
 #pragma unroll
-  for (int d0 = 0; d0 < L::DT; d0 += 2) {
+    for (int d0 = 0; d0 < L::DT; d0 += 2) {
 #pragma unroll
-    for (int d = d0; d < min(d0 + 2, L::DT); ++d)
+      for (int d = d0; d < min(d0 + 2, L::DT); ++d)
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<f4*>(own + (lane & 31) * 68 + 32 * (d - d0) + 8 * (i / 4) + 4 * hi) =
-            f4{sum.o[d][i], sum.o[d][i + 1], sum.o[d][i + 2], sum.o[d][i + 3]};
-    __builtin_amdgcn_wave_barrier();
-    const int d = 32 * d0 + 4 * (lane & 15);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int x = 4 * i + lane / 16;
-      const f4 y = *reinterpret_cast<const f4*>(own + x * 68 + 4 * (lane & 15));
-      if (x < left && d < ch.dim && 4 * (lane & 15) < 32 * (L::DT - d0)) *reinterpret_cast<f4*>(part + (sums + x) * ch.dim + d) = y;
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f4*>(own + (lane & 31) * 68 + 32 * (d - d0) + 8 * (i / 4) + 4 * hi) =
+              f4{sum.o[d][i], sum.o[d][i + 1], sum.o[d][i + 2], sum.o[d][i + 3]};
+      __builtin_amdgcn_wave_barrier();
+      const int d = 32 * d0 + 4 * (lane & 15);
+      const bool there = d < ch.dim && 4 * (lane & 15) < 32 * (L::DT - d0);
+#pragma unroll 2
+      for (int x = lane / 16; x < min(left, 32); x += 4) {
+        const f4 y = *reinterpret_cast<const f4*>(own + x * 68 + 4 * (lane & 15));
+        if (there) *reinterpret_cast<f4*>(part + (sums + x) * ch.dim + d) = y;
+      }
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
+    const float l = sum32(sum.l);
+    if (hi == 0 && lane < left) *reinterpret_cast<float2*>(stat + 2 * (sums + lane)) = float2{sum.mc, l};
   }
-  const float l = sum32(sum.l);
-  if (hi == 0 && lane < left) *reinterpret_cast<float2*>(stat + 2 * (sums + lane)) = float2{sum.mc, l};
+  if (odd) add_wild<T>(pg, ch, sc.window, task, out, out_token, out_head, part);
 }
 
 // Join the shares of a row: a wave each, all lanes on a share's dims.
