@@ -105,28 +105,30 @@ template <int N> __device__ __forceinline__ void arrive() {
 // the remaining row numbers are multiples of 16 rows that go into the instructions' offsets.
 template <int D> struct Reads {
   using L = Tile<D>;
-  uint32_t k[L::KS], v[2][L::DT];
+  // The swizzle leaves bit 4 of a chunk's number alone, so in rows of 32 chunks the second 16 lie 256 bytes on.
+  static constexpr int KN = L::NC == 32 ? L::KS / 2 : L::KS, VN = L::NC == 32 ? L::DT / 2 : L::DT;
+  uint32_t k[KN], v[2][VN];
 
   __device__ __forceinline__ explicit Reads(int lane) {
     const int hi = lane >> 5, col = lane & 31;
 #pragma unroll
-    for (int s = 0; s < L::KS; ++s) k[s] = 16 * L::chunk(col, 2 * s + hi);
+    for (int s = 0; s < KN; ++s) k[s] = 16 * L::chunk(col, 2 * s + hi);
     const int j = lane & 15, cc = 2 * ((lane >> 4) & 1) + ((j & 3) >> 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int t = 0; t < L::DT; ++t) v[e][t] = 16 * L::chunk(8 * e + 4 * hi + (j >> 2), 4 * t + cc) + 8 * (j & 1);
+      for (int t = 0; t < VN; ++t) v[e][t] = 16 * L::chunk(8 * e + 4 * hi + (j >> 2), 4 * t + cc) + 8 * (j & 1);
   }
   // K as A operand: keys 32 h .., dims 16 s ..
   __device__ __forceinline__ u4 kfrag(const char* sk, int h, int s) const {
-    return *reinterpret_cast<const u4*>(sk + k[s] + 32 * 16 * L::NC * h);
+    return *reinterpret_cast<const u4*>(sk + k[s % KN] + 256 * (s / KN) + 32 * 16 * L::NC * h);
   }
   // V^T as A operand, keys 16 step .., dims 32 t ..: transposing reads, each giving a lane 4 keys of one dimension
   __device__ __forceinline__ u4 vfrag(const char* sv, int step, int t) const {
     u4 f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const char* at = sv + v[e][t] + 16 * 16 * L::NC * step;
+      const char* at = sv + v[e][t % VN] + 256 * (t / VN) + 16 * 16 * L::NC * step;
       const u2 x =
           __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)at));
       f[2 * e] = x[0];
@@ -145,8 +147,9 @@ template <int D, int S, int NT> struct Ring {
   static constexpr int NV = RN < 16 ? 16 / RN : 1;              // such loads until the swizzle repeats
 };
 
-// A wave's sums for 32 queries: o, l, and the reference point mc of the exponents (c times a score, or -inf).
-template <class T, int D> struct Sums {
+// A wave's sums for 32 queries: o, l, and the reference point mc of the exponents (c times a score, or -inf).  It takes H
+// times 32 keys of a tile.
+template <class T, int D, int H = 2> struct Sums {
   using L = Tile<D>;
   f16v o[L::DT];
   float mc, l;
@@ -157,10 +160,10 @@ template <class T, int D> struct Sums {
     mc = NEG_INF, l = 0.f;
   }
 
-  // Scores of one tile of 64 keys in LDS: register i of s[h] is key 32 h + 8 (i / 4) + 4 (lane / 32) + i % 4.
+  // Scores of a tile's keys in LDS: register i of s[h] is key 32 h + 8 (i / 4) + 4 (lane / 32) + i % 4.
   static __device__ __forceinline__ void scores(const char* sk, const u4* qf, const Reads<D>& rd, f16v* s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < H; ++h) {
       s[h] = (f16v)(0.f);
 #pragma unroll
       for (int ks = 0; ks < L::KS; ++ks) s[h] = T::mma32(rd.kfrag(sk, h, ks), qf[ks], s[h]);
@@ -181,11 +184,11 @@ template <class T, int D> struct Sums {
   __device__ __forceinline__ void weigh(const f16v* s, float c, uint32_t* pw) {
     // rows whose scores so far are all -inf keep mc = -inf; 0 stands in for it in the differences
     const float base = mc == NEG_INF ? 0.f : mc;
-    float x[32], top = NEG_INF;
+    float x[16 * H], top = NEG_INF;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = fmaf(s[i / 16][i % 16], c, -base);
+    for (int i = 0; i < 16 * H; ++i) x[i] = fmaf(s[i / 16][i % 16], c, -base);
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
+    for (int i = 0; i < 16 * H; i += 2) top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
     top = max32(top);
     // mc may lag behind the largest score by LAG more than LOW, so that o is seldom multiplied.  (binary16, 8192 tokens of
     // 56 heads of 128, scores of deviation 1 and 3: LAG 2 1001 and 1039 us, 4 991 and 1022, 8 991 and 1005.)
@@ -202,11 +205,11 @@ template <class T, int D> struct Sums {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[t][i] *= alpha;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] -= up;
+      for (int i = 0; i < 16 * H; ++i) x[i] -= up;
     }
     float ls = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
+    for (int i = 0; i < 16 * H; i += 2) {
       const float a = exp2_fast(x[i]), b = exp2_fast(x[i + 1]);
       ls += a;
       ls += b;
@@ -217,7 +220,7 @@ template <class T, int D> struct Sums {
 
   __device__ __forceinline__ void add(const char* sv, const uint32_t* pw, const Reads<D>& rd) {
 #pragma unroll
-    for (int st = 0; st < 4; ++st)
+    for (int st = 0; st < 2 * H; ++st)
 #pragma unroll
       for (int t = 0; t < L::DT; ++t)
         o[t] = T::mma32(rd.vfrag(sv, st, t), u4{pw[4 * st], pw[4 * st + 1], pw[4 * st + 2], pw[4 * st + 3]}, o[t]);

@@ -32,11 +32,12 @@ Cut cut_of(const pi_cache* c, int tokens, int heads, int few) {
   return u;
 }
 
-// Which kernel takes a call: that for few rows where the chunks' rows of a key head are up to 48 on the average (32 for wide
-// heads).  A chunk that has more of them, or fewer, is in good hands all the same: only its time hangs on this.
+// Which kernel takes a call: that for few rows where the chunks' rows of a key head are up to 32 on the average.  A chunk that
+// has more of them, or fewer, comes out the same: only its time hangs on this.  (16 chunks behind up to 4000 tokens, 64 heads
+// on 8, 128 wide: 16, 32, 40 and 56 rows a chunk 46, 50, 65 and - us with k_chunk_few, 57, 57, 50 and 50 with k_attn_chunk.)
 int few_of(const pi_cache* c, int tokens, int heads, int n) {
   const int64_t rows = up_div(tokens, std::max(1, std::min(n, tokens))) * (heads / c->kv_heads);
-  return rows > (c->dim > 128 ? 32 : 48) ? 0 : (int)up_div(rows, 16);
+  return rows > 32 ? 0 : (int)up_div(rows, 16);
 }
 
 struct Ws {
@@ -54,7 +55,7 @@ Ws ws_of(const pi_cache* c, const Cut& u) {
 // Of all ways a call with so many rows may go, so that room for more rows is room for fewer.
 size_t ws_bytes_of(const pi_cache* c, int tokens, int heads) {
   size_t most = 0;
-  for (int few = 0; few <= 3; ++few) most = std::max(most, ws_of(c, cut_of(c, tokens, heads, few)).total);
+  for (int few = 0; few <= 2; ++few) most = std::max(most, ws_of(c, cut_of(c, tokens, heads, few)).total);
   return most;
 }
 
@@ -127,7 +128,7 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
     with_type(cache->dtype, cache->dim, [&](auto t, auto d) {
       using T = decltype(t);
       constexpr int D = decltype(d)::value;
-      pia::with_mod(call.mod, [&](auto m) { pia::launch(pia::k_attn_chunk<T, D, decltype(m)::value>, call); });
+      pia::with_mod(call.mod, [&](auto m) { pia::launch(pia::k_attn_chunk<T, D, decltype(m)::value>, call, pia::ch_waves<D>()); });
     });
   }
   auto join = [&](auto t) {

@@ -149,11 +149,11 @@ __device__ __forceinline__ int entry(const int32_t* table, int at) {
 }
 
 // A tile's scores as the softmax takes them, in units of log2(e).  `back` is the tile's first key minus the row's place.
-template <int MOD>
+template <int MOD, int H>
 __device__ __forceinline__ void change(f16v* s, const ChunkScore& sc, float slope, int back) {
   const float at = slope * (float)(back + 4 * (int)((threadIdx.x & 63) >> 5));
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x;
@@ -189,10 +189,11 @@ __device__ __forceinline__ void change16(f4* s, const ChunkScore& sc, float slop
 }
 
 // Scores of keys that a row does not see: it sees those from `lo` on and before `hi` in the places of 16 that `bits` names.
+template <int H>
 __device__ __forceinline__ void hide(f16v* s, int lo, int hi, uint32_t bits) {
   const int half = 4 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < H; ++h)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int key = 32 * h + 8 * (i / 4) + i % 4;
@@ -325,10 +326,8 @@ __global__ void __launch_bounds__(4 * WAVE, D > 128 ? 1 : D <= 64 || MT == 1 ? 3
 k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
             Joint* __restrict__ joints, int32_t* __restrict__ count, float* __restrict__ part, float* __restrict__ stat) {
   using V = Vec<D>;
-  constexpr int NF = V::W * V::G, ROW = 16 * NF + 4, NC = Tile<D>::NC;
-  constexpr bool HELD = MT <= 2;                   // queries stay in registers; else they are read from LDS at each step
-  constexpr int JOIN = 4 * 16 * (ROW + 2) * 4, QUERIES = HELD ? 0 : MT * 16 * NC * 16;
-  __shared__ __attribute__((aligned(16))) char lds[JOIN + QUERIES];
+  constexpr int NF = V::W * V::G, ROW = 16 * NF + 4;
+  __shared__ __attribute__((aligned(16))) float so[4 * 16 * ROW], sm[4 * 16 * 2];
   const Task k = find_task(pg, ch, sc.window, joints, count);
   if (k.rows == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -336,8 +335,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 
   int place[MT];
   float slope[MT];
-  u4 qf[HELD ? MT : 1][V::KS];
-  char* held = lds + JOIN;
+  u4 qf[MT][V::KS];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = k.row0 + min(16 * m + r, k.rows - 1), t = row / group, head = k.g * group + row % group;
@@ -347,12 +345,9 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 #pragma unroll
     for (int s = 0; s < V::KS; ++s) {
       const int c = 4 * s + kg;
-      const u4 x = c < nchunk ? *reinterpret_cast<const u4*>(src + 8 * c) : u4{0, 0, 0, 0};
-      if constexpr (HELD) qf[m][s] = x;
-      else if (w == 0) *reinterpret_cast<u4*>(held + 16 * ((16 * m + r) * NC + (c ^ (r % NC)))) = x;
+      qf[m][s] = c < nchunk ? *reinterpret_cast<const u4*>(src + 8 * c) : u4{0, 0, 0, 0};
     }
   }
-  if constexpr (!HELD) __syncthreads();
   f4 o[MT][NF];
   float mc[MT], l[MT];                             // mc: HIGH under c times the largest score so far
 #pragma unroll
@@ -425,12 +420,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
       for (int h = 0; h < 2; ++h) {
         s[h] = (f4)(0.f);
 #pragma unroll
-        for (int ks = 0; ks < V::KS; ++ks) {
-          u4 b;
-          if constexpr (HELD) b = qf[m][ks];
-          else b = *reinterpret_cast<const u4*>(held + 16 * ((16 * m + r) * NC + ((4 * ks + kg) ^ (r % NC))));
-          s[h] = T::mma16(kf[h][ks], b, s[h]);
-        }
+        for (int ks = 0; ks < V::KS; ++ks) s[h] = T::mma16(kf[h][ks], qf[m][ks], s[h]);
       }
       if constexpr (MOD != 0) change16<MOD>(s, sc, slope[m], k0 - place[m]);
       if (some) {
@@ -505,8 +495,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
   }
 
   // join the waves, 16 rows at a time: o[m][f][i] belongs to dim (16 gr + 4 kg + i) W + f % W of row 16 m + r
-  float* so = reinterpret_cast<float*>(lds);       // [4][16][ROW], then (reference point, l) [4][16][2]
-  float* sm = so + 4 * 16 * ROW;
+  // of wave w's in so [4][16][ROW], (reference point, l) in sm [4][16][2]
   const int64_t sums = ((int64_t)k.slot * ch.kv_heads + k.g) * ch.rows;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -550,16 +539,19 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
   if (k.t0 != k.t1 && __syncthreads_or(odd)) add_wild<T>(pg, ch, sc.window, k, out, out_token, out_head, part);
 }
 
-// One block of 4 waves: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in
-// tiles of 64 from the last one down, which go to LDS past the registers one tile ahead of the products.
+// One block: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in tiles of 64 from
+// the last one down, which go to LDS past the registers one tile ahead of the products.  Four waves; for heads wider than 128,
+// whose sums and tiles leave room for no second block, eight, of which two take half of a tile's keys each for the same rows.
+template <int D> constexpr int ch_waves() { return D > 128 ? 8 : 4; }
 template <class T, int D, int MOD>
-__global__ void __launch_bounds__(4 * WAVE, D <= 64 ? 4 : D <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(ch_waves<D>() * WAVE, D <= 64 ? 4 : D <= 128 ? 2 : 1)
 k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
              Joint* __restrict__ joints, int32_t* __restrict__ count, float* __restrict__ part, float* __restrict__ stat) {
   using L = Tile<D>;
-  constexpr int NT = 4 * WAVE, S = 2;
+  constexpr int NT = ch_waves<D>() * WAVE, S = 2, KW = ch_waves<D>() / 4, H = 2 / KW;
   using R = Ring<D, S, NT>;
   constexpr int SUMS = D <= 64 ? 4 * 32 * 68 * 4 : 0;   // sums on their way out, which take more than small tiles do
+  __shared__ float2 stats[KW > 1 ? NT / 2 : 1];
   __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES > SUMS ? 2 * S * R::BYTES : SUMS];   // K tiles, then V tiles
 
   const Task task = find_task(pg, ch, sc.window, joints, count);
@@ -568,7 +560,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   const int group = ch.heads / ch.kv_heads, nchunk = ch.dim / 8;
   const int first = task.first, last = task.last, from = task.from, to = task.to, before = task.before, t0 = task.t0, t1 = task.t1;
 
-  const int row0 = task.row0 + 32 * w, row = row0 + (lane & 31), end = task.row0 + task.rows;
+  const int half = w / 4, row0 = task.row0 + 32 * (w % 4), row = row0 + (lane & 31), end = task.row0 + task.rows;
   const bool live = row0 < end;
   const int mine = min(row, end - 1), t = mine / group, head = task.g * group + mine % group;
   const int place = before + t;                    // the row sees keys up to here
@@ -596,39 +588,43 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   auto place_at = [&](int x, int id) {
     return uniform((int64_t)((uint64_t)(uint32_t)id * page_bytes + (uint32_t)(x - page_of(ch, x) * (pg.page / 16)) * (uint32_t)(32 * ch.dim)));
   };
-  // A wave loads one place of a tile, LW times 1024 bytes.  What a lane takes of it is the chunk that its place in LDS asks for.
+  // A wave loads one place of a tile, LW times 1024 bytes (of eight waves four the keys and four the values).  What a lane takes
+  // of it is the chunk that its place in LDS asks for.
   constexpr int LW = L::NC / 4, RL = 64 / L::NC;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * LW * w;
+  const bool keys = KW == 1 || half == 0, values = KW == 1 || half == 1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring + 1024 * LW * (w % 4);
   uint32_t off[LW];
 #pragma unroll
   for (int i = 0; i < LW; ++i) {
     const int r = i * RL + lane / L::NC, c = (lane % L::NC) ^ L::swz(r);
     off[i] = c < nchunk ? 2 * (uint32_t)(r * ch.dim + 8 * c) : ~0u;
   }
-  auto look_up = [&](int j) { return entry(table, page_of(ch, 4 * j + w)); };
+  auto look_up = [&](int j) { return entry(table, page_of(ch, 4 * j + w % 4)); };
   // a tile that is whole: every place is there, and some row sees every key
   auto fetch = [&](int j, int id) {
-    const int64_t at = place_at(4 * j + w, id);
+    const int64_t at = place_at(4 * j + w % 4, id);
     const char *ka = kg + at, *va = vg + at;
     const uint32_t dst = lds0 + j % S * R::BYTES;
     if (nchunk == L::NC) {
+      if (keys)
 #pragma unroll
-      for (int i = 0; i < LW; ++i) to_lds(ka, off[i], dst + 1024 * i);
+        for (int i = 0; i < LW; ++i) to_lds(ka, off[i], dst + 1024 * i);
+      if (values)
 #pragma unroll
-      for (int i = 0; i < LW; ++i) to_lds(va, off[i], dst + S * R::BYTES + 1024 * i);
+        for (int i = 0; i < LW; ++i) to_lds(va, off[i], dst + S * R::BYTES + 1024 * i);
     } else {
 #pragma unroll
       for (int i = 0; i < LW; ++i)
         if (off[i] != ~0u) {
-          to_lds(ka, off[i], dst + 1024 * i);
-          to_lds(va, off[i], dst + S * R::BYTES + 1024 * i);
+          if (keys) to_lds(ka, off[i], dst + 1024 * i);
+          if (values) to_lds(va, off[i], dst + S * R::BYTES + 1024 * i);
         }
     }
   };
   // Any tile; keys that no row sees are zeros: with anything else there, 0 times an infinity would be NaN.  Which places
   // there are.
   auto fetch_part = [&](int j) {
-    const int x = 4 * j + w;
+    const int x = 4 * j + w % 4;
     const bool inside = 16 * x < to && 16 * x + 16 > from;
     const int id = inside ? usable_page(entry(table, page_of(ch, x)), pg.pages) : -1;
     const int64_t at = place_at(x, max(id, 0));
@@ -638,12 +634,13 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
       const int key = 16 * x + i * RL + lane / L::NC;
       if (id >= 0 && key < to && key >= from) {
         if (off[i] != ~0u) {
-          to_lds(kg + at, off[i], dst + 1024 * i);
-          to_lds(vg + at, off[i], dst + S * R::BYTES + 1024 * i);
+          if (keys) to_lds(kg + at, off[i], dst + 1024 * i);
+          if (values) to_lds(vg + at, off[i], dst + S * R::BYTES + 1024 * i);
         }
       } else {
-        char* own = ring + j % S * R::BYTES + 1024 * (LW * w + i) + 16 * lane;
-        *reinterpret_cast<u4*>(own) = *reinterpret_cast<u4*>(own + S * R::BYTES) = u4{0, 0, 0, 0};
+        char* own = ring + j % S * R::BYTES + 1024 * (LW * (w % 4) + i) + 16 * lane;
+        if (keys) *reinterpret_cast<u4*>(own) = u4{0, 0, 0, 0};
+        if (values) *reinterpret_cast<u4*>(own + S * R::BYTES) = u4{0, 0, 0, 0};
       }
     }
     uint32_t bits = 0;
@@ -657,10 +654,10 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     return bits;
   };
   const Reads<D> rd(lane);
-  Sums<T, D> sum;
+  Sums<T, D, H> sum;
   sum.clear();
-  f16v s[2];
-  uint32_t pw[16];
+  f16v s[H];
+  uint32_t pw[8 * H];
   bool odd = false;                                // whether there were values that are not finite
   uint32_t bits = 0;
   if (first <= last) bits = fetch_part(last);
@@ -672,6 +669,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     for (int e = page_of(ch, 4 * lower) + tid, end = page_of(ch, 4 * last); e <= end; e += NT) broken |= usable_page(table[e], pg.pages) < 0;
     if (__syncthreads_or(broken)) upper = lower - 1;
   }
+  const int mine_at = KW > 1 ? 32 * 16 * L::NC * half : 0;        // the wave's part of a tile in LDS
   // one tile of any kind, which lies in LDS; `there`: its places
   auto take = [&](int j, uint32_t there) {
     const int k0 = PT_K * j;
@@ -682,11 +680,12 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
       odd = true;
     }
     if (!live || k0 > most || (sc.window > 0 && k0 + PT_K - 1 <= least - sc.window)) return;
-    sum.scores(sk, qf, rd, s);
-    if constexpr (MOD != 0) change<MOD>(s, sc, slope, k0 - place);
-    if (there != 15 || k0 + PT_K - 1 > least || (sc.window > 0 && k0 <= most - sc.window)) hide(s, above, below, there);
+    sum.scores(sk + mine_at, qf, rd, s);
+    if constexpr (MOD != 0) change<MOD, H>(s, sc, slope, k0 + 32 * H * half - place);
+    if (there != 15 || k0 + PT_K - 1 > least || (sc.window > 0 && k0 <= most - sc.window))
+      hide<H>(s, above - 32 * H * half, below - 32 * H * half, there >> 2 * H * half);
     sum.weigh(s, MOD ? 1.f : sc.c, pw);
-    sum.add(sv, pw, rd);
+    sum.add(sv + mine_at, pw, rd);
   };
   for (int j = last; j >= first;) {
     arrive<0>();
@@ -700,18 +699,46 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
       fetch(j - 1, id);
       id = look_up(max(j - 2, lower));
       if (live) {
-        sum.scores(ring + j % S * R::BYTES, qf, rd, s);
-        if constexpr (MOD != 0) change<MOD>(s, sc, slope, PT_K * j - place);
+        sum.scores(ring + j % S * R::BYTES + mine_at, qf, rd, s);
+        if constexpr (MOD != 0) change<MOD, H>(s, sc, slope, PT_K * j + 32 * H * half - place);
         sum.weigh(s, MOD ? 1.f : sc.c, pw);
-        sum.add(ring + (S + j % S) * R::BYTES, pw, rd);
+        sum.add(ring + (S + j % S) * R::BYTES + mine_at, pw, rd);
       }
     }
     bits = 15;
   }
   arrive<0>();
+  if constexpr (KW > 1) {                          // the second half's sums go through LDS, lane by lane
+    f4* theirs = reinterpret_cast<f4*>(ring) + (w % 4) * 64 * 4 * L::DT + lane;
+    if (half == 1) {
+#pragma unroll
+      for (int d = 0; d < L::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          theirs[64 * (4 * d + i)] = f4{sum.o[d][4 * i], sum.o[d][4 * i + 1], sum.o[d][4 * i + 2], sum.o[d][4 * i + 3]};
+      stats[tid % (NT / 2)] = float2{sum.mc, sum.l};
+    }
+    __syncthreads();
+    if (half == 0) {
+      const float2 st = stats[tid];
+      const float top = fmaxf(sum.mc, st.x), base = top == NEG_INF ? 0.f : top;
+      const float a = exp2_fast(sum.mc - base), b = exp2_fast(st.x - base);
+      sum.mc = top, sum.l = fmaf(st.y, b, sum.l * a);
+#pragma unroll
+      for (int d = 0; d < L::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f4 y = theirs[64 * (4 * d + i)];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum.o[d][4 * i + e] = fmaf(y[e], b, sum.o[d][4 * i + e] * a);
+        }
+    }
+    __syncthreads();
+  }
+  const bool writes = live && half == 0;
   if (task.shares == 1) {
-    if (live) sum.store(out + (task.token + t) * out_token + head * out_head, row < end, nchunk);
-  } else if (live) {
+    if (writes) sum.store(out + (task.token + t) * out_token + head * out_head, row < end, nchunk);
+  } else if (writes) {
     // 64 dims at a time through LDS, so that rows are written whole
     float* own = reinterpret_cast<float*>(ring) + w * 32 * 68;
     const int64_t sums = ((int64_t)task.slot * ch.kv_heads + task.g) * ch.rows + 32 * w;

@@ -9,8 +9,7 @@ void pia::launch_few(int dtype, const ChunkCall& c) {
     with_mod(c.mod, [&](auto m) {
       constexpr int MOD = decltype(m)::value;
       if (c.few == 1) launch(k_chunk_few<T, D, MOD, 1>, c);
-      else if (c.few == 2) launch(k_chunk_few<T, D, MOD, 2>, c);
-      else if constexpr (D <= 128) launch(k_chunk_few<T, D, MOD, 3>, c);
+      else launch(k_chunk_few<T, D, MOD, 2>, c);
     });
   });
 }

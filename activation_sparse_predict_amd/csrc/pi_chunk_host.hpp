@@ -20,8 +20,8 @@ struct ChunkCall {
   hipStream_t stream;
 };
 
-template <class K> void launch(K kernel, const ChunkCall& c) {
-  hipLaunchKernelGGL(kernel, dim3(c.blocks), dim3(256), 0, c.stream, c.pg, c.q, c.out, c.out_token, c.out_head, c.ch, c.sc,
+template <class K> void launch(K kernel, const ChunkCall& c, int waves = 4) {
+  hipLaunchKernelGGL(kernel, dim3(c.blocks), dim3(waves * WAVE), 0, c.stream, c.pg, c.q, c.out, c.out_token, c.out_head, c.ch, c.sc,
                      c.joints, c.count, c.part, c.stat);
 }
 
