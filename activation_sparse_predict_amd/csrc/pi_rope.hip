@@ -43,36 +43,41 @@ pir::Part part_of(const pi_heads* x, const pi_heads* out, int32_t heads, const f
   return p;
 }
 
-// rows: heads of a token that are moved, those of v among them
 pi_status launch(bool paged, int dtype, const pi_rope* r, const pir::Part& q, const pir::Part& k, const pir::Part& v,
-                 int rows, const int32_t* pos, const pic::Meta& m, const int32_t* cu, const int32_t* seqs, int n,
+                 const int32_t* pos, const pic::Meta& m, const int32_t* cu, const int32_t* seqs, int n,
                  int tokens, int dim, float eps, void* stream) {
   const int rotary = r ? r->rotary : 0;
   const int mode = !r ? pir::NONE : r->layout == PI_ROPE_PAIRS ? pir::PAIRS : rotary % 16 == 0 ? pir::HALF : pir::ODD;
   const int lanes = mode == pir::ODD ? (int)(up_div(rotary / 2, 8) + up_div(dim - rotary, 16)) : (int)up_div(dim, 16);
   int shift = 0;
   while (1 << shift < lanes) ++shift;
-  const int turns = (int)up_div(rows, 64 >> shift);             // of a wave for all heads of a token
-  // more waves than the card holds at once share a token's angles among more heads
-  const int64_t most = std::max<int64_t>(1, (int64_t)tokens * turns / 8192);
-  int waves = (int)up_div(turns, std::min<int64_t>(turns, most));
-  const int its = (int)up_div(turns, waves);
-  waves = (int)up_div(turns, its);
+  const int per = 64 >> shift;                                  // heads of a wave's turn, all of one kind
+  const int turns = (int)(up_div(q.heads, per) + up_div(k.heads, per) + up_div(v.heads, per));
+  // waves that the card does not hold at once anyway make the angles for several turns
+  const int64_t all = (int64_t)tokens * turns;
+  const int its = all >= 16384 && turns > 2 ? 4 : all >= 8192 && turns > 1 ? 2 : 1;
+  const int waves = (int)up_div(turns, its);
   const int64_t blocks = up_div((int64_t)tokens * waves, 4);
   if (blocks > INT32_MAX) return PI_EUNSUPPORTED;
   const pir::Turn turn{r ? r->steps : nullptr, rotary, !r || r->magnitude == 0.f ? 1.f : r->magnitude};
   (void)hipGetLastError();
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), 0, static_cast<hipStream_t>(stream), turn, q, k, v,
-                       pos, m, cu, seqs, n, tokens, dim, eps, shift, its, waves);
+                       pos, m, cu, seqs, n, tokens, dim, eps, shift, waves);
+  };
+  auto with_its = [&](auto t, auto m, auto p) {
+    using T = decltype(t);
+    constexpr int M = decltype(m)::value;
+    constexpr bool P = decltype(p)::value;
+    if (its == 1) go(pir::k_rope<T, M, P, 1>);
+    else if (its == 2) go(pir::k_rope<T, M, P, 2>);
+    else go(pir::k_rope<T, M, P, 4>);
   };
   auto with_mode = [&](auto t, auto p) {
-    using T = decltype(t);
-    constexpr bool P = decltype(p)::value;
-    if (mode == pir::NONE) go(pir::k_rope<T, pir::NONE, P>);
-    else if (mode == pir::HALF) go(pir::k_rope<T, pir::HALF, P>);
-    else if (mode == pir::PAIRS) go(pir::k_rope<T, pir::PAIRS, P>);
-    else go(pir::k_rope<T, pir::ODD, P>);
+    if (mode == pir::NONE) with_its(t, std::integral_constant<int, pir::NONE>(), p);
+    else if (mode == pir::HALF) with_its(t, std::integral_constant<int, pir::HALF>(), p);
+    else if (mode == pir::PAIRS) with_its(t, std::integral_constant<int, pir::PAIRS>(), p);
+    else with_its(t, std::integral_constant<int, pir::ODD>(), p);
   };
   auto with_pages = [&](auto t) {
     if (paged) with_mode(t, std::true_type());
@@ -145,7 +150,7 @@ pi_status pi_rope_heads(const pi_rope* rope, const int32_t* pos, const pi_heads*
   if ((s = check_part(k, k_out, kv_heads, tokens, dim)) != PI_OK) return s;
   if (tokens == 0) return PI_OK;
   return launch(false, dtype, rope, part_of(q, q_out, heads, q_norm), part_of(k, k_out, kv_heads, k_norm), pir::Part{},
-                heads + kv_heads, pos, pic::Meta{}, nullptr, nullptr, 0, tokens, dim, eps, stream);
+                pos, pic::Meta{}, nullptr, nullptr, 0, tokens, dim, eps, stream);
 }
 
 pi_status pi_cache_append_rope(const pi_cache* c, int32_t layer, const pi_rope* rope, const pi_heads* q,
@@ -164,7 +169,7 @@ pi_status pi_cache_append_rope(const pi_cache* c, int32_t layer, const pi_rope* 
   pir::Part kp = part_of(k, nullptr, c->kv_heads, k_norm), vp = part_of(v, nullptr, c->kv_heads, nullptr);
   kp.dst = static_cast<uint16_t*>(c->k) + at;
   vp.dst = static_cast<uint16_t*>(c->v) + at;
-  return launch(true, c->dtype, rope, part_of(q, q_out, heads, q_norm), kp, vp, heads + 2 * c->kv_heads, nullptr,
+  return launch(true, c->dtype, rope, part_of(q, q_out, heads, q_norm), kp, vp, nullptr,
                 pic::meta_of(c), cu, seqs, n, tokens, c->dim, eps, stream);
 }
 

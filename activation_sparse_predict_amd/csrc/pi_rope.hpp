@@ -94,20 +94,62 @@ template <int MODE> __device__ __forceinline__ Dims dims_of(int l, int dim, int 
   }
 }
 
-// A wave takes one token and `its` times 64 / P of its heads, P = 2^shift lanes a head
-// (those of q, then of k, then of v, which is copied).  The angles are made once for all of them.
-template <class T, int MODE, bool PAGED>
+// A wave takes one token and up to ITS turns, each of 64 / P heads of one kind, P = 2^shift lanes a head: those of q, then of
+// k, then of v, which is copied.  All it loads is asked for before anything else, without conditions, and no load follows a
+// store: the counter that a wave waits on counts both, in order.  The angles are made once for all turns.
+template <class T, int MODE, bool PAGED, int ITS>
 __global__ void __launch_bounds__(256)
 k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::Meta m,
        const int32_t* __restrict__ cu, const int32_t* __restrict__ seqs, int n, int tokens, int dim, float eps, int shift,
-       int its, int waves) {
+       int waves) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t job = (int64_t)blockIdx.x * 4 + w;
   const int t = (int)(job / waves), part = (int)(job % waves);
   if (t >= tokens) return;
+  const int l = lane & ((1 << shift) - 1), mine = lane >> shift, per = 64 >> shift;
+  const Dims d = dims_of<MODE>(l, dim, turn.rotary);
+  const int q_turns = (q.heads + per - 1) / per, k_turns = (k.heads + per - 1) / per;
+  const int begin = part * ITS, end = min(begin + ITS, q_turns + (PAGED ? 2 : 1) * k_turns);
+
+  // a turn's heads: kind 0 q, 1 k, 2 v, from the first one on
+  struct Heads {
+    int kind, first;
+  };
+  auto heads_of = [&](int it) {
+    if (it < q_turns) return Heads{0, it * per};
+    it -= q_turns;
+    return it < k_turns ? Heads{1, it * per} : Heads{2, (it - k_turns) * per};
+  };
+  u4 ra[ITS], rb[ITS];
+#pragma unroll
+  for (int i = 0; i < ITS; ++i) {                  // those that are not there are others again
+    const Heads h = heads_of(min(begin + i, end - 1));
+    const Part& x = h.kind == 0 ? q : h.kind == 1 ? k : v;
+    const uint16_t* src = x.src + t * x.src_token + min(h.first + mine, x.heads - 1) * x.src_head;
+    if constexpr (MODE == ODD) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a0 = src[min(d.a + 2 * e, dim - 1)], a1 = src[min(d.a + 2 * e + 1, dim - 1)];
+        const uint32_t b0 = src[min(d.b + 2 * e, dim - 1)], b1 = src[min(d.b + 2 * e + 1, dim - 1)];
+        ra[i][e] = (2 * e < d.na ? a0 : 0) | (2 * e + 1 < d.na ? a1 << 16 : 0);
+        rb[i][e] = (2 * e < d.nb ? b0 : 0) | (2 * e + 1 < d.nb ? b1 << 16 : 0);
+      }
+    } else {
+      ra[i] = *reinterpret_cast<const u4*>(src + min(d.a, dim - 8));
+      rb[i] = *reinterpret_cast<const u4*>(src + min(d.b, dim - 8));
+    }
+  }
+  float qn[16], kn[16];
+  auto weights = [&](const float* from, float* n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n[e] = from[min(d.a + e, dim - 1)], n[8 + e] = from[min(d.b + e, dim - 1)];
+  };
+  if (q.weight && begin < q_turns) weights(q.weight, qn);
+  if (k.weight && end > q_turns) weights(k.weight, kn);
+
   int at = 0;                                      // the token's position
   bool paged = true;
-  int64_t page_at = 0, head_at = 0;                // of the cache's page and heads, in elements
+  int64_t page_at = 0;                             // of the cache's page and token, in elements
   if constexpr (PAGED) {
     if (t < cu[0]) return;
     const int i = find_seq(cu, n, t);
@@ -124,7 +166,7 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
         at = (int)p;
         const int id = m.table[(int64_t)slot * m.max_pages + at / m.page];
         if ((unsigned)id >= (unsigned)m.pages) bad = PI_CACHE_EPAGE, paged = false;
-        else page_at = ((int64_t)id * k.heads * m.page + at % m.page) * dim, head_at = (int64_t)m.page * dim;
+        else page_at = ((int64_t)id * k.heads * m.page + at % m.page) * dim;
       }
     }
     if (bad && lane == 0) atomicOr(&m.words[1], bad);
@@ -132,8 +174,6 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
   } else if (MODE != NONE) {
     at = pos[t];
   }
-  const int l = lane & ((1 << shift) - 1), per = 64 >> shift;
-  const Dims d = dims_of<MODE>(l, dim, turn.rotary);
   float cs[8], sn[8];
   if constexpr (MODE != NONE) {
     const int first = d.turns ? 8 * l : 0, pairs = turn.rotary / 2;
@@ -143,100 +183,64 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
       sincos_turns((uint32_t)(((uint64_t)(int64_t)at * step) >> 32), turn.magnitude, &cs[e], &sn[e]);
     }
   }
-  const int all = q.heads + k.heads + (PAGED ? k.heads : 0);
   const float over = 1.f / (float)dim;
-
-  struct Row {
-    u4 a, b;
-    int kind, head;                                // 0 q, 1 k, 2 v, 3 none
-  };
-  auto source = [&](int kind, int head) {
-    const Part& x = kind == 0 ? q : kind == 1 ? k : v;
-    return x.src + t * x.src_token + head * x.src_head;
-  };
-  auto load = [&](int it) {
-    Row r;
-    int h = (part * its + it) * per + (lane >> shift);
-    r.kind = h >= all ? 3 : h < q.heads ? 0 : (h -= q.heads) < k.heads ? 1 : (h -= k.heads, 2);
-    if (it >= its) r.kind = 3;
-    if (PAGED && !paged && r.kind > 0) r.kind = 3;
-    r.head = h;
-    r.a = r.b = u4{0, 0, 0, 0};
-    if (r.kind == 3) return r;
-    const uint16_t* src = source(r.kind, h);
-    if constexpr (MODE == ODD) {
-      uint16_t x[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = e < d.na ? src[d.a + e] : 0;
-        x[8 + e] = e < d.nb ? src[d.b + e] : 0;
-      }
+  for (int i = 0; i < ITS; ++i) {
+    if (begin + i >= end) break;
+    const Heads h = heads_of(begin + i);
+    const float* weight = h.kind == 0 ? q.weight : h.kind == 1 ? k.weight : nullptr;
+    u4 ya = ra[i], yb = rb[i];
+    if constexpr (MODE != ODD) {
+      if (d.na == 0) ya = u4{0, 0, 0, 0};
+      if (d.nb == 0) yb = u4{0, 0, 0, 0};
+    }
+    if (h.kind < 2 && (MODE != NONE || weight)) {
+      float x[16];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        r.a[e] = x[2 * e] | (uint32_t)x[2 * e + 1] << 16;
-        r.b[e] = x[8 + 2 * e] | (uint32_t)x[8 + 2 * e + 1] << 16;
+        x[2 * e] = T::low(ya[e]), x[2 * e + 1] = T::high(ya[e]);
+        x[8 + 2 * e] = T::low(yb[e]), x[8 + 2 * e + 1] = T::high(yb[e]);
       }
-    } else {
-      if (d.na > 0) r.a = *reinterpret_cast<const u4*>(src + d.a);
-      if (d.nb > 0) r.b = *reinterpret_cast<const u4*>(src + d.b);
-    }
-    return r;
-  };
-  Row next = load(0);
-  for (int it = 0; it < its; ++it) {
-    const Row r = next;
-    next = load(it + 1);                           // other heads than those written now
-    u4 ya = r.a, yb = r.b;
-    float x[16];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = T::low(r.a[e]), x[2 * e + 1] = T::high(r.a[e]);
-      x[8 + 2 * e] = T::low(r.b[e]), x[8 + 2 * e + 1] = T::high(r.b[e]);
-    }
-    const float* weight = r.kind == 0 ? q.weight : r.kind == 1 ? k.weight : nullptr;
-    if (q.weight || k.weight) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-      for (int o = 1; o < 1 << shift; o *= 2) ss += __shfl_xor(ss, o);
       if (weight) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int o = 1; o < 1 << shift; o *= 2) ss += __shfl_xor(ss, o);
         const float inv = rsqrtf(fmaf(ss, over, eps));
 #pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] *= inv * (h.kind == 0 ? qn[e] : kn[e]);
+      }
+      if constexpr (MODE == HALF || MODE == ODD) {
+        if (d.turns) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = x[e], b = x[8 + e];
+            x[e] = fmaf(a, cs[e], -(b * sn[e]));
+            x[8 + e] = fmaf(b, cs[e], a * sn[e]);
+          }
+        }
+      } else if constexpr (MODE == PAIRS) {
+        const int some = turn.rotary / 2 - 8 * l;  // of the lane's pairs, those that turn
+#pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[e] *= inv * weight[min(d.a + e, dim - 1)];
-          x[8 + e] *= inv * weight[min(d.b + e, dim - 1)];
+          const float a = x[2 * e], b = x[2 * e + 1];
+          x[2 * e] = e < some ? fmaf(a, cs[e], -(b * sn[e])) : a;
+          x[2 * e + 1] = e < some ? fmaf(b, cs[e], a * sn[e]) : b;
+        }
+      }
+      if (d.turns || weight) {                     // all else is moved bit by bit
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ya[e] = T::pack(x[2 * e], x[2 * e + 1]);
+          yb[e] = T::pack(x[8 + 2 * e], x[8 + 2 * e + 1]);
         }
       }
     }
-    if constexpr (MODE == HALF || MODE == ODD) {
-      if (d.turns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = x[e], b = x[8 + e];
-          x[e] = fmaf(a, cs[e], -(b * sn[e]));
-          x[8 + e] = fmaf(b, cs[e], a * sn[e]);
-        }
-      }
-    } else if constexpr (MODE == PAIRS) {
-      const int mine = turn.rotary / 2 - 8 * l;    // of the lane's pairs, those that turn
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = x[2 * e], b = x[2 * e + 1];
-        x[2 * e] = e < mine ? fmaf(a, cs[e], -(b * sn[e])) : a;
-        x[2 * e + 1] = e < mine ? fmaf(b, cs[e], a * sn[e]) : b;
-      }
-    }
-    if (r.kind < 2 && (d.turns || weight)) {       // all else is moved bit by bit
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ya[e] = T::pack(x[2 * e], x[2 * e + 1]);
-        yb[e] = T::pack(x[8 + 2 * e], x[8 + 2 * e + 1]);
-      }
-    }
-    if (r.kind == 3) continue;
-    uint16_t* dst;
-    if (PAGED && r.kind > 0) dst = (r.kind == 1 ? k.dst : v.dst) + page_at + r.head * head_at;
-    else dst = (r.kind == 0 ? q.dst + t * q.dst_token + r.head * q.dst_head : k.dst + t * k.dst_token + r.head * k.dst_head);
+    const Part& y = h.kind == 0 ? q : h.kind == 1 ? k : v;
+    if (h.first + mine >= y.heads || (PAGED && h.kind > 0 && !paged)) continue;
+    const int64_t token = PAGED && h.kind > 0 ? page_at : t * y.dst_token;
+    const int64_t head = PAGED && h.kind > 0 ? (int64_t)m.page * dim : y.dst_head;
+    uint16_t* dst = y.dst + token + h.first * head + mine * head;
     if constexpr (MODE == ODD) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
