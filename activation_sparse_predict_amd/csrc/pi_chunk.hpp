@@ -142,12 +142,6 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)((uint64_t)b << 32 | a);
 }
 
-// A table's entry by a scalar load: the tables do not change while the kernel runs.
-__device__ __forceinline__ int entry(const int32_t* table, int at) {
-  typedef const __attribute__((address_space(4))) int32_t* fixed;
-  return reinterpret_cast<fixed>(reinterpret_cast<uintptr_t>(table))[at];
-}
-
 // A tile's scores as the softmax takes them, in units of log2(e).  `back` is the tile's first key minus the row's place.
 template <int MOD, int H>
 __device__ __forceinline__ void change(f16v* s, const ChunkScore& sc, float slope, int back) {
@@ -371,7 +365,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
       from[h] = max(0, k.from - key), to[h] = min(16, k.to - key);
       int id = 0;
       if (to[h] > from[h]) {
-        const int number = entry(table, page_of(ch, x));
+        const int number = fixed(table, page_of(ch, x));
         id = usable_page(number, pg.pages);
         if (id < 0) {                              // a broken table: its keys are not seen
           if (lane == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
@@ -599,7 +593,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     const int r = i * RL + lane / L::NC, c = (lane % L::NC) ^ L::swz(r);
     off[i] = c < nchunk ? 2 * (uint32_t)(r * ch.dim + 8 * c) : ~0u;
   }
-  auto look_up = [&](int j) { return entry(table, page_of(ch, 4 * j + w % 4)); };
+  auto look_up = [&](int j) { return fixed(table, page_of(ch, 4 * j + w % 4)); };
   // a tile that is whole: every place is there, and some row sees every key
   auto fetch = [&](int j, int id) {
     const int64_t at = place_at(4 * j + w % 4, id);
@@ -626,7 +620,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   auto fetch_part = [&](int j) {
     const int x = 4 * j + w % 4;
     const bool inside = 16 * x < to && 16 * x + 16 > from;
-    const int id = inside ? usable_page(entry(table, page_of(ch, x)), pg.pages) : -1;
+    const int id = inside ? usable_page(fixed(table, page_of(ch, x)), pg.pages) : -1;
     const int64_t at = place_at(x, max(id, 0));
     const uint32_t dst = lds0 + j % S * R::BYTES;
 #pragma unroll
@@ -648,7 +642,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     for (int i = 0; i < 4; ++i) {
       const int y = 4 * j + i;
       if (16 * y >= to || 16 * y + 16 <= from) continue;
-      if (usable_page(entry(table, page_of(ch, y)), pg.pages) >= 0) bits |= 1u << i;
+      if (usable_page(fixed(table, page_of(ch, y)), pg.pages) >= 0) bits |= 1u << i;
       else if (tid == 0) atomicOr(pg.flags, PI_CACHE_EPAGE);
     }
     return bits;

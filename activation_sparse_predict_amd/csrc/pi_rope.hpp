@@ -57,19 +57,28 @@ __device__ __forceinline__ void sincos_turns(uint32_t u, float m, float* c, floa
   *s = (q & 2 ? -y : y) * m;
 }
 
-// The first sequence i whose end cu[i + 1] lies behind token t, by a wave: 64 places at once.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
+// The sequence that holds token t, and its first and last offset: the first i whose end cu[i + 1] lies behind t, by a wave, 64
+// places at once; -1 if there is none.  `ends`: of up to 64 sequences the lane's end, asked for before.
+struct Found {
+  int i, from, to;
+};
+__device__ __forceinline__ Found find_seq(const int32_t* cu, int n, int t, int ends) {
   const int lane = threadIdx.x & (WAVE - 1);
   int lo = 0, len = n;
-  while (true) {
+  while (len > WAVE) {
     const int step = (len + WAVE - 1) / WAVE;
     const uint64_t hit = __ballot(cu[lo + min((lane + 1) * step, len)] > t);
-    if (!hit) return -1;                           // behind the last sequence
+    if (!hit) return Found{-1, 0, 0};
     const int before = (__ffsll((unsigned long long)hit) - 1) * step;
     lo += before;
     len = min(step, len - before);
-    if (step == 1) return lo;
   }
+  if (n > WAVE) ends = cu[lo + min(lane + 1, len)];
+  const uint64_t hit = __ballot(ends > t);
+  if (!hit) return Found{-1, 0, 0};                // behind the last sequence
+  const int l = __ffsll((unsigned long long)hit) - 1;
+  const int from = l > 0 ? __builtin_amdgcn_readlane(ends, l - 1) : fixed(cu, lo);
+  return Found{from <= t ? lo + l : -1, from, __builtin_amdgcn_readlane(ends, l)};
 }
 
 // Dims of a lane: of A from a on (na of them), of B from b on; whether they turn.
@@ -100,11 +109,9 @@ template <int MODE> __device__ __forceinline__ Dims dims_of(int l, int dim, int 
 template <class T, int MODE, bool PAGED, int ITS>
 __global__ void __launch_bounds__(256)
 k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::Meta m,
-       const int32_t* __restrict__ cu, const int32_t* __restrict__ seqs, int n, int tokens, int dim, float eps, int shift,
-       int waves) {
+       const int32_t* __restrict__ cu, const int32_t* __restrict__ seqs, int n, int tokens, int dim, float eps, int shift) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t job = (int64_t)blockIdx.x * 4 + w;
-  const int t = (int)(job / waves), part = (int)(job % waves);
+  const int t = blockIdx.x * 4 + w, part = blockIdx.y;
   if (t >= tokens) return;
   const int l = lane & ((1 << shift) - 1), mine = lane >> shift, per = 64 >> shift;
   const Dims d = dims_of<MODE>(l, dim, turn.rotary);
@@ -120,6 +127,15 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
     it -= q_turns;
     return it < k_turns ? Heads{1, it * per} : Heads{2, (it - k_turns) * per};
   };
+  // what the positions and angles hang on comes first, as loads come in order
+  int ends = 0;
+  if constexpr (PAGED) ends = cu[min(lane + 1, n)];
+  uint64_t steps[8];
+  if constexpr (MODE != NONE) {
+    const int first = d.turns ? 8 * l : 0, pairs = turn.rotary / 2;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) steps[e] = turn.steps[min(first + e, pairs - 1)];
+  }
   u4 ra[ITS], rb[ITS];
 #pragma unroll
   for (int i = 0; i < ITS; ++i) {                  // those that are not there are others again
@@ -151,20 +167,19 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
   bool paged = true;
   int64_t page_at = 0;                             // of the cache's page and token, in elements
   if constexpr (PAGED) {
-    if (t < cu[0]) return;
-    const int i = find_seq(cu, n, t);
-    if (i < 0 || cu[i] > t) return;
-    const int slot = seqs[i];
+    const Found f = find_seq(cu, n, t, ends);
+    if (f.i < 0) return;
+    const int slot = fixed(seqs, f.i);
     int bad = 0;
     if ((unsigned)slot >= (unsigned)m.slots) {
       bad = PI_CACHE_ESLOT;
     } else {
-      const int64_t p = (int64_t)m.lens[slot] - cu[i + 1] + t;
+      const int64_t p = (int64_t)fixed(m.lens, slot) - f.to + t;
       if (p < 0 || p >= (int64_t)m.max_pages * m.page) {
         bad = PI_CACHE_ELENGTH;
       } else {
         at = (int)p;
-        const int id = m.table[(int64_t)slot * m.max_pages + at / m.page];
+        const int id = fixed(m.table, (int64_t)slot * m.max_pages + at / m.page);
         if ((unsigned)id >= (unsigned)m.pages) bad = PI_CACHE_EPAGE, paged = false;
         else page_at = ((int64_t)id * k.heads * m.page + at % m.page) * dim;
       }
@@ -172,16 +187,13 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
     if (bad && lane == 0) atomicOr(&m.words[1], bad);
     if (bad & ~PI_CACHE_EPAGE) return;
   } else if (MODE != NONE) {
-    at = pos[t];
+    at = fixed(pos, t);
   }
   float cs[8], sn[8];
   if constexpr (MODE != NONE) {
-    const int first = d.turns ? 8 * l : 0, pairs = turn.rotary / 2;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint64_t step = turn.steps[min(first + e, pairs - 1)];
-      sincos_turns((uint32_t)(((uint64_t)(int64_t)at * step) >> 32), turn.magnitude, &cs[e], &sn[e]);
-    }
+    for (int e = 0; e < 8; ++e)
+      sincos_turns((uint32_t)(((uint64_t)(int64_t)at * steps[e]) >> 32), turn.magnitude, &cs[e], &sn[e]);
   }
   const float over = 1.f / (float)dim;
 #pragma unroll

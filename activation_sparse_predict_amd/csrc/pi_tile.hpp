@@ -103,6 +103,13 @@ __device__ __forceinline__ int scan64(int v) {
 __device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
+// A value that all lanes ask for, by a scalar load, which waits on a counter of its own: for memory that nothing writes while
+// the kernel runs.
+__device__ __forceinline__ int fixed(const int32_t* p, int64_t at) {
+  typedef const __attribute__((address_space(4))) int32_t* memory;
+  return reinterpret_cast<memory>(reinterpret_cast<uintptr_t>(p))[at];
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 }  // namespace pit
