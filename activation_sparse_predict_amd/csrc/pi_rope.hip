@@ -56,12 +56,13 @@ pi_status launch(bool paged, int dtype, const pi_rope* r, const pir::Part& q, co
   // waves that the card does not hold at once anyway make the angles for several turns
   const int64_t all = (int64_t)tokens * turns;
   const int its = all >= 16384 && turns > 2 ? 4 : all >= 8192 && turns > 1 ? 2 : 1;
-  const dim3 grid((unsigned)up_div(tokens, 4), (unsigned)up_div(turns, its));
+  const int waves = (int)up_div(turns, its);                    // of a token
+  if ((int64_t)tokens * waves > INT32_MAX) return PI_EUNSUPPORTED;
   const pir::Turn turn{r ? r->steps : nullptr, rotary, !r || r->magnitude == 0.f ? 1.f : r->magnitude};
   (void)hipGetLastError();
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, static_cast<hipStream_t>(stream), turn, q, k, v,
-                       pos, m, cu, seqs, n, tokens, dim, eps, shift);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)up_div((int64_t)tokens * waves, 4)), dim3(256), 0, static_cast<hipStream_t>(stream), turn, q, k, v,
+                       pos, m, cu, seqs, n, tokens, dim, eps, shift, (uint32_t)waves);
   };
   auto with_its = [&](auto t, auto m, auto p) {
     using T = decltype(t);
