@@ -82,7 +82,7 @@ __device__ __forceinline__ int shares_of(const Seq& s, uint32_t size) {
 
 // Every tile of rows has one share, and up to `free` more are dealt.  Where there are fewer tiles than that, a share is made
 // as small as it can be with no more than `free` of them in all, so that all blocks run at once: a few steps towards that
-// size, for up to 64 sequences.  Sums are float32: what they may be off by is made up for in the size of a share, so that
+// size, for up to 64 sequences.  Where there are more, those sequences come first whose blocks have most to do.  Sums are float32: what they may be off by is made up for in the size of a share, so that
 // the blocks there are suffice.  `count`: count the tiles that are shared out too.
 __device__ __forceinline__ Piece find_piece(const Pages& pg, const Chunks& ch, int window, int idx, bool count) {
   const int lane = threadIdx.x & (WAVE - 1);
@@ -95,7 +95,8 @@ __device__ __forceinline__ Piece find_piece(const Pages& pg, const Chunks& ch, i
   }
   const float all = add64(work), free = (float)ch.free;
   float want = all / free * 1.0001f;
-  if (ch.n <= WAVE && add64(tiles) < free) {
+  const bool roomy = add64(tiles) < free;
+  if (ch.n <= WAVE && roomy) {
     for (int i = 0; i < 4; ++i) {
       const float got = add64((float)s.tiles * (float)shares_of(s, (uint32_t)min(want, 2e9f) + 1));
       if (got <= free) break;
@@ -103,6 +104,17 @@ __device__ __forceinline__ Piece find_piece(const Pages& pg, const Chunks& ch, i
     }
   }
   const uint32_t size = __builtin_amdgcn_readfirstlane((uint32_t)min(want, 2e9f) + 1);
+  if (ch.n > 1 && ch.n <= WAVE && !roomy) {
+    const int load = s.tiles ? min(s.keys, (int)min(size, (uint32_t)INT32_MAX)) : -1;
+    int rank = 0;
+    for (int j = 0; j < ch.n; ++j) {
+      const int other = __builtin_amdgcn_readlane(load, j);
+      rank += other > load || (other == load && j < lane);
+    }
+    if (lane >= ch.n) rank = lane;
+    auto to = [&](int v) { return __builtin_amdgcn_ds_permute(4 * rank, v); };
+    s = Seq{to(s.first), to(s.count), to(s.slot), to(s.len), to(s.raw), to(s.tiles), to(s.keys)};
+  }
   Piece p{};
   p.size = size;
   int slot = 0, joint = 0;
