@@ -131,14 +131,13 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
       pia::with_mod(call.mod, [&](auto m) { pia::launch(pia::k_attn_chunk<T, D, decltype(m)::value>, call, pia::ch_waves<D>()); });
     });
   }
-  auto join = [&](auto t) {
-    hipLaunchKernelGGL(pia::k_chunk_join<decltype(t)>,
+  with_type(cache->dtype, cache->dim, [&](auto t, auto d) {
+    constexpr int D = decltype(d)::value;
+    hipLaunchKernelGGL((pia::k_chunk_join<decltype(t), D <= 64 ? 16 : D <= 128 ? 32 : 64>),
                        dim3((unsigned)(std::min<int64_t>(u.free, tiles) * cache->kv_heads), (unsigned)up_div(u.rows, 4)),
                        dim3(256), 0, call.stream, call.joints, call.count, call.part, call.stat, call.out, call.out_token,
                        call.out_head, call.ch);
-  };
-  if (cache->dtype == PI_F16) join(pit::H16());
-  else join(pit::B16());
+  });
   return launched();
 }
 

@@ -773,35 +773,53 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   if (odd) add_wild<T>(pg, ch, sc.window, task, out, out_token, out_head, part);
 }
 
-// Join the shares of a row: a wave each, all lanes on a share's dims.
-template <class T>
+// Join the shares of a row: a wave each, N lanes (of 4 dims each) for a share, 64 / N shares at once, eight loads on their way.
+template <class T, int N>
 __global__ void __launch_bounds__(256)
 k_chunk_join(const Joint* __restrict__ joints, const int32_t* __restrict__ count, const float* __restrict__ part,
              const float* __restrict__ stat, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch) {
+  constexpr int AT_ONCE = 64 / N, AHEAD = 8;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int g = blockIdx.x % ch.kv_heads, x = blockIdx.x / ch.kv_heads, r = 4 * blockIdx.y + w;
+  const Joint jt = joints[x];                      // where there is none, what lies there is not used
   if (x >= min(*count, ch.slots / 2)) return;
-  const Joint jt = joints[x];
   if (jt.shares <= 1 || r >= jt.rows || jt.slot + (jt.shares - 1) * jt.step >= ch.slots) return;
   const int group = ch.heads / ch.kv_heads, row = jt.row0 + r;
   auto sums = [&](int i) { return ((int64_t)(jt.slot + i * jt.step) * ch.kv_heads + g) * ch.rows + r; };
-  float2 st = float2{NEG_INF, 0.f};
-  if (lane < jt.shares) st = *reinterpret_cast<const float2*>(stat + 2 * sums(lane));
+  const int d = min(4 * (lane % N), ch.dim - 4), mine = lane / N;
+  auto load = [&](int i) { return *reinterpret_cast<const f4*>(part + sums(min(i, jt.shares - 1)) * ch.dim + d); };
+  const float2 raw = *reinterpret_cast<const float2*>(stat + 2 * sums(min(lane, jt.shares - 1)));
+  f4 y[AHEAD];                                     // the first sums are on their way while the weights are made
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) y[i] = load(AT_ONCE * i + mine);
+  const float2 st = lane < jt.shares ? raw : float2{NEG_INF, 0.f};
   float mm = st.x;
 #pragma unroll
-  for (int y = 32; y; y >>= 1) mm = fmaxf(mm, __shfl_xor(mm, y));
+  for (int z = 32; z; z >>= 1) mm = fmaxf(mm, __shfl_xor(mm, z));
   const float base = mm == NEG_INF ? 0.f : mm;
-  const float weight = exp2_fast(st.x - base), total = add64(lane < jt.shares ? st.y * weight : 0.f);
+  const float weight = exp2_fast(st.x - base), total = add64(st.y * weight);
   const float inv = total == 0.f ? 0.f : 1.f / total;    // a row that sees no key is zero
   f4 sum = (f4)(0.f);
-  const int d = min(4 * lane, ch.dim - 4);
-  for (int i = 0; i < jt.shares; ++i) {
-    const f4 y = *reinterpret_cast<const f4*>(part + sums(i) * ch.dim + d);
-    const float a = __shfl(weight, i);
+  for (int i0 = 0; i0 < jt.shares; i0 += AT_ONCE * AHEAD) {
+    if (i0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = fmaf(y[e], a, sum[e]);
+      for (int i = 0; i < AHEAD; ++i) y[i] = load(i0 + AT_ONCE * i + mine);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = i0 + AT_ONCE * i + mine;
+      const float a = __shfl(weight, min(k, 63));
+      if (k < jt.shares) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = fmaf(y[i][e], a, sum[e]);
+      }
+    }
   }
-  if (4 * lane < ch.dim)
+#pragma unroll
+  for (int z = N; z < 64; z *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], z);
+  if (lane < N && 4 * lane < ch.dim)
     *reinterpret_cast<u2*>(out + (jt.first + row / group) * out_token + (g * group + row % group) * out_head + d) =
         u2{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
 }
