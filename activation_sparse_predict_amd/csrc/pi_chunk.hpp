@@ -13,6 +13,7 @@ namespace pia {
 
 constexpr int CH_ROWS = 128;             // rows of a block of k_attn_chunk
 constexpr int CH_MOST = 64;              // shares of a tile's keys at most
+template <int D> constexpr int ch_waves() { return D > 128 ? 8 : 4; }   // of a block of k_attn_chunk
 
 enum { CH_CAP = 1, CH_SLOPES = 2 };
 
@@ -207,17 +208,18 @@ __device__ __forceinline__ void hide(f16v* s, int lo, int hi, uint32_t bits) {
     }
 }
 
-// Whether a tile in LDS holds a value that is not finite.
+// Whether a tile in LDS holds a value that is not finite, by all threads of a block.
 template <class T, int D> __device__ __forceinline__ bool wild(const char* tile) {
   typedef unsigned short h2 __attribute__((ext_vector_type(2)));
+  constexpr int N = PT_K * Tile<D>::NC / (ch_waves<D>() * WAVE);
   h2 top = {0, 0};
 #pragma unroll
-  for (int i = 0; i < Tile<D>::NC; ++i) {
-    const u4 x = *reinterpret_cast<const u4*>(tile + 16 * (64 * i + (threadIdx.x & 63)));
+  for (int i = 0; i < N; ++i) {
+    const u4 x = *reinterpret_cast<const u4*>(tile + 16 * (ch_waves<D>() * WAVE * i + threadIdx.x));
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(h2, x[e] & 0x7fff7fffu));
   }
-  return __ballot(top[0] >= T::INF || top[1] >= T::INF) != 0;
+  return __syncthreads_or(top[0] >= T::INF || top[1] >= T::INF) != 0;
 }
 
 // 0 times an infinity or NaN of a value that a row does not see is NaN.  So where a tile that not all of a block's rows see
@@ -548,7 +550,6 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 // One block: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in tiles of 64 from
 // the last one down, which go to LDS past the registers one tile ahead of the products.  Four waves; for heads wider than 128,
 // whose sums and tiles leave room for no second block, eight, of which two take half of a tile's keys each for the same rows.
-template <int D> constexpr int ch_waves() { return D > 128 ? 8 : 4; }
 template <class T, int D, int MOD>
 __global__ void __launch_bounds__(ch_waves<D>() * WAVE, D <= 64 ? 4 : D <= 128 ? 2 : 1)
 k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
@@ -667,13 +668,15 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   bool odd = false;                                // whether there were values that are not finite
   uint32_t bits = 0;
   if (first <= last) bits = fetch_part(last);
-  // tiles below the last one that every row of the block sees whole; none where a page is broken
-  int upper = min(last - 1, (before + t0 + 1) / PT_K - 1), lower = max(first, (from + PT_K - 1) / PT_K);
+  // tiles below the last one that lie whole in what some row sees, and of these such as every row of the block sees whole;
+  // none where a page is broken
+  int whole = max(first, (from + PT_K - 1) / PT_K), upper = min(last - 1, (before + t0 + 1) / PT_K - 1), lower = whole;
   if (sc.window > 0) lower = max(lower, (before + t1 - sc.window) / PT_K + 1);
-  if (upper >= lower) {
+  if (whole < last) {
     bool broken = false;
-    for (int e = page_of(ch, 4 * lower) + tid, end = page_of(ch, 4 * last); e <= end; e += NT) broken |= usable_page(table[e], pg.pages) < 0;
-    if (__syncthreads_or(broken)) upper = lower - 1;
+    for (int e = page_of(ch, 4 * whole) + tid, end = page_of(ch, 4 * last); e <= end; e += NT)
+      broken |= usable_page(table[e], pg.pages) < 0;
+    if (__syncthreads_or(broken)) whole = last, upper = lower - 1;
   }
   const int mine_at = KW > 1 ? 32 * 16 * L::NC * half : 0;        // the wave's part of a tile in LDS
   // one tile of any kind, which lies in LDS; `there`: its places
@@ -696,7 +699,11 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   for (int j = last; j >= first;) {
     arrive<0>();
     const uint32_t there = bits;
-    if (j > first) bits = fetch_part(j - 1);
+    if (j > first) {
+      bits = 15;
+      if (j > whole) fetch(j - 1, look_up(j - 1));
+      else bits = fetch_part(j - 1);
+    }
     take(j, there);
     if (--j != upper || upper < lower) continue;
     int id = look_up(max(j - 1, lower));
