@@ -796,7 +796,7 @@ def rope_heads(rope: Optional[Rope], pos, q, q_out, k=None, k_out=None, q_norm=N
               and k.dtype == k_out.dtype == q.dtype, "rope_heads: k, k_out")
         heads = ks[1]
     _need(rope is None or pos is not None, "rope_heads: pos")
-    dev = _gpu("rope_heads: tensors of one GPU", q, q_out, k, k_out, pos, q_norm, k_norm, None if rope is None else rope.steps)
+    dev = _gpu("rope_heads: tensors of one GPU", q, q, q_out, k, k_out, pos, q_norm, k_norm, None if rope is None else rope.steps)
     _check(_on(dev, (_lib or lib()).pi_rope_heads, None if rope is None else rope._ref, _ints(pos, shape[0], "rope_heads: pos"),
                _heads(q, shape, what), _heads(q_out, shape, what), shape[1], _floats(q_norm, shape[2], "rope_heads: q_norm"),
                _heads(k, ks, what) if heads else None, _heads(k_out, ks, what) if heads else None, heads,

@@ -83,8 +83,10 @@ __device__ __forceinline__ int shares_of(const Seq& s, uint32_t size) {
 
 // Every tile of rows has one share, and up to `free` more are dealt.  Where there are fewer tiles than that, a share is made
 // as small as it can be with no more than `free` of them in all, so that all blocks run at once: a few steps towards that
-// size, for up to 64 sequences.  Where there are more, those sequences come first whose blocks have most to do.  Sums are float32: what they may be off by is made up for in the size of a share, so that
-// the blocks there are suffice.  `count`: count the tiles that are shared out too.
+// size, for up to 64 sequences.  Where there are more, those sequences come first whose blocks have most to do.  (24 chunks
+// of 1201 tokens behind up to 2050, 1280 blocks of uneven length on 1024 places: 86 us in the batch's order, 83 so.)  Sums are
+// float32: what they may be off by is made up for in the size of a share, so that the blocks there are suffice.  `count`:
+// count the tiles that are shared out too.
 __device__ __forceinline__ Piece find_piece(const Pages& pg, const Chunks& ch, int window, int idx, bool count) {
   const int lane = threadIdx.x & (WAVE - 1);
   Seq s = seq_of(pg, ch, window, lane);
@@ -137,6 +139,7 @@ __device__ __forceinline__ Piece find_piece(const Pages& pg, const Chunks& ch, i
       p.tile = p.s.tiles - 1 - nth;
       p.slot = slot + of(supto) - of(n > 1 ? blocks : 0) + nth;
       p.joint = joint + of(jupto) - of(js) + nth;
+      if (in < 0 || in >= of(blocks) || p.slot < 0) p.s.count = 0;   // offsets that do not ascend: the sums may not fit
       found = true;
       if (!count) return p;
     }
@@ -244,6 +247,7 @@ template <class T, int D> __device__ __forceinline__ void tame(char* sv) {
 struct Task {
   int g, first, last;                    // key head; key tiles of the share
   int from, to;                          // keys that any row sees
+  int window;                            // 0 where it is no smaller than what the slot holds, so that differences with it fit
   int before, t0, t1;                    // place of the chunk's first token; first and last token of the rows
   int row0, rows, token;                 // first row, rows (0: nothing to do); the chunk's first token in q
   int64_t table;                         // the slot's row of the table
@@ -264,14 +268,15 @@ __device__ __forceinline__ Task find_task(const Pages& pg, const Chunks& ch, int
   k.row0 = ch.tile * pc.tile;
   const int rows = min(ch.tile, pc.s.count * group - k.row0);
   k.t0 = k.row0 / group, k.t1 = (k.row0 + rows - 1) / group;
-  k.to = max(0, k.before + k.t1 + 1), k.from = window > 0 ? max(0, k.before + k.t0 + 1 - window) : 0;
+  k.window = window < pc.s.len ? window : 0;
+  k.to = max(0, k.before + k.t1 + 1), k.from = k.window > 0 ? max(0, k.before + k.t0 + 1 - k.window) : 0;
   const int tiles = k.to > k.from ? (k.to - 1) / PT_K - k.from / PT_K + 1 : 0;
   // shares of this tile: no more than its keys need
   k.shares = max(1, min(pc.shares, (int)(((uint32_t)tiles + pc.size - 1) / pc.size)));
   if (k.g == 0 && pc.share == 0 && threadIdx.x == 0) {
     if (pc.s.slot < 0 || pc.s.len != pc.s.raw || k.before < 0)
       atomicOr(pg.flags, pc.s.slot < 0 ? PI_CACHE_ESLOT : PI_CACHE_ELENGTH);
-    if (pc.shares > 1 && pc.joint < ch.slots / 2)
+    if (pc.shares > 1 && (unsigned)pc.joint < (unsigned)ch.slots / 2)
       joints[pc.joint] = Joint{pc.slot, k.shares, pc.s.first, k.row0, rows, pc.s.tiles};
   }
   k.slot = pc.slot + pc.share * pc.s.tiles;
@@ -289,13 +294,13 @@ __device__ __forceinline__ int page_of(const Chunks& ch, uint32_t place) {
 }
 
 // Whether some of the rows do not see all keys of a tile.
-__device__ __forceinline__ bool at_edge(const Task& k, int window, int tile) {
-  return PT_K * tile + PT_K - 1 > k.before + k.t0 || (window > 0 && PT_K * tile <= k.before + k.t1 - window);
+__device__ __forceinline__ bool at_edge(const Task& k, int tile) {
+  return PT_K * tile + PT_K - 1 > k.before + k.t0 || (k.window > 0 && PT_K * tile <= k.before + k.t1 - k.window);
 }
 
 // What `tame` took from the rows' sums, for all threads of a block after the sums were written.
 template <class T>
-__device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, int window, const Task& k, uint16_t* out,
+__device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, const Task& k, uint16_t* out,
                                          int64_t out_token, int64_t out_head, float* part) {
   __syncthreads();
   const int group = ch.heads / ch.kv_heads, dim = ch.dim;
@@ -303,11 +308,11 @@ __device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, int 
 #pragma unroll 1
   for (int e = threadIdx.x; e < k.rows * dim; e += blockDim.x) {
     const int row = k.row0 + e / dim, d = e % dim, place = k.before + row / group;
-    const int lo = window > 0 ? max(k.from, place + 1 - window) : k.from;
+    const int lo = k.window > 0 ? max(k.from, place + 1 - k.window) : k.from;
     float more = 0.f;
 #pragma unroll 1
     for (int j = k.first; j <= k.last; ++j) {
-      if (!at_edge(k, window, j)) continue;
+      if (!at_edge(k, j)) continue;
 #pragma unroll 1
       for (int key = max(PT_K * j, lo); key < min(PT_K * j + PT_K, place + 1); ++key) {
         const int id = usable_page(pg.table[k.table + page_of(ch, key / 16)], pg.pages);
@@ -418,7 +423,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
         }
       }
     // whether some row does not see one of the keys
-    const bool some = gone || k0 + 31 > k.before + k.t0 || k0 < k.from || (sc.window > 0 && k0 <= k.before + k.t1 - sc.window);
+    const bool some = gone || k0 + 31 > k.before + k.t0 || k0 < k.from || (k.window > 0 && k0 <= k.before + k.t1 - k.window);
     u4 pf[MT];
     float alpha[MT];
 #pragma unroll
@@ -432,7 +437,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
       }
       if constexpr (MOD != 0) change16<MOD>(s, sc, slope[m], k0 - place[m]);
       if (some) {
-        const int hi = place[m] + 1 - k0, lo = sc.window > 0 ? hi - sc.window : 0;
+        const int hi = place[m] + 1 - k0, lo = k.window > 0 ? hi - k.window : 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -468,7 +473,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 #pragma unroll
             for (int e = 0; e < V::W / 2; ++e) x[gr][i][e] = 0;
     }
-    if (k.t0 != k.t1 && at_edge(k, sc.window, st / 2)) {
+    if (k.t0 != k.t1 && at_edge(k, st / 2)) {
 #pragma unroll
       for (int gr = 0; gr < V::G; ++gr)
 #pragma unroll
@@ -544,7 +549,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
       }
     }
   }
-  if (k.t0 != k.t1 && __syncthreads_or(odd)) add_wild<T>(pg, ch, sc.window, k, out, out_token, out_head, part);
+  if (k.t0 != k.t1 && __syncthreads_or(odd)) add_wild<T>(pg, ch, k, out, out_token, out_head, part);
 }
 
 // One block: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in tiles of 64 from
@@ -671,7 +676,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   // tiles below the last one that lie whole in what some row sees, and of these such as every row of the block sees whole;
   // none where a page is broken
   int whole = max(first, (from + PT_K - 1) / PT_K), upper = min(last - 1, (before + t0 + 1) / PT_K - 1), lower = whole;
-  if (sc.window > 0) lower = max(lower, (before + t1 - sc.window) / PT_K + 1);
+  if (task.window > 0) lower = max(lower, (before + t1 - task.window) / PT_K + 1);
   if (whole < last) {
     bool broken = false;
     for (int e = page_of(ch, 4 * whole) + tid, end = page_of(ch, 4 * last); e <= end; e += NT)
@@ -683,15 +688,15 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   auto take = [&](int j, uint32_t there) {
     const int k0 = PT_K * j;
     char *sk = ring + j % S * R::BYTES, *sv = sk + S * R::BYTES;
-    const int below = place + 1 - k0, above = sc.window > 0 ? below - sc.window : 0;
-    if (t0 != t1 && at_edge(task, sc.window, j) && wild<T, D>(sv)) {
+    const int below = place + 1 - k0, above = task.window > 0 ? below - task.window : 0;
+    if (t0 != t1 && at_edge(task, j) && wild<T, D>(sv)) {
       tame<T, D>(sv);
       odd = true;
     }
-    if (!live || k0 > most || (sc.window > 0 && k0 + PT_K - 1 <= least - sc.window)) return;
+    if (!live || k0 > most || (task.window > 0 && k0 + PT_K - 1 <= least - task.window)) return;
     sum.scores(sk + mine_at, qf, rd, s);
     if constexpr (MOD != 0) change<MOD, H>(s, sc, slope, k0 + 32 * H * half - place);
-    if (there != 15 || k0 + PT_K - 1 > least || (sc.window > 0 && k0 <= most - sc.window))
+    if (there != 15 || k0 + PT_K - 1 > least || (task.window > 0 && k0 <= most - task.window))
       hide<H>(s, above - 32 * H * half, below - 32 * H * half, there >> 2 * H * half);
     sum.weigh(s, MOD ? 1.f : sc.c, pw);
     sum.add(sv + mine_at, pw, rd);
@@ -777,7 +782,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     const float l = sum32(sum.l);
     if (hi == 0 && lane < left) *reinterpret_cast<float2*>(stat + 2 * (sums + lane)) = float2{sum.mc, l};
   }
-  if (odd) add_wild<T>(pg, ch, sc.window, task, out, out_token, out_head, part);
+  if (odd) add_wild<T>(pg, ch, task, out, out_token, out_head, part);
 }
 
 // Join the shares of a row: a wave each, N lanes (of 4 dims each) for a share, 64 / N shares at once, eight loads on their way.
@@ -790,8 +795,12 @@ k_chunk_join(const Joint* __restrict__ joints, const int32_t* __restrict__ count
   const int g = blockIdx.x % ch.kv_heads, x = blockIdx.x / ch.kv_heads, r = 4 * blockIdx.y + w;
   const Joint jt = joints[x];                      // where there is none, what lies there is not used
   if (x >= min(*count, ch.slots / 2)) return;
-  if (jt.shares <= 1 || r >= jt.rows || jt.slot + (jt.shares - 1) * jt.step >= ch.slots) return;
   const int group = ch.heads / ch.kv_heads, row = jt.row0 + r;
+  // with offsets that do not ascend a tile may have no block, and its place here holds anything
+  if (jt.shares <= 1 || jt.shares > CH_MOST || r >= min(jt.rows, ch.rows) || jt.slot < 0 || jt.step < 0 ||
+      jt.slot + (int64_t)(jt.shares - 1) * jt.step >= ch.slots)
+    return;
+  if (jt.first < 0 || jt.row0 < 0 || row < 0 || (int64_t)jt.first + row / group >= ch.tokens) return;
   auto sums = [&](int i) { return ((int64_t)(jt.slot + i * jt.step) * ch.kv_heads + g) * ch.rows + r; };
   const int d = min(4 * (lane % N), ch.dim - 4), mine = lane / N;
   auto load = [&](int i) { return *reinterpret_cast<const f4*>(part + sums(min(i, jt.shares - 1)) * ch.dim + d); };

@@ -268,6 +268,54 @@ def test_offsets_that_cannot_be_stay_inside():
     assert (out[50:] == 7).all()
 
 
+def test_offsets_that_do_not_ascend_stay_inside():
+    """Sequences that overlap, more rows in all than the tensor has, behind many tokens: what comes out is not said, but nothing
+    outside the rows is written, and the next call is not led astray."""
+    n, t, heads, dim = 40, 60, 4, 64
+    h = Held(3, 1, 1, 16, dim, [3000] * 2, torch.float16)
+    q = normal(7, t, heads, dim, dtype=torch.float16)
+    big = torch.full((t + 400, heads, dim), 7.0, dtype=torch.float16, device=DEV)
+    pi.attn_chunk(h.cache, 0, normal(8, 400, heads, dim, dtype=torch.float16), big[:400], ints([0, 200, 400]))   # leaves its marks
+    big.fill_(7.0)
+    for cu in ([0, t] * (n // 2) + [0], [t, 0, t, 0, t], [0, t, 5, t, 7, t, 9, t]):
+        pi.attn_chunk(h.cache, 0, q, big[200:200 + t], ints(cu), ints([i % 2 for i in range(len(cu) - 1)]))
+    torch.cuda.synchronize()
+    assert (big[:200] == 7).all() and (big[200 + t:] == 7).all()
+    chunk_ref.check(run(h, q, [20, 40]), *chunk_ref.chunk(q, h.k, h.v, [20, 40]))
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 40, 90, 41])
+def test_chunks_longer_than_their_slots(window):
+    """Rows before a slot's first token are zero, the others see what there is, whatever the window."""
+    h = Held(3, 1, 1, 16, 64, [90, 40], torch.bfloat16)
+    for counts in ([120, 50], [91, 41]):
+        q = normal(7, sum(counts), 2, 64, dtype=torch.bfloat16)
+        out = run(h, q, counts, window=window)
+        at = 0
+        for i, c in enumerate(counts):
+            miss = c - h.lens[i]
+            assert (out[at:at + miss] == 0).all()
+            sl = slice(at + miss, at + c)
+            chunk_ref.check(out[sl], *chunk_ref.chunk(q[sl], h.k[i:i + 1], h.v[i:i + 1], [h.lens[i]], window=window))
+            at += c
+    assert h.cache.errors() == pi.PI_CACHE_ELENGTH
+
+
+def test_tensors_that_want_a_gradient_are_refused():
+    h = Held(3, 1, 1, 16, 64, [90], torch.bfloat16)
+    q = normal(7, 3, 2, 64, dtype=torch.bfloat16)
+    want, cu, rope = q.clone().requires_grad_(), ints([0, 3]), pi.Rope(64, device=DEV)
+    k = q[:, :1].contiguous()
+    for call in (lambda x: pi.attn_chunk(h.cache, 0, x, torch.empty_like(q), cu),
+                 lambda x: pi.rope_heads(rope, ints([0, 1, 2]), x, torch.empty_like(q)),
+                 lambda x: h.cache.append_rope(0, rope, x, torch.empty_like(q), k, k, cu, ints([0]))):
+        with pytest.raises(pi.PiError, match="gradient"):
+            call(want)
+        with torch.no_grad():
+            call(want)
+    torch.cuda.synchronize()
+
+
 def test_what_cannot_be():
     """Slots and lengths that cannot be, pages that cannot be: zeros, or those keys are not seen, and the error word."""
     lens, dim = [100, 50, 300], 64
