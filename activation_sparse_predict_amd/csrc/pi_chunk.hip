@@ -24,7 +24,9 @@ Cut cut_of(const pi_cache* c, int tokens, int heads, int few) {
   Cut u{};
   u.few = few;
   u.tile = few ? 16 * few : pia::CH_ROWS;
-  // blocks that run at once: two, three or (wide heads) one for each compute unit
+  // Blocks that run at once: two, three or (wide heads) one for each compute unit.  (256, 512, 768 and 1024 blocks: one token
+  // behind 1500, 32 heads, 14.6, 16.4, 16.3, 20.1 us; 5 drafts of 16 sequences -, 49, 59, 58; capped, heads of 256, 174, 200,
+  // 198, 208.)
   const int blocks = c->dim > 128 ? 256 : few == 1 || c->dim <= 64 ? 768 : 512;
   u.free = (int)up_div(blocks, c->kv_heads);
   u.slots = 2 * u.free;
@@ -34,7 +36,8 @@ Cut cut_of(const pi_cache* c, int tokens, int heads, int few) {
 
 // Which kernel takes a call: that for few rows where the chunks' rows of a key head are up to 32 on the average.  A chunk that
 // has more of them, or fewer, comes out the same: only its time hangs on this.  (16 chunks behind up to 4000 tokens, 64 heads
-// on 8, 128 wide: 16, 32, 40 and 56 rows a chunk 46, 50, 65 and - us with k_chunk_few, 57, 57, 50 and 50 with k_attn_chunk.)
+// on 8, 128 wide: 40 rows a chunk 65 us with a k_chunk_few of 48 rows a block, 69 with one of 32, 48 with k_attn_chunk; one row
+// a chunk of 32 heads, 8 chunks behind up to 2900: 52 us with k_chunk_few, 68 with k_attn_chunk.)
 int few_of(const pi_cache* c, int tokens, int heads, int n) {
   const int64_t rows = up_div(tokens, std::max(1, std::min(n, tokens))) * (heads / c->kv_heads);
   return rows > 32 ? 0 : (int)up_div(rows, 16);
@@ -131,10 +134,13 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
       pia::with_mod(call.mod, [&](auto m) { pia::launch(pia::k_attn_chunk<T, D, decltype(m)::value>, call, pia::ch_waves<D>()); });
     });
   }
+  // rows of a block of the join: four a wave where there may be many blocks with nothing to do, else one.  (24 chunks of 1201
+  // tokens, heads 64 wide, nothing to join: 78 us, 81 with one; wide heads, most tiles joined: 117 us, 110 with one.)
+  const int each = u.rows >= 64 && cache->dim <= 128 ? 16 : 4;
   with_type(cache->dtype, cache->dim, [&](auto t, auto d) {
     constexpr int D = decltype(d)::value;
     hipLaunchKernelGGL((pia::k_chunk_join<decltype(t), D <= 64 ? 16 : D <= 128 ? 32 : 64>),
-                       dim3((unsigned)(std::min<int64_t>(u.free, tiles) * cache->kv_heads), (unsigned)up_div(u.rows, 4)),
+                       dim3((unsigned)(std::min<int64_t>(u.free, tiles) * cache->kv_heads), (unsigned)up_div(u.rows, each)),
                        dim3(256), 0, call.stream, call.joints, call.count, call.part, call.stat, call.out, call.out_token,
                        call.out_head, call.ch);
   });

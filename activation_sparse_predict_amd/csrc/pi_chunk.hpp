@@ -333,7 +333,9 @@ __device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, cons
 
 // ---- chunks of few rows: 16 MT of them for a block, with the products and the layout of k_attn_decode.  The four waves take
 // steps of 32 keys in turn, whose keys and values go straight to registers: what a compute unit has on its way from memory
-// bounds these, and its registers hold more than its LDS.
+// bounds these, and its registers hold more than its LDS (192 KB with three blocks of MT 1, 64 KB in two blocks' tiles).
+// 8 sequences of one token behind up to 2900, 32 heads of 128: 40 us, 5.5 TB/s of keys and values; one token behind 1500:
+// 9.9 us, latency: slots and lengths, page numbers, pages, the join of the waves.
 template <class T, int D, int MOD, int MT>
 __global__ void __launch_bounds__(4 * WAVE, D > 128 ? 1 : D <= 64 || MT == 1 ? 3 : 2)
 k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
@@ -555,6 +557,15 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 // One block: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in tiles of 64 from
 // the last one down, which go to LDS past the registers one tile ahead of the products.  Four waves; for heads wider than 128,
 // whose sums and tiles leave room for no second block, eight, of which two take half of a tile's keys each for the same rows.
+//
+// 512 tokens of 32 heads on 8, 128 wide, behind 32768: 280 us, 990 TFLOP/s, the matrix cores busy for 43 % of the cycles, as
+// in k_attn_prompt (see there).  The inner loop is that of whole tiles that all rows see, 350 instructions a wave and tile;
+// with page numbers, edges and masks looked at in each tile it was 820 (430 us).  24 chunks, 128 heads on 8, 64 wide: 78 us,
+// vector instructions (the exponentials) and the uneven lengths of blocks: waves wait for 37 % of their time.  Heads 256 wide:
+// 730 TFLOP/s (4096 tokens, 16 heads), products, LDS reads and exponentials of eight waves that keep step follow one another
+// more than they overlap; four waves with 32 more registers of scores took 166 us where eight take 131.  Wave priorities for
+// half of them change nothing; a first round without looking for values that are not finite, and a second one where any came
+// out, costs registers (capped 118 -> 128 us).
 template <class T, int D, int MOD>
 __global__ void __launch_bounds__(ch_waves<D>() * WAVE, D <= 64 ? 4 : D <= 128 ? 2 : 1)
 k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
@@ -786,58 +797,63 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
 }
 
 // Join the shares of a row: a wave each, N lanes (of 4 dims each) for a share, 64 / N shares at once, eight loads on their way.
+// A wave takes several rows of a tile where that has many: most calls with such tiles have nothing to join, and the blocks that
+// find this out take their time too.
 template <class T, int N>
 __global__ void __launch_bounds__(256)
 k_chunk_join(const Joint* __restrict__ joints, const int32_t* __restrict__ count, const float* __restrict__ part,
              const float* __restrict__ stat, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch) {
   constexpr int AT_ONCE = 64 / N, AHEAD = 8;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int g = blockIdx.x % ch.kv_heads, x = blockIdx.x / ch.kv_heads, r = 4 * blockIdx.y + w;
+  const int g = blockIdx.x % ch.kv_heads, x = blockIdx.x / ch.kv_heads;
   const Joint jt = joints[x];                      // where there is none, what lies there is not used
   if (x >= min(*count, ch.slots / 2)) return;
-  const int group = ch.heads / ch.kv_heads, row = jt.row0 + r;
+  const int group = ch.heads / ch.kv_heads;
   // with offsets that do not ascend a tile may have no block, and its place here holds anything
-  if (jt.shares <= 1 || jt.shares > CH_MOST || r >= min(jt.rows, ch.rows) || jt.slot < 0 || jt.step < 0 ||
-      jt.slot + (int64_t)(jt.shares - 1) * jt.step >= ch.slots)
+  if (jt.shares <= 1 || jt.shares > CH_MOST || jt.slot < 0 || jt.step < 0 ||
+      jt.slot + (int64_t)(jt.shares - 1) * jt.step >= ch.slots || jt.first < 0 || jt.row0 < 0)
     return;
-  if (jt.first < 0 || jt.row0 < 0 || row < 0 || (int64_t)jt.first + row / group >= ch.tokens) return;
-  auto sums = [&](int i) { return ((int64_t)(jt.slot + i * jt.step) * ch.kv_heads + g) * ch.rows + r; };
-  const int d = min(4 * (lane % N), ch.dim - 4), mine = lane / N;
-  auto load = [&](int i) { return *reinterpret_cast<const f4*>(part + sums(min(i, jt.shares - 1)) * ch.dim + d); };
-  const float2 raw = *reinterpret_cast<const float2*>(stat + 2 * sums(min(lane, jt.shares - 1)));
-  f4 y[AHEAD];                                     // the first sums are on their way while the weights are made
+  for (int r = 4 * blockIdx.y + w; r < min(jt.rows, ch.rows); r += 4 * gridDim.y) {
+    const int64_t row = (int64_t)jt.row0 + r, token = jt.first + row / group;
+    if (token >= ch.tokens) return;
+    auto sums = [&](int i) { return ((int64_t)(jt.slot + i * jt.step) * ch.kv_heads + g) * ch.rows + r; };
+    const int d = min(4 * (lane % N), ch.dim - 4), mine = lane / N;
+    auto load = [&](int i) { return *reinterpret_cast<const f4*>(part + sums(min(i, jt.shares - 1)) * ch.dim + d); };
+    const float2 raw = *reinterpret_cast<const float2*>(stat + 2 * sums(min(lane, jt.shares - 1)));
+    f4 y[AHEAD];                                   // the first sums are on their way while the weights are made
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) y[i] = load(AT_ONCE * i + mine);
-  const float2 st = lane < jt.shares ? raw : float2{NEG_INF, 0.f};
-  float mm = st.x;
+    for (int i = 0; i < AHEAD; ++i) y[i] = load(AT_ONCE * i + mine);
+    const float2 st = lane < jt.shares ? raw : float2{NEG_INF, 0.f};
+    float mm = st.x;
 #pragma unroll
-  for (int z = 32; z; z >>= 1) mm = fmaxf(mm, __shfl_xor(mm, z));
-  const float base = mm == NEG_INF ? 0.f : mm;
-  const float weight = exp2_fast(st.x - base), total = add64(st.y * weight);
-  const float inv = total == 0.f ? 0.f : 1.f / total;    // a row that sees no key is zero
-  f4 sum = (f4)(0.f);
-  for (int i0 = 0; i0 < jt.shares; i0 += AT_ONCE * AHEAD) {
-    if (i0) {
+    for (int z = 32; z; z >>= 1) mm = fmaxf(mm, __shfl_xor(mm, z));
+    const float base = mm == NEG_INF ? 0.f : mm;
+    const float weight = exp2_fast(st.x - base), total = add64(st.y * weight);
+    const float inv = total == 0.f ? 0.f : 1.f / total;  // a row that sees no key is zero
+    f4 sum = (f4)(0.f);
+    for (int i0 = 0; i0 < jt.shares; i0 += AT_ONCE * AHEAD) {
+      if (i0) {
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) y[i] = load(i0 + AT_ONCE * i + mine);
-    }
+        for (int i = 0; i < AHEAD; ++i) y[i] = load(i0 + AT_ONCE * i + mine);
+      }
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int k = i0 + AT_ONCE * i + mine;
-      const float a = __shfl(weight, min(k, 63));
-      if (k < jt.shares) {
+      for (int i = 0; i < AHEAD; ++i) {
+        const int k = i0 + AT_ONCE * i + mine;
+        const float a = __shfl(weight, min(k, 63));
+        if (k < jt.shares) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] = fmaf(y[i][e], a, sum[e]);
+          for (int e = 0; e < 4; ++e) sum[e] = fmaf(y[i][e], a, sum[e]);
+        }
       }
     }
+#pragma unroll
+    for (int z = N; z < 64; z *= 2)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], z);
+    if (lane < N && 4 * lane < ch.dim)
+      *reinterpret_cast<u2*>(out + token * out_token + (g * group + row % group) * out_head + d) =
+          u2{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
   }
-#pragma unroll
-  for (int z = N; z < 64; z *= 2)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += __shfl_xor(sum[e], z);
-  if (lane < N && 4 * lane < ch.dim)
-    *reinterpret_cast<u2*>(out + (jt.first + row / group) * out_token + (g * group + row % group) * out_head + d) =
-        u2{T::pack(sum[0] * inv, sum[1] * inv), T::pack(sum[2] * inv, sum[3] * inv)};
 }
 
 }  // namespace pia

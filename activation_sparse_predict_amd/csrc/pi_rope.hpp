@@ -105,7 +105,9 @@ template <int MODE> __device__ __forceinline__ Dims dims_of(int l, int dim, int 
 
 // A wave takes one token and up to ITS turns, each of 64 / P heads of one kind, P = 2^shift lanes a head: those of q, then of
 // k, then of v, which is copied.  All it loads is asked for before anything else, without conditions, and no load follows a
-// store: the counter that a wave waits on counts both, in order.  The angles are made once for all turns.
+// store: the counter that a wave waits on counts both, in order (with the next turn's loads behind a turn's stores: 133 us,
+// not 50, for 6151 tokens of 64 heads on 8, 128 wide, with norms).  The angles are made once for all turns.  That case: 45 us
+// in the kernel, 5.0 TB/s read and written, the rate of a large copy.
 template <class T, int MODE, bool PAGED, int ITS>
 __global__ void __launch_bounds__(256)
 k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::Meta m,
