@@ -6,7 +6,8 @@ tokens) and the predictor-guided sparse FFN:
     h  = rms(x + W_o attention(W_qkv x))
     x' = rms(h + ffn(h))
 
-The text goes through the prompt path into one slot of the cache.  That slot is forked once for every question, so all
+The text goes through the prompt path into one slot of the cache, whole or in pieces that each see what the cache holds of
+those before.  That slot is forked once for every question, so all
 questions share the text's whole pages, and each decoding step reads those once for the batch.  A step is captured into
 a graph and replayed.  At the end half of the questions are released and the pool's pages are moved to its front.
 
@@ -42,7 +43,7 @@ class Decoder:
     """Weights, cache and buffers of `slots` sequences."""
 
     def __init__(self, *, layers=2, width=4096, ffn=11008, rank=1024, heads=32, kv_heads=8, dim=128, page=16, pages=2048,
-                 slots=33, max_pages=512, seed=1, device="cuda"):
+                 slots=33, max_pages=512, piece=0, seed=1, device="cuda"):
         self.heads, self.kv_heads, self.dim, self.width, self.device = heads, kv_heads, dim, width, device
         gen = torch.Generator(device=device)
         gen.manual_seed(seed)
@@ -56,6 +57,7 @@ class Decoder:
         self.rows = torch.arange(slots + 1, dtype=torch.int32, device=device)
         self.prefix = torch.zeros(1, dtype=torch.int32, device=device)   # pages that all slots in use have in common
         self.used = set()                              # slots that were filled
+        self.piece = piece                             # tokens of a prompt that go through the layers at once; 0: all
 
     def ints(self, values):
         return torch.tensor(values, dtype=torch.int32, device=self.device)
@@ -92,6 +94,8 @@ class Decoder:
         h, g = self.heads, self.kv_heads
         self.used.add(slot)
         self.prefix.zero_()
+        if self.piece:
+            return torch.cat([self._piece(x[a:a + self.piece], slot, trace) for a in range(0, x.shape[0], self.piece)])
         cu, seqs = self.ints([0, x.shape[0]]), self.ints([slot])
         self.cache.extend(seqs, self.ints([x.shape[0]]))
         for i in range(len(self.ffn)):
@@ -99,6 +103,18 @@ class Decoder:
                 q, k, v = qkv[:, :h], qkv[:, h:h + g], qkv[:, h + g:]
                 self.cache.append(i, k, v, cu, seqs)
                 pi.attn_prompt(q, k, v, out, cu)
+            x = self._layer(i, x, attend, trace)
+        return x
+
+    def _piece(self, x, slot, trace):
+        """The next tokens x [tokens, width] of a slot; their outputs."""
+        h, g = self.heads, self.kv_heads
+        cu, seqs = self.ints([0, x.shape[0]]), self.ints([slot])
+        self.cache.extend(seqs, self.ints([x.shape[0]]))
+        for i in range(len(self.ffn)):
+            def attend(qkv, out):
+                self.cache.append(i, qkv[:, h:h + g], qkv[:, h + g:], cu, seqs)
+                pi.attn_chunk(self.cache, i, qkv[:, :h], out, cu, seqs)
             x = self._layer(i, x, attend, trace)
         return x
 
@@ -125,13 +141,13 @@ class Decoder:
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("layers", 2), ("width", 4096), ("ffn", 11008), ("rank", 1024), ("heads", 32), ("kv-heads", 8),
-                        ("dim", 128), ("page", 16), ("text", 1000), ("questions", 8), ("tokens", 64)):
+                        ("dim", 128), ("page", 16), ("text", 1000), ("questions", 8), ("tokens", 64), ("piece", 0)):
         ap.add_argument("--" + name, type=int, default=value)
     a = ap.parse_args()
     per = (a.text + a.tokens + 8) // a.page + 2        # pages of one sequence
     pages = a.text // a.page + 1 + (a.questions + 1) * (a.tokens // a.page + 3)
     d = Decoder(layers=a.layers, width=a.width, ffn=a.ffn, rank=a.rank, heads=a.heads, kv_heads=a.kv_heads, dim=a.dim,
-                page=a.page, pages=pages, slots=a.questions + 1, max_pages=per)
+                page=a.page, pages=pages, slots=a.questions + 1, max_pages=per, piece=a.piece)
     gen = torch.Generator(device=d.device)
     gen.manual_seed(2)
     text = torch.randn(a.text, a.width, generator=gen, device=d.device)
