@@ -558,8 +558,8 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 // the last one down, which go to LDS past the registers one tile ahead of the products.  Four waves; for heads wider than 128,
 // whose sums and tiles leave room for no second block, eight, of which two take half of a tile's keys each for the same rows.
 //
-// 512 tokens of 32 heads on 8, 128 wide, behind 32768: 280 us, 990 TFLOP/s, the matrix cores busy for 43 % of the cycles, as
-// in k_attn_prompt (see there).  The inner loop is that of whole tiles that all rows see, 350 instructions a wave and tile;
+// 512 tokens of 32 heads on 8, 128 wide, behind 32768: 280 us, 990 TFLOP/s, the matrix cores busy for about half of the
+// cycles, as in k_attn_prompt (see there).  The inner loop is that of whole tiles that all rows see, 350 instructions a wave and tile;
 // with page numbers, edges and masks looked at in each tile it was 820 (430 us).  24 chunks, 128 heads on 8, 64 wide: 78 us,
 // vector instructions (the exponentials) and the uneven lengths of blocks: waves wait for 37 % of their time.  Heads 256 wide:
 // 730 TFLOP/s (4096 tokens, 16 heads), products, LDS reads and exponentials of eight waves that keep step follow one another

@@ -229,8 +229,8 @@ pi_status pi_ffn_stack_static(const pi_layer* layers, int32_t n_layers, const fl
  *    with 8 <= dim <= 256 and dim % 8 == 0; scores, softmax statistics and
  *    sums are float32.
  *  - heads % kv_heads == 0; query head h reads key head h / (heads / kv_heads).
- *  - An output lies over no input, but pi_attn_prompt's and pi_attn_decode's may
- *    be q itself, with q's strides.
+ *  - An output lies over no input, but pi_attn_prompt's, pi_attn_decode's and
+ *    pi_attn_chunk's may be q itself, with q's strides.
  *  - What only the device knows (lengths, slot and page numbers) is checked
  *    there: nothing outside the tensors is ever read or written for it.  An
  *    accounting call (extend, fork, release) that cannot be carried out whole
@@ -392,8 +392,9 @@ pi_status pi_rope_steps(const double* freqs, int32_t n, uint64_t* steps);
  * then y at position pos[t] ([tokens], any int32) as `rope` says.  rope NULL:
  * nothing turns, pos is not read.  q_norm, k_norm NULL: no norm; eps finite and
  * positive where there is one.  k, k_out NULL with kv_heads 0: queries alone.
- * Everything is float32 with one rounding at the end; each output is x's own
- * tensor with its strides, or lies over no input and no other output.
+ * Everything, the sum of squares too, is float32 with one rounding at the end;
+ * what neither turns nor has a norm is moved bit by bit.  Each output is its
+ * input's own tensor with its strides, or lies over no input and no other output.
  */
 pi_status pi_rope_heads(const pi_rope* rope, const int32_t* pos, const pi_heads* q, const pi_heads* q_out, int32_t heads,
                         const float* q_norm, const pi_heads* k, const pi_heads* k_out, int32_t kv_heads,
@@ -403,7 +404,8 @@ pi_status pi_rope_heads(const pi_rope* rope, const int32_t* pos, const pi_heads*
  * pi_cache_append_rope -- pi_cache_append of normed and turned keys: row t of k,
  * as pi_rope_heads makes it at the position that the token has in its slot, and
  * of v go to the slot's pages; row t of q, likewise, goes to q_out (q, q_out NULL
- * with heads 0: keys alone).  Rows of a slot or length that cannot be are not
+ * with heads 0: keys alone), which may be q itself.  As in pi_cache_append no slot
+ * comes twice.  Rows of a slot or length that cannot be are not
  * written, nor is what a broken page would hold.
  */
 pi_status pi_cache_append_rope(const pi_cache* cache, int32_t layer, const pi_rope* rope, const pi_heads* q,
