@@ -20,7 +20,9 @@ using namespace pit;
 //  HALF         rotary % 16 == 0: chunk l and the one rotary / 2 dims on; the lanes
 //               behind these take what does not turn, two chunks each
 //  ODD          other rotary: dims 8 l .. of the first half and of the second, which
-//               start on no chunk; values are read and written one by one
+//               starts on no chunk; rows come and go in chunks l and l + P and are
+//               taken apart in LDS (3018 tokens of 64 heads on 8, 128 wide, 62 of them
+//               turned, with norms: 93 us with values loaded and stored one by one, 52 so)
 enum { NONE = 0, HALF = 1, PAIRS = 2, ODD = 3 };
 
 struct Turn {
@@ -103,6 +105,13 @@ template <int MODE> __device__ __forceinline__ Dims dims_of(int l, int dim, int 
   }
 }
 
+// What a wave's lanes wrote to LDS is there for its other lanes, as they read it in order.
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // A wave takes one token and up to ITS turns, each of 64 / P heads of one kind, P = 2^shift lanes a head: those of q, then of
 // k, then of v, which is copied.  All it loads is asked for before anything else, without conditions, and no load follows a
 // store: the counter that a wave waits on counts both, in order (with the next turn's loads behind a turn's stores: 133 us,
@@ -146,24 +155,18 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
     ends = cu[min(lane + 1, n)];
     load_steps();
   }
+  const int ca = MODE == ODD ? 8 * l : d.a, cb = MODE == ODD ? 8 * (l + (1 << shift)) : d.b;   // the chunks that a lane moves
+  const bool has_a = MODE == ODD ? ca < dim : d.na > 0, has_b = MODE == ODD ? cb < dim : d.nb > 0;
+  __shared__ u4 apart[MODE == ODD ? 4 * 128 : 1];
+  uint16_t* own = reinterpret_cast<uint16_t*>(apart + (MODE == ODD ? 128 * w : 0)) + mine * dim;   // the lane's head
   u4 ra[ITS], rb[ITS];
 #pragma unroll
   for (int i = 0; i < ITS; ++i) {                  // those that are not there are others again
     const Heads h = heads_of(min(begin + i, end - 1));
     const Part& x = h.kind == 0 ? q : h.kind == 1 ? k : v;
     const uint16_t* src = x.src + t * x.src_token + min(h.first + mine, x.heads - 1) * x.src_head;
-    if constexpr (MODE == ODD) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a0 = src[min(d.a + 2 * e, dim - 1)], a1 = src[min(d.a + 2 * e + 1, dim - 1)];
-        const uint32_t b0 = src[min(d.b + 2 * e, dim - 1)], b1 = src[min(d.b + 2 * e + 1, dim - 1)];
-        ra[i][e] = (2 * e < d.na ? a0 : 0) | (2 * e + 1 < d.na ? a1 << 16 : 0);
-        rb[i][e] = (2 * e < d.nb ? b0 : 0) | (2 * e + 1 < d.nb ? b1 << 16 : 0);
-      }
-    } else {
-      ra[i] = *reinterpret_cast<const u4*>(src + min(d.a, dim - 8));
-      rb[i] = *reinterpret_cast<const u4*>(src + min(d.b, dim - 8));
-    }
+    ra[i] = *reinterpret_cast<const u4*>(src + min(ca, dim - 8));
+    rb[i] = *reinterpret_cast<const u4*>(src + min(cb, dim - 8));
   }
   float qn[16], kn[16];
   auto weights = [&](const float* from, float* n) {
@@ -217,6 +220,19 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
       if (d.na == 0) ya = u4{0, 0, 0, 0};
       if (d.nb == 0) yb = u4{0, 0, 0, 0};
     }
+    if (MODE == ODD && h.kind < 2) {
+      if (has_a) *reinterpret_cast<u4*>(own + ca) = ya;
+      if (has_b) *reinterpret_cast<u4*>(own + cb) = yb;
+      settle();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t a0 = own[min(d.a + 2 * e, dim - 1)], a1 = own[min(d.a + 2 * e + 1, dim - 1)];
+        const uint32_t b0 = own[min(d.b + 2 * e, dim - 1)], b1 = own[min(d.b + 2 * e + 1, dim - 1)];
+        ya[e] = (2 * e < d.na ? a0 : 0) | (2 * e + 1 < d.na ? a1 << 16 : 0);
+        yb[e] = (2 * e < d.nb ? b0 : 0) | (2 * e + 1 < d.nb ? b1 << 16 : 0);
+      }
+      settle();
+    }
     if (h.kind < 2 && (MODE != NONE || weight)) {
       float x[16];
 #pragma unroll
@@ -259,21 +275,24 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
         }
       }
     }
+    if (MODE == ODD && h.kind < 2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (e < d.na) own[d.a + e] = (uint16_t)(ya[e / 2] >> 16 * (e % 2));
+        if (e < d.nb) own[d.b + e] = (uint16_t)(yb[e / 2] >> 16 * (e % 2));
+      }
+      settle();
+      ya = *reinterpret_cast<const u4*>(own + min(ca, dim - 8));
+      yb = *reinterpret_cast<const u4*>(own + min(cb, dim - 8));
+      settle();
+    }
     const Part& y = h.kind == 0 ? q : h.kind == 1 ? k : v;
     if (h.first + mine >= y.heads || (PAGED && h.kind > 0 && !paged)) continue;
     const int64_t token = PAGED && h.kind > 0 ? page_at : t * y.dst_token;
     const int64_t head = PAGED && h.kind > 0 ? (int64_t)m.page * dim : y.dst_head;
     uint16_t* dst = y.dst + token + h.first * head + mine * head;
-    if constexpr (MODE == ODD) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (e < d.na) dst[d.a + e] = (uint16_t)(ya[e / 2] >> 16 * (e % 2));
-        if (e < d.nb) dst[d.b + e] = (uint16_t)(yb[e / 2] >> 16 * (e % 2));
-      }
-    } else {
-      if (d.na > 0) *reinterpret_cast<u4*>(dst + d.a) = ya;
-      if (d.nb > 0) *reinterpret_cast<u4*>(dst + d.b) = yb;
-    }
+    if (has_a) *reinterpret_cast<u4*>(dst + ca) = ya;
+    if (has_b) *reinterpret_cast<u4*>(dst + cb) = yb;
   }
 }
 
