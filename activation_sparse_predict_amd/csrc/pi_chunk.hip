@@ -106,17 +106,12 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   const int64_t tiles = up_div((int64_t)tokens * (heads / cache->kv_heads), u.tile) + most;
   char* base = static_cast<char*>(ws);
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
-  // the page of a place of 16 keys by a multiplication: ceil(2^(31 + shift) / per) is off by less than 1, and with
-  // 2^shift <= per < 2^(shift + 1) that changes no quotient of a place below 2^30
-  const uint32_t per = cache->page / 16;
-  uint32_t shift = 0;
-  while (per >> (shift + 1)) ++shift;
-  const uint32_t mul = (uint32_t)(((uint64_t(1) << (31 + shift)) + per - 1) / per);
   pia::ChunkCall call{};
   call.pg = pages_of(cache, layer);
   call.q = rows_of(q);
   call.out = static_cast<uint16_t*>(out->p), call.out_token = out->token_stride, call.out_head = out->head_stride;
-  call.ch = pia::Chunks{cu, seqs, n, tokens, heads, cache->kv_heads, cache->dim, u.tile, u.free, u.slots, u.rows, mul, shift};
+  call.ch = pia::Chunks{cu, seqs, n, tokens, heads, cache->kv_heads, cache->dim, u.tile, u.free, u.slots, u.rows,
+                       pish::divide_by(cache->page / 16)};
   call.sc = sc;
   call.count = reinterpret_cast<int32_t*>(base), call.joints = reinterpret_cast<pia::Joint*>(base + W.joints);
   call.part = floats(W.part), call.stat = floats(W.stat);

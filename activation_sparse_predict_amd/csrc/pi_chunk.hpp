@@ -31,7 +31,7 @@ struct Chunks {
   int tile;                              // rows of a block
   int free;                              // shares to deal beside one a tile
   int slots, rows;                       // places for sums in the workspace, rows of each
-  uint32_t mul, shift;                   // a place's page: mulhi(2 place, mul) >> shift
+  Divide page;                           // a place's page from its number
 };
 
 // A tile of rows whose keys are shared out, for k_chunk_join.
@@ -178,7 +178,7 @@ __device__ __forceinline__ void change(f16v* s, const ChunkScore& sc, float slop
     }
 }
 
-// The same for the scores of a step of 32 keys of few_rows.
+// The same for the scores of a step of 32 keys of k_chunk_few.
 template <int MOD>
 __device__ __forceinline__ void change16(f4* s, const ChunkScore& sc, float slope, int back) {
   const float at = slope * (float)(back + 4 * (int)((threadIdx.x & 63) >> 4));
@@ -289,9 +289,7 @@ __device__ __forceinline__ Task find_task(const Pages& pg, const Chunks& ch, int
   return k;
 }
 
-__device__ __forceinline__ int page_of(const Chunks& ch, uint32_t place) {
-  return (int)(__umulhi(2 * place, ch.mul) >> ch.shift);
-}
+__device__ __forceinline__ int page_of(const Chunks& ch, uint32_t place) { return divided(place, ch.page); }
 
 // Whether some of the rows do not see all keys of a tile.
 __device__ __forceinline__ bool at_edge(const Task& k, int tile) {
@@ -575,13 +573,15 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   using R = Ring<D, S, NT>;
   constexpr int SUMS = D <= 64 ? 4 * 32 * 68 * 4 : 0;   // sums on their way out, which take more than small tiles do
   __shared__ float2 stats[KW > 1 ? NT / 2 : 1];
-  __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES > SUMS ? 2 * S * R::BYTES : SUMS];   // K tiles, then V tiles
+  // K tiles, then V tiles
+  __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES > SUMS ? 2 * S * R::BYTES : SUMS];
 
   const Task task = find_task(pg, ch, sc.window, joints, count);
   if (task.rows == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), hi = lane >> 5;
   const int group = ch.heads / ch.kv_heads, nchunk = ch.dim / 8;
-  const int first = task.first, last = task.last, from = task.from, to = task.to, before = task.before, t0 = task.t0, t1 = task.t1;
+  const int first = task.first, last = task.last, from = task.from, to = task.to;
+  const int before = task.before, t0 = task.t0, t1 = task.t1;
 
   const int half = w / 4, row0 = task.row0 + 32 * (w % 4), row = row0 + (lane & 31), end = task.row0 + task.rows;
   const bool live = row0 < end;
@@ -609,7 +609,8 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   const char *vg = reinterpret_cast<const char*>(pg.v) + (int64_t)task.g * head_bytes;
   // byte of a place of 16 keys, from its page's number
   auto place_at = [&](int x, int id) {
-    return uniform((int64_t)((uint64_t)(uint32_t)id * page_bytes + (uint32_t)(x - page_of(ch, x) * (pg.page / 16)) * (uint32_t)(32 * ch.dim)));
+    const uint32_t in = (uint32_t)(x - page_of(ch, x) * (pg.page / 16)) * (uint32_t)(32 * ch.dim);
+    return uniform((int64_t)((uint64_t)(uint32_t)id * page_bytes + in));
   };
   // A wave loads one place of a tile, LW times 1024 bytes (of eight waves four the keys and four the values).  What a lane takes
   // of it is the chunk that its place in LDS asks for.

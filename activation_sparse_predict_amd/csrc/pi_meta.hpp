@@ -17,7 +17,7 @@ inline Meta meta_of(const pi_cache* c) {
   int32_t* lens = table + (int64_t)c->slots * c->max_pages;
   int32_t* ref = lens + c->slots;
   return Meta{table, lens, ref, ref + c->pages, ref + 2 * (int64_t)c->pages, c->slots, c->max_pages, c->pages,
-                   c->page};
+              c->page};
 }
 
 }  // namespace pic

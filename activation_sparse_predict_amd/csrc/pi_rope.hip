@@ -61,8 +61,8 @@ pi_status launch(bool paged, int dtype, const pi_rope* r, const pir::Part& q, co
   const pir::Turn turn{r ? r->steps : nullptr, rotary, !r || r->magnitude == 0.f ? 1.f : r->magnitude};
   (void)hipGetLastError();
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)up_div((int64_t)tokens * waves, 4)), dim3(256), 0, static_cast<hipStream_t>(stream), turn, q, k, v,
-                       pos, m, cu, seqs, n, tokens, dim, eps, shift, (uint32_t)waves);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)up_div((int64_t)tokens * waves, 4)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), turn, q, k, v, pos, m, cu, seqs, n, tokens, dim, eps, shift, (uint32_t)waves);
   };
   auto with_its = [&](auto t, auto m, auto p) {
     using T = decltype(t);

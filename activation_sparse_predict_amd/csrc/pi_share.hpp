@@ -30,6 +30,19 @@ PI_BOTH int place_of(int key, int page, int max_pages) {
   return p < max_pages ? p : max_pages - 1;
 }
 
+// The page of a place of 16 keys by a multiplication, `per` places a page (1 .. 256): ceil(2^(31 + shift) / per) is off by
+// less than 1, and with 2^shift <= per < 2^(shift + 1) that changes no quotient of a place below 2^30.
+struct Divide {
+  uint32_t mul, shift;
+};
+PI_BOTH Divide divide_by(uint32_t per) {
+  Divide d{0, 0};
+  while (per >> (d.shift + 1)) ++d.shift;
+  d.mul = (uint32_t)(((uint64_t(1) << (31 + d.shift)) + per - 1) / per);
+  return d;
+}
+PI_BOTH int divided(uint32_t place, Divide d) { return (int)((uint32_t)((uint64_t)(2 * place) * d.mul >> 32) >> d.shift); }
+
 // Pieces of `size` keys; near the largest length the sum would not fit an int.
 PI_BOTH int pieces(int keys, int size) { return (int)(((uint32_t)keys + size - 1) / size); }
 
