@@ -268,10 +268,12 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
         }
       }
       if (d.turns || weight) {                     // all else is moved bit by bit
+        // (a lane may hold pairs of both kinds, and a NaN that is widened and packed again need not keep its bits)
+        const int packed = MODE == PAIRS && !weight ? turn.rotary / 2 - 8 * l : 8;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          ya[e] = T::pack(x[2 * e], x[2 * e + 1]);
-          yb[e] = T::pack(x[8 + 2 * e], x[8 + 2 * e + 1]);
+          if (MODE != PAIRS || e < packed) ya[e] = T::pack(x[2 * e], x[2 * e + 1]);
+          if (MODE != PAIRS || 4 + e < packed) yb[e] = T::pack(x[8 + 2 * e], x[8 + 2 * e + 1]);
         }
       }
     }
