@@ -225,9 +225,17 @@ template <class T, int D> __device__ __forceinline__ bool wild(const char* tile)
   return __syncthreads_or(top[0] >= T::INF || top[1] >= T::INF) != 0;
 }
 
-// 0 times an infinity or NaN of a value that a row does not see is NaN.  So where a tile that not all of a block's rows see
-// whole holds such values, they count as zeros (`tame`) and are added at the end to the results of the rows that see them
-// (`add_wild`): a weight times an infinity is that infinity, times NaN is NaN.
+// 0 times an infinity or NaN is NaN, for a value that a row does not see as for one whose key has no weight.  So where a tile
+// that not all of a block's rows see whole holds such values, they count as zeros there (`tame`); and where there were any, or
+// a sum came out not finite, the elements that see such values get at the end what these make of them, whatever the keys'
+// weights are (`add_wild`): that hangs on no tile, share or order.  Infinities of one sign give that infinity, else NaN.
+enum { WILD_UP = 1, WILD_DOWN = 2, WILD_NAN = 4 };
+template <class T> __device__ __forceinline__ int kind_of(uint32_t x) {          // of a value's 16 bits
+  return (x & 0x7fffu) < T::INF ? 0 : (x & 0x7fffu) > T::INF ? WILD_NAN : x & 0x8000u ? WILD_DOWN : WILD_UP;
+}
+__device__ __forceinline__ float value_of(int kinds) {
+  return kinds == WILD_UP ? -NEG_INF : kinds == WILD_DOWN ? NEG_INF : __builtin_nanf("");
+}
 template <class T> __device__ __forceinline__ uint32_t finite(uint32_t x) {      // a mask of the halves that are
   return ((x & 0x7fffu) >= T::INF ? 0u : 0xffffu) | ((x >> 16 & 0x7fffu) >= T::INF ? 0u : 0xffff0000u);
 }
@@ -296,36 +304,57 @@ __device__ __forceinline__ bool at_edge(const Task& k, int tile) {
   return PT_K * tile + PT_K - 1 > k.before + k.t0 || (k.window > 0 && PT_K * tile <= k.before + k.t1 - k.window);
 }
 
-// What `tame` took from the rows' sums, for all threads of a block after the sums were written.
+// Elements that see values which are not finite, for all threads of a block after the sums were written.  A row's total
+// weight is in `total`: where it is NaN, a score was, and so is the row.  `kinds`: room for `dim` numbers.
 template <class T>
 __device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, const Task& k, uint16_t* out,
-                                         int64_t out_token, int64_t out_head, float* part) {
-  __syncthreads();
-  const int group = ch.heads / ch.kv_heads, dim = ch.dim;
+                                         int64_t out_token, int64_t out_head, float* part, const float* total, int* kinds) {
+  const int group = ch.heads / ch.kv_heads, dim = ch.dim, nchunk = dim / 8;
   const int64_t sums = ((int64_t)k.slot * ch.kv_heads + k.g) * ch.rows;
+  auto value_at = [&](int key) -> const uint16_t* {        // NULL in a broken page
+    const int id = usable_page(pg.table[k.table + page_of(ch, key / 16)], pg.pages);
+    return id < 0 ? nullptr : pg.v + (((int64_t)id * ch.kv_heads + k.g) * pg.page + key % pg.page) * dim;
+  };
+  for (int d = threadIdx.x; d < dim; d += blockDim.x) kinds[d] = 0;
+  __syncthreads();
+  // of tiles that all rows see
+  const int at_once = blockDim.x / nchunk, c = threadIdx.x % nchunk, mine = threadIdx.x / nchunk;
+  if (mine < at_once) {
+#pragma unroll 1
+    for (int j = k.first; j <= k.last; ++j) {
+      if (at_edge(k, j)) continue;
+#pragma unroll 1
+      for (int key = PT_K * j + mine; key < PT_K * j + PT_K; key += at_once) {
+        const uint16_t* v = value_at(key);
+        if (!v) continue;
+        const u4 x = *reinterpret_cast<const u4*>(v + 8 * c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int kind = kind_of<T>(x[e / 2] >> 16 * (e % 2));
+          if (kind) atomicOr(&kinds[8 * c + e], kind);
+        }
+      }
+    }
+  }
+  __syncthreads();
 #pragma unroll 1
   for (int e = threadIdx.x; e < k.rows * dim; e += blockDim.x) {
-    const int row = k.row0 + e / dim, d = e % dim, place = k.before + row / group;
+    const int x = e / dim, row = k.row0 + x, d = e % dim, place = k.before + row / group;
     const int lo = k.window > 0 ? max(k.from, place + 1 - k.window) : k.from;
-    float more = 0.f;
+    int all = kinds[d];
 #pragma unroll 1
     for (int j = k.first; j <= k.last; ++j) {
       if (!at_edge(k, j)) continue;
 #pragma unroll 1
       for (int key = max(PT_K * j, lo); key < min(PT_K * j + PT_K, place + 1); ++key) {
-        const int id = usable_page(pg.table[k.table + page_of(ch, key / 16)], pg.pages);
-        if (id < 0) continue;
-        const uint32_t v = pg.v[(((int64_t)id * ch.kv_heads + k.g) * pg.page + key % pg.page) * dim + d];
-        if ((v & 0x7fffu) >= T::INF) more += T::low(v);
+        const uint16_t* v = value_at(key);
+        if (v) all |= kind_of<T>(v[d]);
       }
     }
-    if (more == 0.f) continue;
-    if (k.shares > 1) {
-      part[(sums + row - k.row0) * dim + d] += more;
-    } else {
-      uint16_t* y = out + (k.token + row / group) * out_token + (k.g * group + row % group) * out_head + d;
-      *y = (uint16_t)T::pack(T::low(*y) + more, 0.f);
-    }
+    if (all == 0) continue;
+    const float value = total[x] == total[x] ? value_of(all) : total[x];
+    if (k.shares > 1) part[(sums + x) * dim + d] = value;
+    else out[(k.token + row / group) * out_token + (k.g * group + row % group) * out_head + d] = (uint16_t)T::pack(value, 0.f);
   }
 }
 
@@ -340,7 +369,8 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
             Joint* __restrict__ joints, int32_t* __restrict__ count, float* __restrict__ part, float* __restrict__ stat) {
   using V = Vec<D>;
   constexpr int NF = V::W * V::G, ROW = 16 * NF + 4;
-  __shared__ __attribute__((aligned(16))) float so[4 * 16 * ROW], sm[4 * 16 * 2];
+  __shared__ __attribute__((aligned(16))) float so[4 * 16 * ROW], sm[4 * 16 * 2], total[16 * MT];
+  __shared__ int odds[4];
   const Task k = find_task(pg, ch, sc.window, joints, count);
   if (k.rows == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -510,10 +540,19 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
   // join the waves, 16 rows at a time: o[m][f][i] belongs to dim (16 gr + 4 kg + i) W + f % W of row 16 m + r
   // of wave w's in so [4][16][ROW], (reference point, l) in sm [4][16][2]
   const int64_t sums = ((int64_t)k.slot * ch.kv_heads + k.g) * ch.rows;
+  float bad = 0.f;                                 // NaN where a sum is not finite
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bad = fmaf(o[m][f][i], 0.f, bad);
+  const bool any = __ballot(odd || bad != bad) != 0;
+  if (lane == 0) odds[w] = any;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     if (16 * m >= k.rows) break;
-    __syncthreads();
+    if (m > 0) __syncthreads();
     const float ll = sum16(l[m]);
     if (lane < 16) *reinterpret_cast<float2*>(sm + (16 * w + r) * 2) = float2{mc[m], ll};
 #pragma unroll
@@ -538,6 +577,7 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
         oo = fmaf(so[(16 * i + x) * ROW + d], a, oo);
         od = fmaf(so[(16 * i + x) * ROW + d + 1], a, od);
       }
+      if (d == 0) total[16 * m + x] = tl;
       if (k.shares == 1) {
         const float inv = tl == 0.f ? 0.f : 1.f / tl;   // a row that sees no key is zero
         const int row = k.row0 + 16 * m + x;
@@ -549,7 +589,9 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
       }
     }
   }
-  if (k.t0 != k.t1 && __syncthreads_or(odd)) add_wild<T>(pg, ch, k, out, out_token, out_head, part);
+  if (!(odds[0] | odds[1] | odds[2] | odds[3])) return;
+  __syncthreads();
+  add_wild<T>(pg, ch, k, out, out_token, out_head, part, total, reinterpret_cast<int*>(so));
 }
 
 // One block: 128 rows of a key head, 32 for each wave, over one share of the keys that any of them sees, in tiles of 64 from
@@ -573,6 +615,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
   using R = Ring<D, S, NT>;
   constexpr int SUMS = D <= 64 ? 4 * 32 * 68 * 4 : 0;   // sums on their way out, which take more than small tiles do
   __shared__ float2 stats[KW > 1 ? NT / 2 : 1];
+  __shared__ int odds[4];
   // K tiles, then V tiles
   __shared__ __attribute__((aligned(1024))) char ring[2 * S * R::BYTES > SUMS ? 2 * S * R::BYTES : SUMS];
 
@@ -701,7 +744,7 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     const int k0 = PT_K * j;
     char *sk = ring + j % S * R::BYTES, *sv = sk + S * R::BYTES;
     const int below = place + 1 - k0, above = task.window > 0 ? below - task.window : 0;
-    if (t0 != t1 && at_edge(task, j) && wild<T, D>(sv)) {
+    if (t0 != t1 && at_edge(task, j) && __builtin_expect(wild<T, D>(sv), 0)) {
       tame<T, D>(sv);
       odd = true;
     }
@@ -737,6 +780,16 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     }
     bits = 15;
   }
+  auto mark = [&] {                                // whether the wave's sums hold what is not finite
+    float bad = 0.f;
+#pragma unroll
+    for (int d = 0; d < L::DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) bad = fmaf(sum.o[d][i], 0.f, bad);
+    const bool any = __ballot(bad != bad) != 0;
+    if (lane == 0) odds[w % 4] = any;
+  };
+  if constexpr (KW == 1) mark();
   arrive<0>();
   if constexpr (KW > 1) {                          // the second half's sums go through LDS, lane by lane
     f4* theirs = reinterpret_cast<f4*>(ring) + (w % 4) * 64 * 4 * L::DT + lane;
@@ -762,6 +815,8 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum.o[d][4 * i + e] = fmaf(y[e], b, sum.o[d][4 * i + e] * a);
         }
+      mark();
+      stats[tid].y = sum32(sum.l);
     }
     __syncthreads();
   }
@@ -794,7 +849,16 @@ k_attn_chunk(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, in
     const float l = sum32(sum.l);
     if (hi == 0 && lane < left) *reinterpret_cast<float2*>(stat + 2 * (sums + lane)) = float2{sum.mc, l};
   }
-  if (odd) add_wild<T>(pg, ch, task, out, out_token, out_head, part);
+  if (__builtin_expect(!(odd || (odds[0] | odds[1] | odds[2] | odds[3])), 1)) return;
+  __syncthreads();
+  float* total = reinterpret_cast<float*>(ring);
+  if constexpr (KW > 1) {                          // (from there, not from a register: fewer are spilled in the loop)
+    if (tid < CH_ROWS) total[tid] = stats[64 * (tid / 32) + tid % 32].y;
+  } else {
+    const float l = sum32(sum.l);
+    if (hi == 0) total[32 * w + lane] = l;
+  }
+  add_wild<T>(pg, ch, task, out, out_token, out_head, part, total, reinterpret_cast<int*>(total + CH_ROWS));
 }
 
 // Join the shares of a row: a wave each, N lanes (of 4 dims each) for a share, 64 / N shares at once, eight loads on their way.
@@ -830,7 +894,7 @@ k_chunk_join(const Joint* __restrict__ joints, const int32_t* __restrict__ count
     for (int z = 32; z; z >>= 1) mm = fmaxf(mm, __shfl_xor(mm, z));
     const float base = mm == NEG_INF ? 0.f : mm;
     const float weight = exp2_fast(st.x - base), total = add64(st.y * weight);
-    const float inv = total == 0.f ? 0.f : 1.f / total;  // a row that sees no key is zero
+    const float inv = total == 0.f ? 1.f : 1.f / total;  // sums of a row that sees no key are zero
     f4 sum = (f4)(0.f);
     for (int i0 = 0; i0 < jt.shares; i0 += AT_ONCE * AHEAD) {
       if (i0) {
@@ -843,7 +907,7 @@ k_chunk_join(const Joint* __restrict__ joints, const int32_t* __restrict__ count
         const float a = __shfl(weight, min(k, 63));
         if (k < jt.shares) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = fmaf(y[i][e], a, sum[e]);
+          for (int e = 0; e < 4; ++e) sum[e] = fmaf(y[i][e], fabsf(y[i][e]) < -NEG_INF ? a : 1.f, sum[e]);
         }
       }
     }

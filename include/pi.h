@@ -424,7 +424,9 @@ pi_status pi_cache_append_rope(const pi_cache* cache, int32_t layer, const pi_ro
  *   out = sum_j p_j v_j,  p = softmax(x)
  * A chunk may be one token, a whole prompt or anything between, and a batch any mix
  * of them; a slot may come more than once.  Keys a row does not see leave no trace
- * in it.  A row that sees no key (a slot that cannot be, PI_CACHE_ESLOT, a slot that
+ * in it.  An infinite value reaches every row that sees its key, however small the
+ * key's weight is (nought too, where the score is -inf or far below others): infinities
+ * of one sign give that infinity, of both, as a NaN does, NaN.  A row that sees no key (a slot that cannot be, PI_CACHE_ESLOT, a slot that
  * holds fewer than c tokens, PI_CACHE_ELENGTH) is zero; keys of a broken page
  * (PI_CACHE_EPAGE) are not seen.  Rows that no sequence holds are not written.
  * cu as in pi_attn_prompt; n <= 4096.  A capped score is off by at most 2^-21 cap
