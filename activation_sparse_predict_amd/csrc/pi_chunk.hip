@@ -34,15 +34,6 @@ Cut cut_of(const pi_cache* c, int tokens, int heads, int few) {
   return u;
 }
 
-// Which kernel takes a call: that for few rows where the chunks' rows of a key head are up to 32 on the average.  A chunk that
-// has more of them, or fewer, comes out the same: only its time hangs on this.  (16 chunks behind up to 4000 tokens, 64 heads
-// on 8, 128 wide: 40 rows a chunk 65 us with a k_chunk_few of 48 rows a block, 69 with one of 32, 48 with k_attn_chunk; one row
-// a chunk of 32 heads, 8 chunks behind up to 2900: 52 us with k_chunk_few, 68 with k_attn_chunk.)
-int few_of(const pi_cache* c, int tokens, int heads, int n) {
-  const int64_t rows = up_div(tokens, std::max(1, std::min(n, tokens))) * (heads / c->kv_heads);
-  return rows > 32 ? 0 : (int)up_div(rows, 16);
-}
-
 struct Ws {
   size_t joints, part, stat, total;
 };
@@ -100,7 +91,7 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   if (tokens == 0) return PI_OK;
   if (!ws || ws_bytes < ws_bytes_of(cache, tokens, heads) || !on(ws, kWsAlign)) return PI_EWORKSPACE;
   if (folded(out, tokens, heads, cache->dim)) return PI_EINVAL;
-  const Cut u = cut_of(cache, tokens, heads, few_of(cache, tokens, heads, n));
+  const Cut u = cut_of(cache, tokens, heads, pish::few_tiles(tokens, n, heads / cache->kv_heads));
   const Ws W = ws_of(cache, u);
   const int64_t most = std::min(n, tokens);        // a tile of each chunk may be short
   const int64_t tiles = up_div((int64_t)tokens * (heads / cache->kv_heads), u.tile) + most;

@@ -43,6 +43,23 @@ PI_BOTH Divide divide_by(uint32_t per) {
 }
 PI_BOTH int divided(uint32_t place, Divide d) { return (int)((uint32_t)((uint64_t)(2 * place) * d.mul >> 32) >> d.shift); }
 
+// Which kernel takes a call with chunks of `tokens` tokens in all, `group` rows (heads of a key head) a token: that for few
+// rows, 16 or 32 a block (1, 2), or that of 128 rows a block (0).  A chunk comes out the same on either; only its time hangs on
+// this.  The host knows no chunk's own length, so the first takes calls with up to 32 rows a chunk on the average, whose longest
+// chunk has 256 at most: all tokens but one for each other chunk, or all of them where some chunks must be empty.  It reads a
+// longer one's keys for every 32 rows.  Few rows first, in us:
+//   one token behind 1500, 32 heads 14.5 and 16.7, 16 heads on 8, 256 wide, 14.6 and 22.1; 8 tokens of 40 heads on 8, 80 wide,
+//   behind up to 1500 13.1 and 17.5; 8 times 4 tokens of 16 heads on 8, 256 wide, behind up to 4000 47 and 58
+//   31 single tokens behind up to 4000 and 512 behind 32768, 32 heads, 796 and 466; 63 and 512 1547 and 606; 31 and 64 of 32
+//   heads on 8 205 and 112
+// What the limit costs where chunks are alike: 32 times 8 tokens of 16 heads on 8, 256 wide, behind up to 4000 160 and 181.
+PI_BOTH int few_tiles(int tokens, int n, int group) {
+  const int chunks = n < 1 ? 1 : n < tokens ? n : tokens < 1 ? 1 : tokens;
+  const int64_t mean = (int64_t)((tokens + chunks - 1) / chunks) * group;
+  const int64_t most = (int64_t)(n > tokens ? tokens : tokens - chunks + 1) * group;
+  return mean > 32 || most > 256 ? 0 : mean > 16 ? 2 : 1;
+}
+
 // Pieces of `size` keys; near the largest length the sum would not fit an int.
 PI_BOTH int pieces(int keys, int size) { return (int)(((uint32_t)keys + size - 1) / size); }
 
