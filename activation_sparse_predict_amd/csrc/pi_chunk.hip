@@ -25,8 +25,9 @@ Cut cut_of(const pi_cache* c, int tokens, int heads, int few) {
   u.few = few;
   u.tile = few ? 16 * few : pia::CH_ROWS;
   // Blocks that run at once: two, three or (wide heads) one for each compute unit.  (256, 512, 768 and 1024 blocks: one token
-  // behind 1500, 32 heads, 14.6, 16.4, 16.3, 20.1 us; 5 drafts of 16 sequences -, 49, 59, 58; capped, heads of 256, 174, 200,
-  // 198, 208.)
+  // behind 1500, 32 heads, 14.2, 14.4, 14.3, 15.7 us; 8 single tokens with a bias behind up to 2900 57, 50, 52, 50; 32 single
+  // tokens of 64 heads on 8 behind up to 4000 67, 58, 58, 65; 16 sequences of 5 drafts 55, 49, 58, 57; 512 tokens behind 32768
+  // 346, 288, 298, 291; capped, heads of 256, 114, 139, 144, 157.)
   const int blocks = c->dim > 128 ? 256 : few == 1 || c->dim <= 64 ? 768 : 512;
   u.free = (int)up_div(blocks, c->kv_heads);
   u.slots = 2 * u.free;
