@@ -59,9 +59,12 @@ pi_status launch(bool paged, int dtype, const pi_rope* r, const pir::Part& q, co
   const int waves = (int)up_div(turns, its);                    // of a token
   if ((int64_t)tokens * waves > INT32_MAX) return PI_EUNSUPPORTED;
   const pir::Turn turn{r ? r->steps : nullptr, rotary, !r || r->magnitude == 0.f ? 1.f : r->magnitude};
+  // a launch counts the threads of a dimension in 32 bits, and what is more is cut off without an error
+  const int64_t blocks = up_div((int64_t)tokens * waves, 4);
+  const unsigned across = (unsigned)std::min<int64_t>(blocks, 1 << 23);
   (void)hipGetLastError();
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)up_div((int64_t)tokens * waves, 4)), dim3(256), 0,
+    hipLaunchKernelGGL(kernel, dim3(across, (unsigned)up_div(blocks, across)), dim3(256), 0,
                        static_cast<hipStream_t>(stream), turn, q, k, v, pos, m, cu, seqs, n, tokens, dim, eps, shift, (uint32_t)waves);
   };
   auto with_its = [&](auto t, auto m, auto p) {

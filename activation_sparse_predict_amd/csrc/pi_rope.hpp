@@ -123,9 +123,9 @@ k_rope(Turn turn, Part q, Part k, Part v, const int32_t* __restrict__ pos, pic::
        const int32_t* __restrict__ cu, const int32_t* __restrict__ seqs, int n, int tokens, int dim, float eps, int shift,
        uint32_t waves) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t job = blockIdx.x * 4 + w;         // neighbouring waves take neighbouring heads
+  const uint32_t job = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + w;   // neighbouring waves take neighbouring heads
   const int t = (int)(job / waves), part = (int)(job % waves);
-  if (t >= tokens) return;
+  if (job / waves >= (uint32_t)tokens) return;
   const int l = lane & ((1 << shift) - 1), mine = lane >> shift, per = 64 >> shift;
   const Dims d = dims_of<MODE>(l, dim, turn.rotary);
   const int q_turns = (q.heads + per - 1) / per, k_turns = (k.heads + per - 1) / per;
