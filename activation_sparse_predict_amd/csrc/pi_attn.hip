@@ -87,7 +87,7 @@ pi_status pi_attn_prompt(const pi_heads* q, const pi_heads* k, const pi_heads* v
   const int hg = group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1, rows = 128 / hg;
   // a tile of each sequence may be short
   const int64_t blocks = (up_div(tokens, rows) + std::min(n, tokens)) * (heads / hg);
-  if (blocks > INT32_MAX) return PI_EUNSUPPORTED;
+  if (!launches(blocks, 256)) return PI_EUNSUPPORTED;
   if (folded(out, tokens, heads, dim)) return PI_EINVAL;
   (void)hipGetLastError();
   with_type(dtype, dim, [&](auto t, auto d) {

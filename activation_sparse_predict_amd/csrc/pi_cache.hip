@@ -96,7 +96,7 @@ pi_status pi_cache_append(const pi_cache* c, int32_t layer, const pi_heads* k, c
   if ((s = check_heads(k, tokens)) != PI_OK || (s = check_heads(v, tokens)) != PI_OK) return s;
   if (tokens == 0) return PI_OK;
   const int64_t threads = (int64_t)tokens * c->kv_heads * (c->dim / 8);
-  if (up_div(threads, 256) > INT32_MAX) return PI_EUNSUPPORTED;
+  if (!launches(up_div(threads, 256), 256)) return PI_EUNSUPPORTED;
   const int64_t at = (int64_t)layer * c->pages * c->kv_heads * c->page * c->dim;
   (void)hipGetLastError();
   hipLaunchKernelGGL(pic::k_cache_append, dim3((unsigned)up_div(threads, 256)), dim3(256), 0,

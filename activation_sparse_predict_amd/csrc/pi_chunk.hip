@@ -96,6 +96,8 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   const Ws W = ws_of(cache, u);
   const int64_t most = std::min(n, tokens);        // a tile of each chunk may be short
   const int64_t tiles = up_div((int64_t)tokens * (heads / cache->kv_heads), u.tile) + most;
+  const int64_t blocks = (tiles + u.free) * cache->kv_heads;
+  if (!launches(blocks, 64 * (u.few || cache->dim <= 128 ? 4 : 8))) return PI_EUNSUPPORTED;
   char* base = static_cast<char*>(ws);
   auto floats = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
   pia::ChunkCall call{};
@@ -109,7 +111,7 @@ pi_status pi_attn_chunk(const pi_cache* cache, int32_t layer, const pi_heads* q,
   call.part = floats(W.part), call.stat = floats(W.stat);
   call.mod = (cap > 0.f ? pia::CH_CAP : 0) | (slopes ? pia::CH_SLOPES : 0);
   call.few = u.few;
-  call.blocks = (unsigned)((tiles + u.free) * cache->kv_heads);
+  call.blocks = (unsigned)blocks;
   call.stream = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   if (u.few) {

@@ -18,6 +18,10 @@ inline int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // PI_OK, or PI_EHIP with the error kept for pi_last_hip_error (defined in pi_ffn.hip).
 pi_status launched();
 
+// Whether a launch in one dimension holds so many blocks: its threads are counted in 32 bits, and what is more is cut off
+// without an error.
+inline bool launches(int64_t blocks, int threads) { return blocks <= UINT32_MAX / threads; }
+
 // Shape limits of a cache (pointers, sizes, alignment); see pi_cache in pi.h.
 pi_status check_cache(const pi_cache* c);
 // Alignment of a [tokens][heads][dim] tensor; see pi_heads in pi.h.

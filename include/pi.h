@@ -231,6 +231,8 @@ pi_status pi_ffn_stack_static(const pi_layer* layers, int32_t n_layers, const fl
  *  - heads % kv_heads == 0; query head h reads key head h / (heads / kv_heads).
  *  - An output lies over no input, but pi_attn_prompt's, pi_attn_decode's and
  *    pi_attn_chunk's may be q itself, with q's strides.
+ *  - A pi_cache_append, pi_attn_prompt or pi_attn_chunk that would take 2^32
+ *    threads or more in one launch is refused (PI_EUNSUPPORTED).
  *  - What only the device knows (lengths, slot and page numbers) is checked
  *    there: nothing outside the tensors is ever read or written for it.  An
  *    accounting call (extend, fork, release) that cannot be carried out whole
