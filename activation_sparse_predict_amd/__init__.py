@@ -85,6 +85,7 @@ class PiRopeScaling(ctypes.Structure):
 
 
 _HEADS = struct.Struct("@Pqq")                         # PiHeads
+_MOST = (1 << 31) - 1                                  # an int32; ctypes would keep the lower bits of what is larger
 
 _LAYOUT = {"half": 0, "pairs": 1}
 _RULE = {None: 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
@@ -474,10 +475,17 @@ def _heads(t, shape, what: str) -> bytes:
     """The pi_heads of a [tokens][heads][dim] tensor with strides, the last dimension contiguous, as the bytes of the
     structure (which take a third of a PiHeads object's time)."""
     token, head, one = t.stride()
-    if one != 1 and shape[2] != 1:
+    if one != 1 and shape[2] != 1 or shape[0] > _MOST:
         raise PiError(PI_EINVAL, what)
     # the stride of a dimension of one element says nothing
     return _HEADS.pack(t.data_ptr(), token if shape[0] > 1 else 0, head if shape[1] > 1 else 0)
+
+
+def _real(x: float, what: str) -> float:
+    """A number that means something else where it is 0, and would be as a float32."""
+    if 0 < x <= 2.0 ** -150:
+        raise PiError(PI_EINVAL, what)
+    return x
 
 
 def _capturing(dev: int, handle: Optional[int] = None) -> bool:
@@ -716,7 +724,7 @@ def attn_prompt(q, k, v, out, cu, scale: float = 0.0, stream=None):
     offsets, what = _ints(cu, None, "attn_prompt: cu"), "attn_prompt: strides"
     dev = _gpu("attn_prompt: tensors of one GPU", cu, q, k, v, out)
     _check(_on(dev, (_lib or lib()).pi_attn_prompt, _heads(q, qs, what), _heads(k, ks, what), _heads(v, ks, what),
-               _heads(out, qs, what), qs[0], qs[1], ks[1], qs[2], _dtype_of(q), offsets, n, scale,
+               _heads(out, qs, what), qs[0], qs[1], ks[1], qs[2], _dtype_of(q), offsets, n, _real(scale, "attn_prompt: scale"),
                _stream_on(dev, stream)), "pi_attn_prompt")
 
 
@@ -740,8 +748,8 @@ def attn_decode(cache: Cache, layer: int, q, out, prefix=None, seqs=None, scale:
         memory, size = ws.data_ptr(), ws.numel() * ws.element_size()
     what = "attn_decode: strides"
     _check(_on(dev, cache._lib.pi_attn_decode, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), batch,
-               heads, _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"), scale,
-               memory, size, on), "pi_attn_decode")
+               heads, _ints(seqs, batch, "attn_decode: seqs"), _ints(prefix, 1, "attn_decode: prefix"),
+               _real(scale, "attn_decode: scale"), memory, size, on), "pi_attn_decode")
 
 
 class Rope:
@@ -826,8 +834,9 @@ def attn_chunk(cache: Cache, layer: int, q, out, cu, seqs=None, scale: float = 0
         memory, size = ws.data_ptr(), ws.numel() * ws.element_size()
     what = "attn_chunk: strides"
     _check(_on(dev, cache._lib.pi_attn_chunk, cache._ref, layer, _heads(q, shape, what), _heads(out, shape, what), tokens, heads,
-               _ints(cu, n + 1, "attn_chunk: cu"), _ints(seqs, n, "attn_chunk: seqs"), n, scale, cap,
-               _floats(slopes, heads, "attn_chunk: slopes"), window, memory, size, on), "pi_attn_chunk")
+               _ints(cu, n + 1, "attn_chunk: cu"), _ints(seqs, n, "attn_chunk: seqs"), n,
+               _real(scale, "attn_chunk: scale"), _real(cap, "attn_chunk: cap"), _floats(slopes, heads, "attn_chunk: slopes"),
+               min(window, _MOST) if window >= 0 else -1, memory, size, on), "pi_attn_chunk")
 
 
 class Q4Matrix:
