@@ -362,7 +362,7 @@ __device__ __forceinline__ void add_wild(const Pages& pg, const Chunks& ch, cons
 // steps of 32 keys in turn, whose keys and values go straight to registers: what a compute unit has on its way from memory
 // bounds these, and its registers hold more than its LDS (192 KB with three blocks of MT 1, 64 KB in two blocks' tiles).
 // 8 sequences of one token behind up to 2900, 32 heads of 128: 40 us, 5.5 TB/s of keys and values; one token behind 1500:
-// 9.9 us, latency: slots and lengths, page numbers, pages, the join of the waves.
+// 10.4 us, latency: slots and lengths, page numbers, pages, the join of the waves.
 template <class T, int D, int MOD, int MT>
 __global__ void __launch_bounds__(4 * WAVE, D > 128 ? 1 : D <= 64 || MT == 1 ? 3 : 2)
 k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int64_t out_head, Chunks ch, ChunkScore sc,
@@ -603,7 +603,9 @@ k_chunk_few(Pages pg, Rows q, uint16_t* __restrict__ out, int64_t out_token, int
 // with page numbers, edges and masks looked at in each tile it was 820 (430 us).  24 chunks, 128 heads on 8, 64 wide: 78 us,
 // vector instructions (the exponentials) and the uneven lengths of blocks: waves wait for 37 % of their time.  Heads 256 wide:
 // 730 TFLOP/s (4096 tokens, 16 heads), products, LDS reads and exponentials of eight waves that keep step follow one another
-// more than they overlap; four waves with 32 more registers of scores took 166 us where eight take 131.  Wave priorities for
+// more than they overlap; four waves with 32 more registers of scores took 166 us where eight take 131.  These spill 22 to 25
+// registers a lane, the offsets `off` among them, and a reload waits for all loads before it: tiles at the edge wait so, and
+// heads of 136 to 248 in every tile (512 tokens behind 8192, 16 heads on 8: 152 us 192 wide, 98 us 256 wide).  Wave priorities for
 // half of them change nothing; a first round without looking for values that are not finite, and a second one where any came
 // out, costs registers (capped 118 -> 128 us).
 template <class T, int D, int MOD>

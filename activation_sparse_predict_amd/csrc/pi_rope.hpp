@@ -22,7 +22,9 @@ using namespace pit;
 //  ODD          other rotary: dims 8 l .. of the first half and of the second, which
 //               starts on no chunk; rows come and go in chunks l and l + P and are
 //               taken apart in LDS (3018 tokens of 64 heads on 8, 128 wide, 62 of them
-//               turned, with norms: 93 us with values loaded and stored one by one, 52 so)
+//               turned, with norms: 93 us with values loaded and stored one by one, 49 so; 22
+//               the bytes take, but lanes that turn and others are counted apart, so of 16
+//               lanes a head half have work)
 enum { NONE = 0, HALF = 1, PAIRS = 2, ODD = 3 };
 
 struct Turn {

@@ -227,7 +227,8 @@ pi_status pi_ffn_stack_static(const pi_layer* layers, int32_t n_layers, const fl
  * top of this file hold, and further:
  *  - Attention and cache tensors are PI_F16 or PI_BF16 (else PI_EUNSUPPORTED),
  *    with 8 <= dim <= 256 and dim % 8 == 0; scores, softmax statistics and
- *    sums are float32.
+ *    sums are float32, and a softmax's weights are rounded to the tensors' type
+ *    for their product with the values.
  *  - heads % kv_heads == 0; query head h reads key head h / (heads / kv_heads).
  *  - An output lies over no input, but pi_attn_prompt's, pi_attn_decode's and
  *    pi_attn_chunk's may be q itself, with q's strides.
